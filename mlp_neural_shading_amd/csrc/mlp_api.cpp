@@ -14,6 +14,7 @@
 
 #include "mlp.h"
 #include "mlp_testing.h"
+#include "mlp_error.h"
 #include "mlp_layered.h"
 #include "mlp_layout.h"
 #include "mlp_pack.h"
@@ -21,9 +22,11 @@
 
 using mlpk::KernelEntry;
 
-namespace {
+namespace mlpk {
 
+namespace {
 thread_local std::string t_error;
+}
 
 int fail(int code, const char *fmt, ...)
 {
@@ -46,6 +49,14 @@ int hip_fail(hipError_t e, const char *what)
 {
     return fail(MLP_ERR_HIP, "%s failed: %s (%d)", what, hipGetErrorString(e), (int)e);
 }
+
+}  // namespace mlpk
+
+using mlpk::fail;
+using mlpk::hip_fail;
+using mlpk::ok;
+
+namespace {
 
 struct State {
     bool packed = false;
@@ -721,7 +732,7 @@ int mlp_debug_read_packed(void *host_dst, size_t bytes)
     return ok();
 }
 
-const char *mlp_last_error(void) { return t_error.c_str(); }
+const char *mlp_last_error(void) { return mlpk::t_error.c_str(); }
 
 void mlp_release(void)
 {
