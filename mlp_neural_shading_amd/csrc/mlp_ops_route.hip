@@ -172,11 +172,410 @@ __global__ __launch_bounds__(64) void route_tokens(RouteArgs r)
     }
 }
 
+// ---- the same, L lanes per token ------------------------------------------------------------------
+//
+// For up to L * VPL experts: lane i of a token's L = 16 or 64 lanes holds the experts VPL i .. VPL i + VPL - 1, so
+// 64 / L tokens share a wave and a group of experts is a run of whole lanes.  The choice runs on FP32 keys first
+// (the logits where they give the order, else score + bias), brought to whole numbers of 31 bits: the key's place
+// between the token's smallest and largest above the expert's index counted down, so that every key differs and
+// equal ones go to the lower index.  The next best key below b is then the largest key - b mod 2^32: one
+// subtraction and half a maximum per expert and pick, against a comparison, a search and a removal.  Where
+// neighbours among the k + 1 best (or two groups' values) lie within the error that a key may have, and are not the
+// same logit and bias, the order is not certain, and the wave chooses once more on keys in 64 bits.  The chosen
+// scores themselves are computed in 64 bits (the softmax's sum in FP32).
+
+constexpr float kLow = -__builtin_huge_valf();
+
+// Reductions over a token's lanes, the result in all of them: rotations within a row of 16 lanes, then swaps of
+// rows and of halves.
+template <int L, class F>
+__device__ __forceinline__ unsigned lanes_reduce(unsigned v, F f)
+{
+    v = f(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, true));  // row_ror 8, 4, 2, 1
+    v = f(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, true));
+    v = f(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, true));
+    v = f(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, true));
+    if constexpr (L == 64) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = f(r[0], r[1]);
+        const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = f(h[0], h[1]);
+    }
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v)
+{
+    return __builtin_bit_cast(float, lanes_reduce<L>(__builtin_bit_cast(unsigned, v), [](unsigned a, unsigned b) {
+                                  return __builtin_bit_cast(unsigned, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+                              }));
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v)
+{
+    return __builtin_bit_cast(float, lanes_reduce<L>(__builtin_bit_cast(unsigned, v), [](unsigned a, unsigned b) {
+                                  return __builtin_bit_cast(unsigned, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+                              }));
+}
+template <int L>
+__device__ __forceinline__ unsigned lanes_max(unsigned v)
+{
+    return lanes_reduce<L>(v, [](unsigned a, unsigned b) { return a > b ? a : b; });
+}
+template <int L>
+__device__ __forceinline__ double lanes_sum(double v)
+{
+#pragma unroll
+    for (int d = L / 2; d; d >>= 1)
+        v += __shfl_xor(v, d);
+    return v;
+}
+
+__device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504088896340736f); }
+
+template <class T, int N>
+struct __attribute__((packed, aligned(2))) Packed {
+    T v[N];
+};
+
+// This lane's VPL logits; -infinity for NaN and past the last expert.
+template <class T, int VPL>
+__device__ __forceinline__ void load_logits(const T *logit, int e0, int experts, float (&x)[VPL])
+{
+    if (e0 + VPL <= experts) {
+        const Packed<T, VPL> p = *(const Packed<T, VPL> *)(logit + e0);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            x[v] = (float)p.v[v];
+    } else {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const float z = (float)logit[e0 + v < experts ? e0 + v : experts - 1];
+            x[v] = e0 + v < experts ? z : kLow;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+        x[v] = fmaxf(x[v], kLow);  // the maximum of a NaN and a number is the number
+}
+
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+// The middle one of first >= second and v.
+__device__ __forceinline__ float middle(float first, float second, float v) { return __builtin_amdgcn_fmed3f(first, second, v); }
+__device__ __forceinline__ double middle(double first, double second, double v) { return fmax(second, fmin(first, v)); }
+
+// exp to 2^-30 of its value: 2^n times the Taylor polynomial of degree 8 on |r| <= ln(2) / 2 (its next
+// term is below 2^-32).
+__device__ __forceinline__ double exp_near(double v)
+{
+    const double n = rint(v * 1.4426950408889634);
+    const double r = fma(n, -0.6931471805599453, v);
+    double q = 1.0 / 40320;
+    q = fma(q, r, 1.0 / 5040);
+    q = fma(q, r, 1.0 / 720);
+    q = fma(q, r, 1.0 / 120);
+    q = fma(q, r, 1.0 / 24);
+    q = fma(q, r, 1.0 / 6);
+    q = fma(q, r, 0.5);
+    q = fma(q, r, 1.0);
+    q = fma(q, r, 1.0);
+    return ldexp(q, (int)n);
+}
+// 1 / v for a normal v: the hardware's estimate and a step of Newton's.
+__device__ __forceinline__ double one_over(double v)
+{
+    const double e = __builtin_amdgcn_rcp(v);
+    return fma(e, fma(-v, e, 1.0), e);
+}
+
+// Masks the keys of the groups that are not among the topk_groups best.  In FP32 (`near`: how far two keys may lie
+// from their true distance, apart from the rounding of a sum; 0 for exact keys) clears `sure` where two groups are too near each other.
+template <class K, int L, int VPL>
+__device__ __forceinline__ void mask_groups(const RouteArgs &r, K (&key)[VPL], K near, bool &sure)
+{
+    const int lane = threadIdx.x & 63, me = lane & (L - 1), row = lane - me;
+    const K none = -__builtin_huge_valf();
+    const int lanes = r.experts / r.groups / VPL;  // of a group: a power of two
+    K first = none, second = none;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+        second = middle(first, second, key[v]);
+        first = larger(first, key[v]);
+    }
+    for (int d = 1; d < lanes; d <<= 1) {
+        const K of = __shfl_xor(first, d), os = __shfl_xor(second, d);
+        const K low = of < first ? of : first, high = os > second ? os : second;
+        first = of > first ? of : first;
+        second = low > high ? low : high;
+    }
+    const K value = r.group_top == 2 && second > none ? first + second : first;
+    int better = 0;  // groups before this one
+    for (int d = lanes; d < L; d += lanes) {
+        const int at = (me + d) & (L - 1);  // a lane of the group d / lanes further
+        const K other = __shfl(value, row + at);
+        better += at < me ? other >= value : other > value;
+    }
+    const bool out = better >= r.topk_groups || !(value > none);
+    if (near > 0) {  // FP32: the worst group taken and the best one left
+        const float taken = -lanes_max<L>(out ? kLow : -(float)value), left = lanes_max<L>(out ? (float)value : kLow);
+        if (left > kLow && !(taken - left > 2 * near + fabsf(taken) * (1.0f / (1 << 22))))
+            sure = false;
+    }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+        key[v] = out ? none : key[v];
+}
+
+// The choice on 64-bit keys: in lane j < k the j-th best expert, -1 where none is left.
+template <class T, int L, int VPL>
+__device__ __forceinline__ int choose_exactly(const RouteArgs &r, const T *logit)
+{
+    const int lane = threadIdx.x & 63, me = lane & (L - 1), e0 = me * VPL;
+    float x[VPL];
+    load_logits<T, VPL>(logit, e0, r.experts, x);
+    double key[VPL], scale = 1.0;
+    if (r.sigmoid) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            key[v] = 1.0 / (1.0 + exp(-(double)x[v]));
+    } else {
+        float top = kLow;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            top = fmaxf(top, x[v]);
+        top = lanes_max<L>(top);
+        double sum = 0.0;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const double e = exp((double)x[v] - (double)top);
+            key[v] = !(x[v] > kLow) ? 0.0 : x[v] == top ? 1.0 : e;  // of infinities too
+            sum += key[v];
+        }
+        scale = 1.0 / lanes_sum<L>(sum);
+    }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+        key[v] = key[v] * scale + (r.bias ? (double)r.bias[e0 + v < r.experts ? e0 + v : r.experts - 1] : 0.0);
+        key[v] = x[v] > kLow && key[v] > kNone ? key[v] : kNone;
+    }
+    bool unused;
+    if (r.topk_groups < r.groups)
+        mask_groups<double, L, VPL>(r, key, 0.0, unused);
+    int index = -1;
+    for (int j = 0; j < r.k; ++j) {
+        double best = kNone;
+        int at = r.experts;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            if (key[v] > best) {
+                best = key[v];
+                at = e0 + v;
+            }
+#pragma unroll
+        for (int d = L / 2; d; d >>= 1) {
+            const double ov = __shfl_xor(best, d);
+            const int oi = __shfl_xor(at, d);
+            if (ov > best || (ov == best && oi < at)) {
+                best = ov;
+                at = oi;
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            key[v] = e0 + v == at ? kNone : key[v];
+        if (me == j && best > kNone)
+            index = at;
+    }
+    return index;
+}
+
+template <class T, int L, int VPL>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void route_lanes(RouteArgs r)
+{
+    const int lane = threadIdx.x & 63, me = lane & (L - 1), e0 = me * VPL;
+    constexpr unsigned kIndex = L * VPL - 1;             // the bits of the index
+    // Places for the keys, as many as FP32 counts and 31 bits hold; 0 for masked ones.
+    constexpr unsigned kPlaces = L * VPL <= 256 ? 1u << 23 : 1u << 22;
+    static_assert((uint64_t)kPlaces * (L * VPL) <= 1u << 31, "31 bits");
+    // Without a bias, and without a sum of two scores, the logits give the order: a score rises with its logit.
+    const bool by_logit = !r.bias && (r.topk_groups == r.groups || r.group_top == 1);
+    float bias[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+        bias[v] = 0.0f;
+    if (r.bias && e0 + VPL <= r.experts) {
+        struct __attribute__((packed, aligned(4))) Floats {
+            float v[VPL];
+        };
+        const Floats f = *(const Floats *)(r.bias + e0);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            bias[v] = f.v[v];
+    } else if (r.bias) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            bias[v] = r.bias[e0 + v < r.experts ? e0 + v : r.experts - 1];
+    }
+    // One round of tokens per wave: in a loop over rounds, the compiler moves the constants of the 64-bit exp before
+    // it, and the common path spills.
+    const int64_t t = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * (64 / L) + lane / L;
+    const bool live = t < r.tokens;
+    const T *logit = (const T *)r.logits + (live ? t : r.tokens - 1) * r.ld;
+    float key[VPL];
+    load_logits<T, VPL>(logit, e0, r.experts, key);
+    float top = kLow, total = 0.0f;  // softmax: largest logit, sum of exp(logit - top)
+    float near = 0.0f;
+    if (r.sigmoid) {
+        if (!by_logit) {
+            // A score is off by less than 2^-22: its argument's rounding through a slope of |x| s (1 - s) < 0.23,
+            // exp and the reciprocal.
+            near = 1.0f / (1 << 20);
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) {
+                const float s = __builtin_amdgcn_rcpf(1.0f + exp_of(-key[v])) + bias[v];
+                key[v] = fmaxf(key[v] > kLow ? s : kLow, kLow);  // a NaN is masked
+            }
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            top = fmaxf(top, key[v]);
+        top = lanes_max<L>(top);
+        const bool infinite = top == __builtin_huge_valf();  // the others' scores are then exactly 0
+        if (!by_logit || !r.renormalise || infinite) {
+            float e[VPL];
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) {
+                const float ev = exp_of(key[v] - top);
+                e[v] = key[v] == top ? 1.0f : ev;
+                total += key[v] > kLow ? e[v] : 0.0f;
+            }
+            total = lanes_sum<L>(total);
+            if (!by_logit) {
+                // off by less than 2^-18 of the largest score: exp, and 16 + 6 additions in the sum
+                const float scale = __builtin_amdgcn_rcpf(total);
+                near = scale * (1.0f / (1 << 17));
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) {
+                    const float s = e[v] * scale + bias[v];
+                    key[v] = fmaxf(key[v] > kLow ? s : kLow, kLow);  // a NaN is masked
+                }
+            } else if (infinite) {
+#pragma unroll
+                for (int v = 0; v < VPL; ++v)
+                    key[v] = key[v] > kLow ? e[v] : kLow;
+            }
+        }
+    }
+    bool sure = true;
+    if (r.topk_groups < r.groups)
+        mask_groups<float, L, VPL>(r, key, near, sure);
+
+    float high = kLow, low = -kLow;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+        high = fmaxf(high, key[v]);
+        low = fminf(low, key[v] > kLow ? key[v] : -kLow);
+    }
+    high = lanes_max<L>(high);
+    low = fmaxf(-lanes_max<L>(-low), high - 64.0f);  // what lies further off shares the last place
+    const float step = high > low ? (float)(kPlaces - 4) / (high - low) : 0.0f;  // infinite keys: 0 or not sure
+    if (!(high - low < -kLow) && high > kLow)
+        sure = false;
+    unsigned place[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+        const unsigned q = (unsigned)(fmaxf(key[v] - low, 0.0f) * step + 1.0f);
+        place[v] = key[v] > kLow ? (q * (L * VPL)) + (kIndex - (unsigned)(e0 + v)) : 0u;
+    }
+    unsigned best = 0x80000000u, mine = 0u, next = 0u;
+    for (int j = 0; j <= r.k; ++j) {
+        unsigned below = place[0] - best;
+#pragma unroll
+        for (int v = 1; v < VPL; ++v)
+            below = max(below, place[v] - best);
+        below = lanes_max<L>(below);
+        best = best ? best + below : 0u;  // 0: none is left
+        mine = me == j ? best : mine;
+        next = me == j - 1 ? best : next;
+    }
+    int index = mine ? (int)(kIndex - (mine & kIndex)) : -1;
+    if (mine && next && me < r.k) {
+        // places are off by 1 each, and by what the keys are off
+        const float apart = (float)(mine / (L * VPL) - next / (L * VPL));
+        if (!(apart > 3.0f + step * (near + fmaxf(fabsf(high), fabsf(low)) * (1.0f / (1 << 22))))) {
+            const int after = (int)(kIndex - (next & kIndex));
+            sure = sure && logit[index] == logit[after] && (!r.bias || r.bias[index] == r.bias[after]);
+        }
+    }
+    if (me >= r.k)
+        index = -1;
+    if (__any(!sure))
+        index = choose_exactly<T, L, VPL>(r, logit);
+
+    // The chosen scores, in lane j the j-th.
+    double score = 0.0;
+    if (index >= 0) {
+        const double z = (double)(float)logit[index];
+        if (r.sigmoid) {
+            const double e = exp_near(fmax(-fabs(z), -800.0));  // 0 from there on
+            score = (z < 0.0 ? e : 1.0) * one_over(1.0 + e);
+        } else {
+            score = (float)z == top ? 1.0 : exp_near(fmax(z - (double)top, -800.0));
+        }
+    }
+    const double part = r.renormalise ? lanes_sum<L>(score) : r.sigmoid ? 1.0 : (double)total;
+    if (live && me < r.k) {
+        r.index[t * r.k + me] = index;
+        const double w = part > 1e-300 ? score * one_over(part) : part > 0.0 ? score / part : 0.0;
+        r.weight[t * r.k + me] = index >= 0 ? (float)(w * (double)r.scale) : 0.0f;
+    }
+}
+
+// Whether `lanes` lanes of vpl experts each serve this router: room for the experts and for k + 1 picks, and
+// groups of whole lanes, a power of two of them, filling the lanes in use evenly.
+bool lanes_serve(const RouteArgs &r, int lanes, int vpl)
+{
+    if (r.experts > lanes * vpl || r.k >= lanes)
+        return false;
+    if (r.topk_groups == r.groups)
+        return true;
+    const int per = r.experts / r.groups;
+    return r.experts == lanes * vpl && per % vpl == 0 && (per / vpl & (per / vpl - 1)) == 0;
+}
+
+template <class T, int L, int VPL>
+hipError_t launch_lanes(const RouteArgs &r, hipStream_t stream)
+{
+    constexpr int64_t kMost = (int64_t)1 << 25;  // tokens per launch: a grid counts its threads in 32 bits
+    hipError_t err = hipSuccess;
+    for (int64_t t = 0; t < r.tokens && err == hipSuccess; t += kMost) {
+        RouteArgs part = r;
+        part.tokens = r.tokens - t < kMost ? r.tokens - t : kMost;
+        part.logits = (const T *)r.logits + t * r.ld;
+        part.index += t * r.k;
+        part.weight += t * r.k;
+        const int64_t blocks = (part.tokens + 4 * (64 / L) - 1) / (4 * (64 / L));
+        hipLaunchKernelGGL((route_lanes<T, L, VPL>), dim3((unsigned)blocks), dim3(256), 0, stream, part);
+        err = hipGetLastError();
+    }
+    return err;
+}
+
 template <class T>
 hipError_t launch_route_typed(const RouteArgs &r, hipStream_t stream)
 {
     const dim3 grid((unsigned)(r.tokens < 256 * 64 ? r.tokens : 256 * 64));
     const size_t lds = (size_t)(r.experts + r.groups) * sizeof(double);
+    if (lanes_serve(r, 16, 4))
+        return launch_lanes<T, 16, 4>(r, stream);
+    if (lanes_serve(r, 16, 8))
+        return launch_lanes<T, 16, 8>(r, stream);
+    if (lanes_serve(r, 16, 16))
+        return launch_lanes<T, 16, 16>(r, stream);
+    if (lanes_serve(r, 64, 8))
+        return launch_lanes<T, 64, 8>(r, stream);
     const int vpl = (r.experts + 63) / 64;
     if (vpl <= 1)
         hipLaunchKernelGGL((route_tokens<T, 1>), grid, dim3(64), lds, stream, r);
