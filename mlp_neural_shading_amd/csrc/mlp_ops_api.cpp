@@ -210,10 +210,11 @@ int mlp_linear(const mlp_linear_args *a, void *stream)
     p.in = a->in_width;
     p.out = a->out_width;
     p.act = a->act;
+    p.y_fp32 = a->out_dtype == MLP_DTYPE_FP32;
     if (!mlpk::product_fits(p, a->gated, false))
         return fail(MLP_ERR_UNSUPPORTED, "%lld rows of %d outputs are more tiles than one launch holds", (long long)a->rows,
                     a->out_width);
-    const hipError_t err = mlpk::launch_product(p, a->dtype, a->out_dtype, a->gated, false, (hipStream_t)stream);
+    const hipError_t err = mlpk::launch_product(p, a->dtype, a->gated, false, (hipStream_t)stream);
     return err == hipSuccess ? ok() : hip_fail(err, "launching the layer");
 }
 
@@ -368,6 +369,7 @@ int mlp_expert_linear(const mlp_expert_linear_args *a, void *stream)
     p.in = a->in_width;
     p.out = a->out_width;
     p.act = a->act;
+    p.y_fp32 = a->combine || a->out_dtype == MLP_DTYPE_FP32;
     p.offsets = a->offsets;
     p.slots = a->x_slots ? nullptr : a->slots;
     p.experts = a->experts;
@@ -375,8 +377,7 @@ int mlp_expert_linear(const mlp_expert_linear_args *a, void *stream)
     if (!mlpk::product_fits(p, a->gated, true))
         return fail(MLP_ERR_UNSUPPORTED, "%lld slots of %d outputs are more tiles than one launch holds", (long long)n,
                     a->out_width);
-    hipError_t err = mlpk::launch_product(p, a->dtype, a->combine ? (int)MLP_DTYPE_FP32 : a->out_dtype, a->gated, true,
-                                          (hipStream_t)stream);
+    hipError_t err = mlpk::launch_product(p, a->dtype, a->gated, true, (hipStream_t)stream);
     if (err != hipSuccess)
         return hip_fail(err, "launching the experts' layer");
     if (a->combine) {

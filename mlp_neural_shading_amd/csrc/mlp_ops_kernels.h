@@ -22,6 +22,7 @@ struct ProductArgs {
     int64_t rows;  // dense: rows; grouped: slots, in use or not (tokens * k)
     int in, out;   // widths; a gated layer's w has 2 * out rows
     int act;       // MLP_EPI_*
+    int y_fp32;    // 1: y and residual are FP32, 0: of the inputs' type
     // grouped only
     const int32_t *offsets;  // [experts + 1]
     const int32_t *slots;    // the assignment of each slot, or NULL: x is by slot
@@ -30,7 +31,7 @@ struct ProductArgs {
 
 enum { kFp16 = 0, kBf16 = 1, kFp32 = 2 };  // MLP_DTYPE_*
 
-hipError_t launch_product(const ProductArgs &p, int dtype, int out_dtype, bool gated, bool grouped, hipStream_t stream);
+hipError_t launch_product(const ProductArgs &p, int dtype, bool gated, bool grouped, hipStream_t stream);
 // Whether one launch holds the product's tiles.
 bool product_fits(const ProductArgs &p, bool gated, bool grouped);
 

@@ -33,42 +33,69 @@ struct Vec8<__bf16> {
 __device__ __forceinline__ f16x mfma32(h8 a, h8 b, f16x c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f16x mfma32(b8 a, b8 b, f16x c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
 
-// The epilogue's activation, FP32 to FP32.  NaN stays NaN.
-__device__ __forceinline__ float activate(float v, int act)
+__device__ __forceinline__ f4 mfma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f4 mfma16(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+
+// v (1 + erf(v / sqrt 2)) / 2.  erfc(u) = t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) exp(-u^2), t = 1 / (1 + 0.3275911 u),
+// for u >= 0: Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26, off by at most 1.5e-7;
+// written with erfc on the negative side too, so nothing cancels there.
+__device__ __forceinline__ float gelu(float v)
+{
+    const float u = fabsf(v) * 0.70710678118654752440f;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, u, 1.0f));
+    float q = fmaf(t, 1.061405429f, -1.453152027f);
+    q = fmaf(t, q, 1.421413741f);
+    q = fmaf(t, q, -0.284496736f);
+    q = fmaf(t, q, 0.254829592f);
+    const float half_erfc = 0.5f * t * q * __builtin_amdgcn_exp2f(u * u * -1.44269504088896340736f);
+    return v * (v < 0.0f ? half_erfc : 1.0f - half_erfc);
+}
+
+// Calls f with the epilogue's activation (MLP_EPI_*), FP32 to FP32; NaN stays NaN.  The choice is made once for a
+// tile of sums.  (Once for all of a wave's tiles, the compiler merges 128 sums from five branches and spills them.)
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F f)
 {
     switch (act) {
     case 1:
-        return v < 0.0f ? v * kSlope : v;
+        f([](float v) { return v < 0.0f ? v * kSlope : v; });
+        break;
     case 2:
-        return v < 0.0f ? 0.0f : v;
+        f([](float v) { return v < 0.0f ? 0.0f : v; });
+        break;
     case 3:
-        return 0.5f * v * (1.0f + erff(v * 0.70710678118654752440f));
+        f([](float v) { return gelu(v); });
+        break;
     case 4:
-        return v / (1.0f + __expf(-v));
+        f([](float v) { return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896340736f)); });
+        break;
     default:
-        return v;
+        f([](float v) { return v; });
     }
 }
 
-// 16 bytes from an address aligned to an element only (the hardware takes any alignment).
+template <int V>
+struct Number {
+    static constexpr int value = V;
+};
+
+// 16 bytes from an address aligned to an element only: one load, which the hardware takes at any alignment, at
+// full rate where it happens to be aligned.
 struct __attribute__((packed, aligned(2))) Unaligned16 {
     u4 v;
 };
-template <bool A16, class T>
+template <class T>
 __device__ __forceinline__ u4 load16(const T *p)
 {
-    if constexpr (A16)
-        return *(const u4 *)p;
-    else
-        return ((const Unaligned16 *)p)->v;
+    return ((const Unaligned16 *)p)->v;
 }
 
 // The 8 columns from `col` of a row of `width`, zero past its end; reads no byte past it.
-template <bool A16, class T>
+template <class T>
 __device__ __forceinline__ u4 load16_tail(const T *row, int col, int width)
 {
     if (col + 8 <= width)
-        return load16<A16>(row + col);
+        return load16(row + col);
     typename Vec8<T>::type v = (typename Vec8<T>::type)(T)0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -143,96 +170,234 @@ __device__ __forceinline__ int64_t xcd_tile(unsigned b, int64_t n)
     return b / 8 < per && t < n ? t : -1;
 }
 
-constexpr int BK = 64;  // K per stage: 128 bytes of every row
+// One workgroup's tile: which rows of y, which outputs, whose weights.
+template <class T>
+struct Tile {
+    int64_t row0, row1;  // rows (slots) [row0, row1)
+    int o0;              // first output
+    const T *w, *bias;
+};
 
-// WM x WN waves, each MT x NT MFMA tiles of 32 weight rows x 32 rows.  LDS holds two stages of both
-// operands, 128 bytes a row; chunk c (16 bytes) of row r sits at r * 128 + 16 (c ^ ((r / 2) % 8)), so the
-// 16 rows that one 256-byte LDS cycle of a fragment read serves fall in 16 different slots.
-// A gated layer's tile takes 32 gate rows, the 32 rows they gate, and so on: tile rows
-// 64 i .. 64 i + 31 are gates and 64 i + 32 .. 64 i + 63 their partners, so a lane holds both.
-template <class T, class OUT, bool GROUPED, bool GATED, bool A16, int WM, int WN, int MT, int NT>
-__global__ __launch_bounds__(64 * WM *WN) void product_tile(ProductArgs p)
+constexpr int kBlockRows = 4;
+
+// This workgroup's tile of BO outputs x BN rows; false if it has none.
+template <class T, bool GROUPED, bool GATED, int BO, int BN>
+__device__ __forceinline__ bool take_tile(const ProductArgs &p, Tile<T> &tile)
+{
+    const int n_out = (p.out + BO - 1) / BO;
+    tile.w = (const T *)p.w;
+    tile.bias = (const T *)p.bias;
+    const int row_tiles = GROUPED ? total_tiles(p.offsets, p.experts, (int)p.rows, BN) : (int)((p.rows + BN - 1) / BN);
+    const int64_t t = xcd_tile(blockIdx.x, (int64_t)row_tiles * n_out);
+    if (t < 0)
+        return false;
+    // Blocks of kBlockRows row tiles, the rows of a block fastest: the 32 workgroups that an XCD runs at once
+    // then read 4 row panels and 8 weight panels instead of 2 and 16 (1 and 32).
+    const int block = (int)(t / ((int64_t)kBlockRows * n_out)), in_block = (int)(t - (int64_t)block * kBlockRows * n_out);
+    const int rows_here = min(kBlockRows, row_tiles - block * kBlockRows);
+    const int rt = block * kBlockRows + in_block % rows_here;
+    tile.o0 = in_block / rows_here * BO;
+    if constexpr (GROUPED) {
+        RowTile r;
+        if (!find_tile(p.offsets, p.experts, (int)p.rows, BN, rt, r))
+            return false;
+        tile.row0 = r.row0;
+        tile.row1 = r.row1;
+        tile.w += r.expert * p.w_stride;
+        if (tile.bias)
+            tile.bias += (int64_t)r.expert * p.out * (GATED ? 2 : 1);
+    } else {
+        tile.row0 = (int64_t)rt * BN;
+        tile.row1 = tile.row0 + BN < p.rows ? tile.row0 + BN : p.rows;
+    }
+    return true;
+}
+
+// The weight row behind row r of a tile.  A gated layer's tile takes 32 gate rows, the 32 rows they gate, and
+// so on (tile rows 64 i .. 64 i + 31 and 64 i + 32 .. 64 i + 63), so one wave holds both.  Rows past the last
+// repeat it; what they give is never stored.
+template <bool GATED>
+__device__ __forceinline__ int weight_row(int o0, int r, int out)
+{
+    int o = GATED ? o0 + (r >> 6) * 32 + (r & 31) : o0 + r;
+    o = o < out ? o : out - 1;
+    return GATED && (r & 32) ? o + out : o;
+}
+
+// The row of x behind row r of a tile's rows [row0, row1), the last one where r is past it.
+template <bool GROUPED>
+__device__ __forceinline__ int64_t input_row(const ProductArgs &p, int64_t r, int64_t row1)
+{
+    r = r < row1 ? r : row1 - 1;
+    if (GROUPED && p.slots) {
+        const int a = min(max(p.slots[r], 0), (int)p.rows - 1);
+        r = a / p.k;
+    }
+    return r;
+}
+
+// The bias as the C operand: lane (g, n) of an MFMA tile holds its rows 8 q + 4 g + i (i = 0 .. 3) of column n.
+template <class T, bool GATED>
+__device__ __forceinline__ f16x bias_tile(const T *bias, int o0, int r0, int g, int out)
+{
+    struct __attribute__((packed, aligned(2))) Half4 {
+        T v[4];
+    };
+    f16x b = (f16x)0.0f;
+    if (bias)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int r = r0 + 8 * q + 4 * g;
+            if (weight_row<false>(GATED ? o0 + (r >> 6) * 32 : o0, (GATED ? r & 31 : r) + 3, INT32_MAX) < out) {
+                const Half4 v = *(const Half4 *)(bias + weight_row<GATED>(o0, r, out));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    b[4 * q + i] = (float)v.v[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    b[4 * q + i] = (float)bias[weight_row<GATED>(o0, r + i, out)];
+            }
+        }
+    return b;
+}
+
+struct __attribute__((packed, aligned(2))) Float8 {
+    float v[8];
+};
+
+// The epilogue of one wave: MT x NT MFMA tiles whose first weight row is tile row r0 and first row `row`.
+// One 32 x 32 tile of outputs at a time: the activation and the gate on the sums as they lie, then through 4 KB of
+// LDS of the wave's own (no barrier: one wave writes and reads it) into rows (FP32; chunk k of row n at
+// n * 128 + 16 (k ^ ((n / 2) % 8))), from which a lane takes 8 outputs, adds the residual, rounds once and
+// stores.  The residual is requested kAhead tiles ahead: its latency would otherwise stand once per tile.
+template <class T, bool GATED, int MT, int NT>
+__device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][NT], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
 {
     typedef typename Vec8<T>::type V8;
-    constexpr int TH = 64 * WM * WN, BM = 32 * WM * MT, BN = 32 * WN * NT;
-    constexpr int BO = GATED ? BM / 2 : BM;       // outputs per tile
-    constexpr int OW = GATED ? MT * 16 : MT * 32;  // outputs per wave
-    constexpr int CA = BM * 8 / TH, CB = BN * 8 / TH;  // 16-byte chunks per thread and stage
+    struct __attribute__((packed, aligned(2))) Half8 {
+        V8 v;
+    };
+    const int lane = threadIdx.x & 63, g = lane >> 5, n = lane & 31;
+    constexpr int MO = GATED ? MT / 2 : MT, TILES = MO * NT, kAhead = TILES < 4 ? TILES : 4;
+    const int oc = 8 * (lane & 3), rl = lane >> 2;  // this lane's outputs and (of 16 at a time) row
+    auto out_of = [&](int t) { return o0 + (GATED ? r0 / 2 : r0) + 32 * (t % MO) + oc; };
+    auto row_of = [&](int t, int i) { return row + 32 * (t / MO) + 16 * i + rl; };
+    const bool half_res = p.residual && !p.y_fp32;
+    Half8 res[TILES][2];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (row_of(t, i) < row1 && out_of(t) + 8 <= p.out)
+                res[t][i] = *(const Half8 *)((const T *)p.residual + row_of(t, i) * p.ldr + out_of(t));
+    };
+    if (half_res)
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t)
+            fetch(t);
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+        const int mt = (t % MO) * (GATED ? 2 : 1), nt = t / MO;
+        f16x z = acc[mt][nt];
+        with_activation(p.act, [&](auto act) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                z[j] = act(z[j]);
+        });
+        if constexpr (GATED)
+            z *= acc[mt + 1][nt];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            *(f4 *)(ob + n * 128 + 16 * ((2 * q + g) ^ ((n >> 1) & 7))) = f4{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
+        if (half_res && t + kAhead < TILES)
+            fetch(t + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
+        const int o = out_of(t);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int rt = 16 * i + rl;
+            const int64_t yr = row_of(t, i);
+            if (yr >= row1 || o >= p.out)
+                continue;
+            const uint8_t *lr = ob + rt * 128;
+            const int sw = (rt >> 1) & 7;
+            const int64_t at = yr * p.ldy + o;
+            if (o + 8 <= p.out) {
+                const f4 lo = *(const f4 *)(lr + 16 * ((oc / 4) ^ sw)), hi = *(const f4 *)(lr + 16 * ((oc / 4 + 1) ^ sw));
+                f8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                if (p.y_fp32) {
+                    if (p.residual) {
+                        const Float8 r = *(const Float8 *)((const float *)p.residual + yr * p.ldr + o);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            v[j] += r.v[j];
+                    }
+                    Float8 y;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        y.v[j] = v[j];
+                    *(Float8 *)((float *)p.y + at) = y;
+                } else {
+                    if (half_res)
+                        v += __builtin_convertvector(res[t][i].v, f8);
+                    Half8 y;
+                    y.v = __builtin_convertvector(v, V8);  // nearest even
+                    *(Half8 *)((T *)p.y + at) = y;
+                }
+            } else {  // the last outputs of a width that is no multiple of 8
+#pragma unroll 1
+                for (int j = 0; o + j < p.out; ++j) {
+                    float z = *(const float *)(lr + 16 * ((oc / 4 + j / 4) ^ sw) + 4 * (j % 4));
+                    const int64_t ar = yr * p.ldr + o + j;
+                    if (p.residual)
+                        z += p.y_fp32 ? ((const float *)p.residual)[ar] : (float)((const T *)p.residual)[ar];
+                    if (p.y_fp32)
+                        ((float *)p.y)[at + j] = z;
+                    else
+                        ((T *)p.y)[at + j] = (T)z;
+                }
+            }
+        }
+    }
+}
+
+// WM x WN waves, each MT x NT MFMA tiles of 32 weight rows x 32 rows, K advancing 64 per stage through two
+// stages of LDS: each thread loads its chunks of stage s + 1 into registers while stage s is multiplied.
+// 128 bytes a row; chunk c (16 bytes) of row r sits at slot c ^ ((r / 2) % 8): the 16 rows that one 256-byte
+// LDS cycle of a fragment read serves fall in 16 different slots.
+template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int WPE>
+__global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void product_tile(ProductArgs p)
+{
+    typedef typename Vec8<T>::type V8;
+    constexpr int BK = 64, TH = 64 * WM * WN, BM = 32 * WM * MT, BN = 32 * WN * NT;
+    constexpr int RPP = TH / 8;  // rows the workgroup stages at a time, one chunk per thread
+    constexpr int CA = BM / RPP, CB = BN / RPP;
     constexpr int A_ST = BM * 128, STAGE = (BM + BN) * 128;
-    static_assert(CA * TH == BM * 8 && CB * TH == BN * 8 && (TH / 8) % 16 == 0, "whole chunks per thread, one swizzle per thread");
+    static_assert(CA * RPP == BM && CB * RPP == BN && RPP % 16 == 0, "whole chunks per thread, one swizzle per thread");
     static_assert(!GATED || MT % 2 == 0, "gate and partner tiles in one wave");
-    static_assert(WM * WN * 32 * OW * 4 <= 2 * STAGE, "the epilogue's FP32 rows fit the stages");
+    static_assert(WM * WN * 4096 <= 2 * STAGE, "the epilogue's rows fit the stages");
     __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
 
-    const int n_out = (p.out + BO - 1) / BO;
-    int64_t row0, row1;
-    int ot;
-    const T *w = (const T *)p.w;
-    const T *bias = (const T *)p.bias;
-    if constexpr (GROUPED) {
-        const int64_t t = xcd_tile(blockIdx.x, (int64_t)total_tiles(p.offsets, p.experts, (int)p.rows, BN) * n_out);
-        RowTile rt;
-        if (t < 0 || !find_tile(p.offsets, p.experts, (int)p.rows, BN, (int)(t / n_out), rt))
-            return;  // whole workgroup, before any barrier
-        ot = (int)(t % n_out);
-        row0 = rt.row0;
-        row1 = rt.row1;
-        w += rt.expert * p.w_stride;
-        if (bias)
-            bias += (int64_t)rt.expert * p.out * (GATED ? 2 : 1);
-    } else {
-        const int64_t t = xcd_tile(blockIdx.x, (p.rows + BN - 1) / BN * n_out);
-        if (t < 0)
-            return;
-        ot = (int)(t % n_out);
-        row0 = t / n_out * BN;
-        row1 = row0 + BN < p.rows ? row0 + BN : p.rows;
-    }
-    const int o0 = ot * BO;
-
+    Tile<T> tile;
+    if (!take_tile<T, GROUPED, GATED, (GATED ? BM / 2 : BM), BN>(p, tile))
+        return;  // whole workgroup, before any barrier
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave % WM, wn = wave / WM;
     const int g = lane >> 5, n = lane & 31;
-
-    // The rows this thread stages: chunk c = tid % 8 of tile rows tid / 8 + i * TH / 8.  Rows past the end
-    // repeat the last one; what they give is never stored.
-    const int c = tid & 7;
+    const int c = tid % 8, r_in = tid / 8;
     const T *wp[CA], *xp[CB];
 #pragma unroll
-    for (int i = 0; i < CA; ++i) {
-        const int r = (tid >> 3) + i * (TH / 8);
-        int o = GATED ? o0 + (r >> 6) * 32 + (r & 31) : o0 + r;
-        o = o < p.out ? o : p.out - 1;
-        if (GATED && (r & 32))
-            o += p.out;
-        wp[i] = w + (int64_t)o * p.ldw + 8 * c;
-    }
+    for (int i = 0; i < CA; ++i)
+        wp[i] = tile.w + (int64_t)weight_row<GATED>(tile.o0, r_in + i * RPP, p.out) * p.ldw + 8 * c;
 #pragma unroll
-    for (int i = 0; i < CB; ++i) {
-        int64_t r = row0 + (tid >> 3) + i * (TH / 8);
-        r = r < row1 ? r : row1 - 1;
-        if (GROUPED && p.slots) {
-            const int a = min(max(p.slots[r], 0), (int)p.rows - 1);
-            r = a / p.k;
-        }
-        xp[i] = (const T *)p.x + r * p.ldx + 8 * c;
-    }
-    const int st = (tid >> 3) * 128 + 16 * (c ^ ((tid >> 4) & 7));
+    for (int i = 0; i < CB; ++i)
+        xp[i] = (const T *)p.x + input_row<GROUPED>(p, tile.row0 + r_in + i * RPP, tile.row1) * p.ldx + 8 * c;
+    const int st = r_in * 128 + 16 * (c ^ ((r_in >> 1) & 7));
 
-    // Bias: lane (g, n) of MFMA tile (mt, nt) holds tile rows 32 mt + 8 q + 4 g + i (i = 0 .. 3) of row n.
     f16x acc[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        f16x b = (f16x)0.0f;
-        if (bias) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int r = (wm * MT + mt) * 32 + 8 * (j >> 2) + 4 * g + (j & 3);
-                const int o = GATED ? o0 + (r >> 6) * 32 + (r & 31) : o0 + r;
-                if (o < p.out)
-                    b[j] = (float)bias[o + (GATED && (r & 32) ? p.out : 0)];
-            }
-        }
+        const f16x b = bias_tile<T, GATED>(tile.bias, tile.o0, (wm * MT + mt) * 32, g, p.out);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             acc[mt][nt] = b;
@@ -244,27 +409,27 @@ __global__ __launch_bounds__(64 * WM *WN) void product_tile(ProductArgs p)
     auto load = [&](int s) {
 #pragma unroll
         for (int i = 0; i < CA; ++i)
-            ra[i] = load16<A16>(wp[i] + s * BK);
+            ra[i] = load16(wp[i] + s * BK);
 #pragma unroll
         for (int i = 0; i < CB; ++i)
-            rb[i] = load16<A16>(xp[i] + s * BK);
+            rb[i] = load16(xp[i] + s * BK);
     };
     auto load_tail = [&]() {
 #pragma unroll
         for (int i = 0; i < CA; ++i)
-            ra[i] = load16_tail<A16>(wp[i] - 8 * c, full * BK + 8 * c, p.in);
+            ra[i] = load16_tail(wp[i] - 8 * c, full * BK + 8 * c, p.in);
 #pragma unroll
         for (int i = 0; i < CB; ++i)
-            rb[i] = load16_tail<A16>(xp[i] - 8 * c, full * BK + 8 * c, p.in);
+            rb[i] = load16_tail(xp[i] - 8 * c, full * BK + 8 * c, p.in);
     };
     auto store = [&](int s) {
         uint8_t *d = lds + (s & 1) * STAGE + st;
 #pragma unroll
         for (int i = 0; i < CA; ++i)
-            *(u4 *)(d + i * (TH / 8) * 128) = ra[i];
+            *(u4 *)(d + i * RPP * 128) = ra[i];
 #pragma unroll
         for (int i = 0; i < CB; ++i)
-            *(u4 *)(d + A_ST + i * (TH / 8) * 128) = rb[i];
+            *(u4 *)(d + A_ST + i * RPP * 128) = rb[i];
     };
     const int a_rd = (wm * MT * 32 + n) * 128, b_rd = A_ST + (wn * NT * 32 + n) * 128, swz = (n >> 1) & 7;
     auto multiply = [&](int s) {
@@ -308,69 +473,260 @@ __global__ __launch_bounds__(64 * WM *WN) void product_tile(ProductArgs p)
     }
     multiply(s);
     __syncthreads();
+    epilogue<T, GATED>(p, acc, lds + wave * 4096, tile.o0, wm * MT * 32, tile.row0 + wn * NT * 32, tile.row1);
+}
 
-    // Epilogue, 32 rows of the wave at a time through its own LDS region (no barrier: one wave writes and
-    // reads it): lane (g, n) writes its outputs of row n in FP32, 4 at a time (chunk k of row n at
-    // n * OW * 4 + 16 (k ^ (n % NCH))), then the lanes read whole rows back, 8 outputs each, add the residual, round and
-    // store 16 (FP32: 32) bytes.
-    constexpr int NCH = OW / 4, LPR = OW / 8, RPI = 64 / LPR;  // chunks per row; lanes per row; rows per instruction
-    uint8_t *ob = lds + wave * (32 * OW * 4);
+// The same for rows of whole 16-byte chunks: the stages go from memory into LDS directly, NS of them in flight.
+// A stage is 64 columns, 128 bytes of every row: whole cache lines (at 32 columns each line came from L2 twice).
+// A stage's last quarter is multiplied after the barrier that frees it, while the next stage's first fragments are
+// read, so the matrix unit does not wait for LDS there.
+template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int NS, int WPE>
+__global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void product_big(ProductArgs p)
+{
+    typedef typename Vec8<T>::type V8;
+    constexpr int BK = 64, TH = 64 * WM * WN, BM = 32 * WM * MT, BN = 32 * WN * NT;
+    constexpr int RPP = TH / 8;
+    constexpr int CA = BM / RPP, CB = BN / RPP;  // 16-byte loads per thread and stage
+    constexpr int A_ST = BM * 128, STAGE = (BM + BN) * 128;
+    static_assert(CA * RPP == BM && CB * RPP == BN && RPP % 16 == 0, "whole chunks per thread, one swizzle per thread");
+    static_assert(!GATED || MT % 2 == 0, "gate and partner tiles in one wave");
+    static_assert(WM * WN * 4096 <= STAGE, "the epilogue's rows fit a stage");
+    static_assert(NS == 2 || NS == 3, "");
+    // A variable each: the compiler then knows that a load into one does not touch another.
+    __shared__ __attribute__((aligned(16))) uint8_t l0[STAGE], l1[STAGE], l2[NS == 3 ? STAGE : 16];
+
+    Tile<T> tile;
+    if (!take_tile<T, GROUPED, GATED, (GATED ? BM / 2 : BM), BN>(p, tile))
+        return;  // whole workgroup, before any barrier
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int g = lane >> 5, n = lane & 31;
+    const int r_in = tid / 8;
+    const int c = (tid & 7) ^ ((r_in >> 1) & 7);  // the chunk that this thread's slot holds
+    const T *src[CA + CB];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int i = 0; i < CA; ++i)
+        src[i] = tile.w + (int64_t)weight_row<GATED>(tile.o0, r_in + i * RPP, p.out) * p.ldw + 8 * c;
 #pragma unroll
-        for (int mt = 0; mt < MT; mt += GATED ? 2 : 1)
+    for (int i = 0; i < CB; ++i)
+        src[CA + i] = (const T *)p.x + input_row<GROUPED>(p, tile.row0 + r_in + i * RPP, tile.row1) * p.ldx + 8 * c;
+
+    const int full = p.in / BK;
+    int issued = 0;  // stages requested; past the last whole one it is requested again, unused
+    auto request = [&](uint8_t *dst) {
+        const int step = issued + 1 < full ? BK : 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                f4 v;
+        for (int i = 0; i < CA + CB; ++i) {
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src[i],
+                                             (__attribute__((address_space(3))) void *)(dst + wave * 1024 + i * (TH * 16)), 16, 0, 0);
+            src[i] += step;
+        }
+        ++issued;
+    };
+    V8 fa[2][MT], fb[2][NT];
+    const int a_rd = (wm * MT * 32 + n) * 128, b_rd = A_ST + (wn * NT * 32 + n) * 128, swz = (n >> 1) & 7;
+    auto read = [&](const uint8_t *d, int kb) {
+        const int ch = 16 * ((2 * kb + g) ^ swz);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[i] = activate(acc[mt][nt][4 * q + i], p.act);
-                    if constexpr (GATED)
-                        v[i] *= acc[mt + 1][nt][4 * q + i];
-                }
-                const int k = (GATED ? mt / 2 : mt) * 8 + 2 * q + g;
-                *(f4 *)(ob + n * (OW * 4) + 16 * (k ^ (n & (NCH - 1)))) = v;
-            }
-        const int o = o0 + wm * OW + 8 * (lane % LPR);
+        for (int mt = 0; mt < MT; ++mt)
+            fa[kb & 1][mt] = *(const V8 *)(d + a_rd + mt * 32 * 128 + ch);
 #pragma unroll
-        for (int i = 0; i < 32 / RPI; ++i) {
-            const int rl = i * RPI + lane / LPR;
-            const int64_t row = row0 + (wn * NT + nt) * 32 + rl;
-            const int k = 2 * (lane % LPR);
-            const f4 lo = *(const f4 *)(ob + rl * (OW * 4) + 16 * (k ^ (rl & (NCH - 1))));
-            const f4 hi = *(const f4 *)(ob + rl * (OW * 4) + 16 * ((k + 1) ^ (rl & (NCH - 1))));
-            if (row >= row1 || o >= p.out)
-                continue;
-            float v[8];
+        for (int nt = 0; nt < NT; ++nt)
+            fb[kb & 1][nt] = *(const V8 *)(d + b_rd + nt * 32 * 128 + ch);
+    };
+    f16x acc[MT][NT];
+    auto multiply = [&](int kb) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = lo[j];
-                v[4 + j] = hi[j];
-            }
-            OUT *y = (OUT *)p.y + row * p.ldy + o;
-            const OUT *res = p.residual ? (const OUT *)p.residual + row * p.ldr + o : nullptr;
-            struct __attribute__((packed, aligned(2))) Out8 {
-                OUT v[8];
-            };
-            if (o + 8 <= p.out) {
-                if (res) {
-                    const Out8 r = *(const Out8 *)res;
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[j] += (float)r.v[j];
-                }
-                Out8 out;
+            for (int nt = 0; nt < NT; ++nt)
+                acc[mt][nt] = mfma32(fa[kb & 1][mt], fb[kb & 1][nt], acc[mt][nt]);
+    };
+    auto mix = [&]() {  // one MFMA, then one LDS read
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    out.v[j] = (OUT)v[j];  // nearest even
-                *(Out8 *)y = out;
+        for (int i = 0; i < (MT * NT < MT + NT ? MT * NT : MT + NT); ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        if constexpr (MT * NT > MT + NT)
+            __builtin_amdgcn_sched_group_barrier(0x008, MT * NT - MT - NT, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr int AHEAD = (NS - 2) * (CA + CB);  // loads still in flight when the next stage has to be there
+    // One stage, whose first fragments have been read: cur is its buffer, nxt the next stage's.
+    auto quarters = [&](const uint8_t *__restrict cur) {
+#pragma unroll
+        for (int kb = 0; kb < 3; ++kb) {
+            read(cur, kb + 1);
+            multiply(kb);
+            mix();
+        }
+    };
+    auto last = [&](const uint8_t *__restrict nxt, uint8_t *__restrict freed) {
+        request(freed);
+        read(nxt, 0);
+        multiply(3);
+        mix();
+    };
+    auto turn = [&](auto ahead) {
+        constexpr int V = decltype(ahead)::value;
+        __builtin_amdgcn_s_waitcnt(0x0070 | (V & 15) | (V >> 4) << 14);  // vmcnt(V) lgkmcnt(0)
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+#define MLP_STAGE(CUR, NXT)                                                                                    \
+    quarters(CUR);                                                                                             \
+    turn(Number<AHEAD>{});                                                                                     \
+    last(NXT, CUR);                                                                                            \
+    if (++s == full)                                                                                           \
+        break;
+    if (full) {
+        request(l0);
+        request(l1);
+        if constexpr (NS == 3)
+            request(l2);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const f16x b = bias_tile<T, GATED>(tile.bias, tile.o0, (wm * MT + mt) * 32, g, p.out);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            acc[mt][nt] = b;
+    }
+    if (full) {
+        turn(Number<(NS - 1) * (CA + CB)>{});
+        read(l0, 0);
+        for (int s = 0;;) {
+            MLP_STAGE(l0, l1)
+            if constexpr (NS == 3) {
+                MLP_STAGE(l1, l2)
+                MLP_STAGE(l2, l0)
             } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (o + j < p.out)
-                        y[j] = (OUT)(v[j] + (res ? (float)res[j] : 0.0f));
+                MLP_STAGE(l1, l0)
             }
         }
+    }
+#undef MLP_STAGE
+    __builtin_amdgcn_s_waitcnt(0x0070);  // the requests past the end
+    __syncthreads();
+    if (full * BK < p.in) {  // a partial last stage, through registers
+#pragma unroll
+        for (int i = 0; i < CA + CB; ++i) {
+            const T *row = src[i] - 8 * c - (full ? (full - 1) * BK : 0);
+            *(u4 *)(l0 + tid * 16 + i * (TH * 16)) = load16_tail(row, full * BK + 8 * c, p.in);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+            read(l0, kb);
+            multiply(kb);
+        }
+        __syncthreads();
+    }
+    epilogue<T, GATED>(p, acc, l0 + wave * 4096, tile.o0, wm * MT * 32, tile.row0 + wn * NT * 32, tile.row1);
+}
+
+// Few rows: a workgroup of NW waves (blockDim / 64, at most 16) takes 16 * MA weight rows and up to 16 rows of
+// x, and its waves share K: each multiplies a run of columns straight from memory (16 x 16 x 32 MFMA, weights = A,
+// x = B; lane (g, n) loads the 16 bytes of row n at columns 8 g), kDepth steps requested at once, and the waves'
+// sums meet in LDS.  Every wave's loads are independent, with no LDS or barrier between them; the weights' bytes are
+// the floor (7 x 2,048 -> 2 x 4,096 gated: 33.6 MB).  Taking 32 or 64 rows at once instead of several workgroups that
+// read the same weights from L2 was slower (32 x 4,096 -> 4,096: 20 against 14 us; 64 x 4,096 -> 1,024: 27 against 10).
+template <class T, bool GROUPED, bool GATED, int MA>
+__global__ __launch_bounds__(1024) void product_few(ProductArgs p)
+{
+    typedef typename Vec8<T>::type V8;
+    static_assert(!GATED || MA == 2, "16 gates and the 16 they gate");
+    constexpr int BO = GATED ? 16 : 16 * MA, BN = 16, kDepth = 4;
+    constexpr int SUMS = 16 * MA * BN;  // per wave
+    extern __shared__ float sums[];      // [NW][MA][16 rows of x][16 weight rows]
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int nw = blockDim.x >> 6, g = lane >> 4, n = lane & 15;
+    const int n_out = (p.out + BO - 1) / BO;
+    const int o0 = (int)(blockIdx.x % n_out) * BO;
+    int64_t row0 = (int64_t)(blockIdx.x / n_out) * BN, row1 = row0 + BN < p.rows ? row0 + BN : p.rows;
+    const T *w = (const T *)p.w, *bias = (const T *)p.bias;
+    if constexpr (GROUPED) {
+        RowTile rt;
+        if (!find_tile(p.offsets, p.experts, (int)p.rows, BN, (int)(blockIdx.x / n_out), rt))
+            return;  // whole workgroup
+        row0 = rt.row0;
+        row1 = rt.row1;
+        w += rt.expert * p.w_stride;
+        if (bias)
+            bias += (int64_t)rt.expert * p.out * (GATED ? 2 : 1);
+    }
+    const T *wp[MA];
+#pragma unroll
+    for (int i = 0; i < MA; ++i) {
+        int o = o0 + (GATED ? 0 : 16 * i) + n;
+        o = (o < p.out ? o : p.out - 1) + (GATED && i ? p.out : 0);
+        wp[i] = w + (int64_t)o * p.ldw;
+    }
+    const T *xp = (const T *)p.x + input_row<GROUPED>(p, row0 + n, row1) * p.ldx;
+
+    f4 acc[MA];
+#pragma unroll
+    for (int j = 0; j < MA; ++j)
+        acc[j] = (f4)0.0f;
+    const int share = ((p.in + nw - 1) / nw + 31) / 32 * 32;
+    const int begin = wave * share, end = min(begin + share, p.in);
+    int k = begin;
+    u4 a[kDepth][MA], b[kDepth];
+    auto multiply = [&](int d) {
+#pragma unroll
+        for (int j = 0; j < MA; ++j)
+            acc[j] = mfma16(__builtin_bit_cast(V8, a[d][j]), __builtin_bit_cast(V8, b[d]), acc[j]);
+    };
+    for (; k + 32 * kDepth <= end; k += 32 * kDepth) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+#pragma unroll
+            for (int j = 0; j < MA; ++j)
+                a[d][j] = load16(wp[j] + k + 32 * d + 8 * g);
+            b[d] = load16(xp + k + 32 * d + 8 * g);
+        }
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d)
+            multiply(d);
+    }
+    for (; k < end; k += 32) {  // the rest, and a last step of fewer than 32 columns
+#pragma unroll
+        for (int j = 0; j < MA; ++j)
+            a[0][j] = load16_tail(wp[j], k + 8 * g, p.in);
+        b[0] = load16_tail(xp, k + 8 * g, p.in);
+        multiply(0);
+    }
+    // Lane (g, n) of an MFMA tile holds weight rows 4 g .. 4 g + 3 of row n.
+#pragma unroll
+    for (int j = 0; j < MA; ++j)
+        *(f4 *)(sums + wave * SUMS + (j * 16 + n) * 16 + 4 * g) = acc[j];
+    __syncthreads();
+    for (int i = tid; i < BO * BN; i += blockDim.x) {
+        // 16 outputs of a row together
+        const int ol = i % 16, oj = GATED ? 0 : i / 16 % MA, rl = i / BO;
+        const int at = (oj * 16 + rl) * 16 + ol;
+        const int o = o0 + 16 * oj + ol;
+        const int64_t row = row0 + rl;
+        if (o >= p.out || row >= row1)
+            continue;
+        float z = bias ? (float)bias[o] : 0.0f, u = GATED && bias ? (float)bias[o + p.out] : 0.0f;
+        for (int v = 0; v < nw; ++v) {
+            z += sums[v * SUMS + at];
+            if constexpr (GATED)
+                u += sums[v * SUMS + at + 256];
+        }
+        with_activation(p.act, [&](auto act) { z = act(z); });
+        if constexpr (GATED)
+            z *= u;
+        if (p.residual)
+            z += p.y_fp32 ? ((const float *)p.residual)[row * p.ldr + o] : (float)((const T *)p.residual)[row * p.ldr + o];
+        if (p.y_fp32)
+            ((float *)p.y)[row * p.ldy + o] = z;
+        else
+            ((T *)p.y)[row * p.ldy + o] = (T)z;
     }
 }
 
@@ -403,49 +759,106 @@ __global__ __launch_bounds__(256) void combine_rows(CombineArgs c)
     }
 }
 
-constexpr int kTileRows = 64, kTileOut = 64;  // of the one tile below (a gated tile: half the outputs)
+// ---- which kernel ---------------------------------------------------------------------------------
 
-int64_t tiles_most(const ProductArgs &p, bool gated, bool grouped)
+// kBig 256 weight rows x 256 rows, kMid 128 x 128, kSmall 128 x 64 (all three straight into LDS), kTile 64 x 128 through
+// registers, kFew 16 x 16, kFewWide 32 x 16.
+enum Form { kBig, kMid, kSmall, kTile, kFew, kFewWide };
+struct Shape {
+    int bm, bn, threads;
+};
+constexpr Shape kShapes[] = {{256, 256, 512}, {128, 128, 256}, {128, 64, 256}, {64, 128, 256}, {16, 16, 1024}, {32, 16, 1024}};
+
+// Row tiles of bn rows there can be at most.
+int64_t row_tiles(const ProductArgs &p, bool grouped, int bn)
 {
-    const int64_t bo = gated ? kTileOut / 2 : kTileOut, n_out = (p.out + bo - 1) / bo;
-    const int64_t row_tiles = grouped ? p.rows / kTileRows + (p.rows < p.experts ? p.rows : p.experts) : (p.rows + kTileRows - 1) / kTileRows;
-    return (row_tiles * n_out + 7) / 8 * 8;
+    return grouped ? p.rows / bn + (p.rows < p.experts ? p.rows : p.experts) : (p.rows + bn - 1) / bn;
 }
 
-template <class T, class OUT, bool GROUPED, bool GATED>
-hipError_t launch(const ProductArgs &p, hipStream_t stream)
+int64_t tiles_most(const ProductArgs &p, bool gated, bool grouped, Form f)
+{
+    const Shape s = kShapes[f];
+    const int64_t bo = gated ? (f == kFew || f == kFewWide ? 16 : s.bm / 2) : s.bm;
+    const int64_t tiles = (p.out + bo - 1) / bo * row_tiles(p, grouped, s.bn);
+    return f == kFew || f == kFewWide ? tiles : (tiles + 7) / 8 * 8;  // the XCDs' runs are equally long
+}
+
+// Chosen by how many tiles there are for 256 CUs (MI355X), us measured in BF16:
+//   - fewer than 1,024 tiles of 16 x 16: kFew, whose waves share K (1 x 1,024 -> 1,024: 3 against 11 with 128 x 64
+//     tiles; 64 x 4,096 -> 1,024: 10 against 41; 300 x 1,024 -> 1,024, 1,216 tiles: 13 both), from 512 on 32 weight
+//     rows at a time (32 x 4,096 -> 4,096: 14 against 17);
+//   - at most 64 weight rows, or rows that are not 16-byte aligned (which kTile alone takes): kTile (262,144 rows
+//     64 -> 64: 19 against 30 with 128 x 128);
+//   - more than 512 tiles of 128 x 128, two per CU: kBig (8,192 x 4,096 -> 4,096: 232 against 281; 65,536 x 1,024 ->
+//     1,024: 146 against 191), 192 and more: kMid (5,003 x 1,008 -> 776: 23 against 28 with kSmall; 2,048^3: 27
+//     against 48 with kBig), else kSmall (512 x 1,024 -> 4,096: 12 against 16).
+// The experts' rows fill their last tiles by half: kBig and kMid only from 192 and 96 rows per expert on (2,048
+// assignments over 32 experts, 1,024 -> 2 x 1,024: 35 with kSmall, 46 with kMid; 32,768: 363 with kMid, 310 with kBig).
+Form choose_form(const ProductArgs &p, bool gated, bool grouped)
 {
     const bool a16 = p.ldx % 8 == 0 && p.ldw % 8 == 0 && p.w_stride % 8 == 0 && (((uintptr_t)p.x | (uintptr_t)p.w) & 15) == 0;
-    const dim3 grid((unsigned)tiles_most(p, GATED, GROUPED));
-    constexpr int WM = GATED ? 1 : 2, WN = GATED ? 2 : 2, MT = GATED ? 2 : 1;
-    if (a16)
-        hipLaunchKernelGGL((product_tile<T, OUT, GROUPED, GATED, true, WM, WN, MT, 1>), grid, dim3(64 * WM * WN), 0, stream, p);
-    else
-        hipLaunchKernelGGL((product_tile<T, OUT, GROUPED, GATED, false, WM, WN, MT, 1>), grid, dim3(64 * WM * WN), 0, stream, p);
+    const int64_t wide = (int64_t)p.out * (gated ? 2 : 1);
+    const int64_t few = row_tiles(p, grouped, 16) * ((wide + 15) / 16);
+    if (few < 1024)
+        return gated || few >= 512 ? kFewWide : kFew;
+    if (!a16 || wide <= 64)
+        return kTile;
+    const int64_t used = grouped ? (p.rows < p.experts ? p.rows : p.experts) : 1, each = p.rows / used;
+    const int64_t mid = (p.rows / 128 + (used + 1) / 2) * ((wide + 127) / 128);
+    if (mid > 512 && (!grouped || each >= 192))
+        return kBig;
+    return mid >= 192 && (!grouped || each >= 96) ? kMid : kSmall;
+}
+
+template <class T, bool GROUPED, bool GATED>
+hipError_t launch(const ProductArgs &p, hipStream_t stream)
+{
+    const Form form = choose_form(p, GATED, GROUPED);
+    const dim3 grid((unsigned)tiles_most(p, GATED, GROUPED, form)), block(kShapes[form].threads);
+    switch (form) {
+    case kBig:
+        hipLaunchKernelGGL((product_big<T, GROUPED, GATED, 2, 4, 4, 2, 2, 2>), grid, block, 0, stream, p);
+        break;
+    case kMid:
+        hipLaunchKernelGGL((product_big<T, GROUPED, GATED, 2, 2, 2, 2, 2, 2>), grid, block, 0, stream, p);
+        break;
+    case kSmall:
+        hipLaunchKernelGGL((product_big<T, GROUPED, GATED, 2, 2, 2, 1, 3, 2>), grid, block, 0, stream, p);
+        break;
+    case kTile:
+        hipLaunchKernelGGL((product_tile<T, GROUPED, GATED, 1, 4, 2, 1, 3>), grid, block, 0, stream, p);
+        break;
+    default:
+        // 64 columns or more for each of up to 16 waves
+        const int waves = p.in >= 1024 ? 16 : p.in >= 512 ? 8 : p.in >= 256 ? 4 : p.in >= 128 ? 2 : 1;
+        const size_t lds = (size_t)waves * kShapes[form].bm * 16 * 4;
+        if (GATED || form == kFewWide)
+            hipLaunchKernelGGL((product_few<T, GROUPED, GATED, 2>), grid, dim3(64 * waves), lds, stream, p);
+        else
+            hipLaunchKernelGGL((product_few<T, GROUPED, GATED, GATED ? 2 : 1>), grid, dim3(64 * waves), lds, stream, p);
+    }
     return hipGetLastError();
 }
 
-template <class T, class OUT>
+template <class T>
 hipError_t launch(const ProductArgs &p, bool gated, bool grouped, hipStream_t stream)
 {
     if (grouped)
-        return gated ? launch<T, OUT, true, true>(p, stream) : launch<T, OUT, true, false>(p, stream);
-    return gated ? launch<T, OUT, false, true>(p, stream) : launch<T, OUT, false, false>(p, stream);
+        return gated ? launch<T, true, true>(p, stream) : launch<T, true, false>(p, stream);
+    return gated ? launch<T, false, true>(p, stream) : launch<T, false, false>(p, stream);
 }
 
 }  // namespace
 
 bool product_fits(const ProductArgs &p, bool gated, bool grouped)
 {
-    return tiles_most(p, gated, grouped) * 256 <= UINT32_MAX;  // a grid counts its threads in 32 bits
+    const Form form = choose_form(p, gated, grouped);
+    return tiles_most(p, gated, grouped, form) * kShapes[form].threads <= UINT32_MAX;  // a grid counts its threads in 32 bits
 }
 
-hipError_t launch_product(const ProductArgs &p, int dtype, int out_dtype, bool gated, bool grouped, hipStream_t stream)
+hipError_t launch_product(const ProductArgs &p, int dtype, bool gated, bool grouped, hipStream_t stream)
 {
-    if (dtype == kFp16)
-        return out_dtype == kFp32 ? launch<_Float16, float>(p, gated, grouped, stream)
-                                  : launch<_Float16, _Float16>(p, gated, grouped, stream);
-    return out_dtype == kFp32 ? launch<__bf16, float>(p, gated, grouped, stream) : launch<__bf16, __bf16>(p, gated, grouped, stream);
+    return dtype == kFp16 ? launch<_Float16>(p, gated, grouped, stream) : launch<__bf16>(p, gated, grouped, stream);
 }
 
 hipError_t launch_combine(const CombineArgs &c, int out_dtype, hipStream_t stream)

@@ -91,9 +91,9 @@ def lib() -> ctypes.CDLL:
 
 def _call(name: str, args: ctypes.Structure, device) -> None:
     """Enqueue on the current stream of the tensors' device."""
-    f = getattr(lib(), name)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+    f = getattr(_lib or lib(), name)
+    stream = torch._C._cuda_getCurrentRawStream(device.index)  # torch.cuda.current_stream takes longer than the launch
+    if torch._C._cuda_getDevice() == device.index:
         rc = f(ctypes.addressof(args), stream)
     else:
         with torch.cuda.device(device):
@@ -105,7 +105,7 @@ def _call(name: str, args: ctypes.Structure, device) -> None:
 def _workspace(name: str, args: ctypes.Structure, device):
     """Scratch memory for the call, from the current stream's allocator; None where it needs none."""
     need = _u64()
-    rc = getattr(lib(), name)(ctypes.addressof(args), ctypes.addressof(need))
+    rc = getattr(_lib or lib(), name)(ctypes.addressof(args), ctypes.addressof(need))
     if rc != B.MLP_OK:
         raise B.MlpError(rc, name, B.mlp_last_error())
     if not need.value:

@@ -56,6 +56,28 @@ def test_linear(rows, k, n, dtype):
     R.check(y, *R.linear64(x, w, b, r, "gelu"), torch.float32, "fp32")
 
 
+# (rows, in, out, gated): sizes that take the larger tiles, whole and with borders in every direction, K below a
+# stage, of one, of whole ones and with a rest
+LARGE = [(5000, 200, 1800, False), (5000, 40, 1801, False), (4864, 128, 2048, False), (2600, 264, 1700, True),
+         (2500, 72, 1500, False), (2048, 64, 2048, False), (1300, 200, 1100, True), (600, 136, 700, False), (640, 192, 640, False),
+         (300, 64, 650, True), (9000, 72, 64, False), (9001, 33, 50, False), (4000, 64, 32, True), (700, 101, 903, False),
+         (513, 77, 455, True), (150, 1040, 1000, False)]
+
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("rows,k,n,gated", LARGE)
+def test_linear_large(rows, k, n, gated, dtype):
+    g, t = gen(rows + k), HALF[dtype]
+    wide = 2 * n if gated else n
+    x, w = rnd(g, rows, k, dtype=t), rnd(g, wide, k, dtype=t, scale=k ** -0.5)
+    b, r = rnd(g, wide, dtype=t), rnd(g, rows, n, dtype=t)
+    log("linear large", rows, k, n, gated, dtype)
+    y = ops.linear(gpu(x), gpu(w), gpu(b), residual=gpu(r), act="silu", gated=gated)
+    R.check(y, *R.linear64(x, w, b, r, "silu", gated), t, "epilogue")
+    y = ops.linear(gpu(x), gpu(w), residual=gpu(r.float()), gated=gated, out_dtype=torch.float32)
+    R.check(y, *R.linear64(x, w, None, r, "none", gated), torch.float32, "fp32")
+
+
 @pytest.mark.parametrize("act", ops.ACTIVATIONS)
 @pytest.mark.parametrize("rows,k,n", [(1, 96, 40), (9, 130, 33), (70, 64, 96), (260, 136, 200)])
 def test_linear_activations_and_gates(rows, k, n, act):
@@ -270,7 +292,8 @@ def test_dispatch_large():
 # ---- the experts' layers -----------------------------------------------------------------------------
 
 EXPERT_SIZES = [(1, 1, 1, 8, 8), (1, 2, 3, 40, 24), (3, 4, 9, 33, 17), (8, 4, 32, 128, 96), (64, 2, 4, 64, 64), (37, 3, 5, 200, 130),
-                (300, 1, 16, 64, 64), (500, 2, 3, 96, 264), (260, 6, 70, 72, 40), (20, 2, 200, 16, 16)]
+                (300, 1, 16, 64, 64), (500, 2, 3, 96, 264), (260, 6, 70, 72, 40), (20, 2, 200, 16, 16), (3000, 2, 4, 72, 1200),
+                (900, 2, 5, 136, 700), (4000, 1, 16, 64, 64), (1000, 3, 20, 40, 264), (700, 2, 6, 33, 300)]
 
 
 def routed(g, tokens, k, experts, drop=True):
