@@ -45,6 +45,7 @@ enum {
 };
 
 #define MLP_OPS_MAX_WIDTH (1 << 20) /* widths of mlp_linear and mlp_expert_linear */
+#define MLP_OPS_MAX_STRIDE (1 << 24) /* row strides of y and residual there, in elements */
 #define MLP_OPS_MAX_EXPERTS 1024
 #define MLP_OPS_MAX_TOPK 32 /* experts per token */
 

@@ -58,6 +58,15 @@ int check_matrix(const char *name, const void *p, int64_t rows, int64_t cols, in
     return MLP_OK;
 }
 
+// The kernels step through y and residual in 32 bits.
+int check_stride(const char *name, int64_t ld)
+{
+    if (ld > MLP_OPS_MAX_STRIDE)
+        return fail(MLP_ERR_INVALID_ARGUMENT, "the row stride of %s, %lld, is larger than %d", name, (long long)ld,
+                    MLP_OPS_MAX_STRIDE);
+    return MLP_OK;
+}
+
 int check_vector(const char *name, const void *p, int size)
 {
     if (!p)
@@ -183,6 +192,7 @@ int mlp_linear(const mlp_linear_args *a, void *stream)
     MLP_TRY(check_matrix("x", a->x, a->rows, a->in_width, a->ldx, 2));
     MLP_TRY(check_matrix("w", a->w, wide, a->in_width, a->ldw, 2));
     MLP_TRY(check_matrix("y", a->y, a->rows, a->out_width, a->ldy, out_size));
+    MLP_TRY(check_stride("y", a->ldy));
     if (a->bias)
         MLP_TRY(check_vector("bias", a->bias, 2));
     const Span y = span(a->y, a->rows, a->out_width, a->ldy, out_size);
@@ -191,6 +201,7 @@ int mlp_linear(const mlp_linear_args *a, void *stream)
         return fail(MLP_ERR_INVALID_ARGUMENT, "y overlaps x, w or bias");
     if (a->residual) {
         MLP_TRY(check_matrix("residual", a->residual, a->rows, a->out_width, a->ldr, out_size));
+        MLP_TRY(check_stride("residual", a->ldr));
         if (!(a->residual == a->y && (a->ldr == a->ldy || a->rows == 1)) &&
             overlap(y, span(a->residual, a->rows, a->out_width, a->ldr, out_size)))
             return fail(MLP_ERR_INVALID_ARGUMENT, "y overlaps residual without being it");
@@ -333,6 +344,7 @@ int mlp_expert_linear(const mlp_expert_linear_args *a, void *stream)
         return fail(MLP_ERR_INVALID_ARGUMENT, "w_stride %lld does not hold an expert's %lld rows", (long long)a->w_stride,
                     (long long)wide);
     MLP_TRY(check_matrix("y", a->y, y_rows, a->out_width, a->ldy, out_size));
+    MLP_TRY(check_stride("y", a->ldy));
     if (a->bias)
         MLP_TRY(check_vector("bias", a->bias, 2));
     MLP_TRY(check_vector("offsets", a->offsets, 4));
@@ -351,6 +363,7 @@ int mlp_expert_linear(const mlp_expert_linear_args *a, void *stream)
         return fail(MLP_ERR_INVALID_ARGUMENT, "y overlaps an input");
     if (a->residual) {
         MLP_TRY(check_matrix("residual", a->residual, y_rows, a->out_width, a->ldr, out_size));
+        MLP_TRY(check_stride("residual", a->ldr));
         if (!(a->residual == a->y && (a->ldr == a->ldy || y_rows == 1)) &&
             overlap(y, span(a->residual, y_rows, a->out_width, a->ldr, out_size)))
             return fail(MLP_ERR_INVALID_ARGUMENT, "y overlaps residual without being it");

@@ -36,19 +36,25 @@ __device__ __forceinline__ f16x mfma32(b8 a, b8 b, f16x c) { return __builtin_am
 __device__ __forceinline__ f4 mfma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f4 mfma16(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
-// v (1 + erf(v / sqrt 2)) / 2.  erfc(u) = t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) exp(-u^2), t = 1 / (1 + 0.3275911 u),
-// for u >= 0: Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26, off by at most 1.5e-7;
-// written with erfc on the negative side too, so nothing cancels there.
+// v (1 + erf(v / sqrt 2)) / 2 = max(v, 0) - |v| h, h = erfc(|v| / sqrt 2) / 2.  log2 h is smooth, so h = 2^P(|v|) with
+// a polynomial of degree 8, fitted to log2 h on [0, 5.5] by weighted least squares, the weights moved until the error
+// is level: h is off by at most 1e-5 of itself, the result by at most 0.5 (2^-20 of itself + 2^-22 |v|).  P falls ever
+// faster beyond.  One exponential and 11 full-rate operations; the activation of a 256 x 256 tile is not hidden by
+// its matrix products, and a formula with a reciprocal too took 45 us of 200 for 65,536 x 1,024 -> 1,024.
 __device__ __forceinline__ float gelu(float v)
 {
-    const float u = fabsf(v) * 0.70710678118654752440f;
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, u, 1.0f));
-    float q = fmaf(t, 1.061405429f, -1.453152027f);
-    q = fmaf(t, q, 1.421413741f);
-    q = fmaf(t, q, -0.284496736f);
-    q = fmaf(t, q, 0.254829592f);
-    const float half_erfc = 0.5f * t * q * __builtin_amdgcn_exp2f(u * u * -1.44269504088896340736f);
-    return v * (v < 0.0f ? half_erfc : 1.0f - half_erfc);
+    const float a = fabsf(v);
+    float q = -3.5220297e-07f;
+    q = fmaf(q, a, 5.6110379e-06f);
+    q = fmaf(q, a, -1.72344253e-06f);
+    q = fmaf(q, a, -0.000653760426f);
+    q = fmaf(q, a, 0.00784936733f);
+    q = fmaf(q, a, -0.0531285442f);
+    q = fmaf(q, a, -0.458965724f);
+    q = fmaf(q, a, -1.15113954f);
+    q = fmaf(q, a, -0.999999219f);
+    const float h = __builtin_amdgcn_exp2f(q);
+    return fmaf(-fminf(a, 100.0f), h, fmaxf(v, 0.0f));  // infinity times 0 would be NaN; a NaN is in h
 }
 
 // Calls f with the epilogue's activation (MLP_EPI_*), FP32 to FP32; NaN stays NaN.  The choice is made once for a
@@ -123,15 +129,25 @@ __device__ __forceinline__ int tiles_of(const int32_t *offsets, int experts, int
     return end > begin ? (end - begin - 1) / bn + 1 : 0;
 }
 
+// Inclusive sum over the wave: within rows of 16 lanes, then row 0 into row 1 and 2 into 3, then the first half into
+// the second.
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast 31 into rows 2 and 3
+    return v;
+}
+
 __device__ __forceinline__ int total_tiles(const int32_t *offsets, int experts, int rows, int bn)
 {
     int sum = 0, b, e;
     for (int base = 0; base < experts; base += 64)
         sum += tiles_of(offsets, experts, rows, bn, base + (threadIdx.x & 63), b, e);
-#pragma unroll
-    for (int d = 32; d; d >>= 1)
-        sum += __shfl_xor(sum, d);
-    return __builtin_amdgcn_readfirstlane(sum);
+    return __builtin_amdgcn_readlane(wave_scan(sum), 63);
 }
 
 __device__ __forceinline__ bool find_tile(const int32_t *offsets, int experts, int rows, int bn, int tile, RowTile &out)
@@ -141,23 +157,17 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int experts, i
     for (int base = 0; base < experts; base += 64) {
         int begin, end;
         const int count = tiles_of(offsets, experts, rows, bn, base + lane, begin, end);
-        int upto = count;  // inclusive scan
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(upto, d);
-            upto += lane >= d ? v : 0;
-        }
+        const int upto = wave_scan(count);
         const int mine = tile - before - (upto - count);  // this tile within the lane's expert
         const unsigned long long hit = __ballot(mine >= 0 && mine < count);
         if (hit) {
             const int src = __ffsll((unsigned long long)hit) - 1;
-            const int r0 = begin + mine * bn;  // valid in lane src
             out.expert = base + src;
-            out.row0 = __builtin_amdgcn_readfirstlane(__shfl(r0, src));
-            out.row1 = min(out.row0 + bn, __builtin_amdgcn_readfirstlane(__shfl(end, src)));
+            out.row0 = __builtin_amdgcn_readlane(begin + mine * bn, src);
+            out.row1 = min(out.row0 + bn, __builtin_amdgcn_readlane(end, src));
             return true;
         }
-        before += __builtin_amdgcn_readfirstlane(__shfl(upto, 63));
+        before += __builtin_amdgcn_readlane(upto, 63);
     }
     return false;
 }
@@ -266,30 +276,43 @@ struct __attribute__((packed, aligned(2))) Float8 {
     float v[8];
 };
 
-// The epilogue of one wave: MT x NT MFMA tiles whose first weight row is tile row r0 and first row `row`.
-// One 32 x 32 tile of outputs at a time: the activation and the gate on the sums as they lie, then through 4 KB of
-// LDS of the wave's own (no barrier: one wave writes and reads it) into rows (FP32; chunk k of row n at
-// n * 128 + 16 (k ^ ((n / 2) % 8))), from which a lane takes 8 outputs, adds the residual, rounds once and
-// stores.  The residual is requested kAhead tiles ahead: its latency would otherwise stand once per tile.
+// The epilogue of one wave: MT x NT MFMA tiles whose first weight row is tile row r0 and first row `row` (the same
+// in all lanes).  One 32 x 32 tile of outputs at a time: the activation and the gate on the sums as they lie, then
+// through 4 KB of LDS of the wave's own (no barrier: one wave writes and reads it) into rows, from which a lane takes
+// 8 outputs and stores them at once.  Without a residual the outputs are rounded before LDS (chunk k of 8 bytes of row
+// n at n * 64 + 8 (k ^ 2 ((n / 4) % 4))); with one, or in FP32, after it and after the addition (chunk k of 16 bytes at
+// n * 128 + 16 (k ^ ((n / 2) % 8))).  The residual is requested kAhead tiles ahead: its latency would otherwise stand
+// once per tile.  Addresses are a base per tile plus 32 bits per lane (262,144 rows 64 -> 64: 20.4 -> 18.7 us with both).
 template <class T, bool GATED, int MT, int NT>
 __device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][NT], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
 {
     typedef typename Vec8<T>::type V8;
+    typedef T V4 __attribute__((ext_vector_type(4)));
     struct __attribute__((packed, aligned(2))) Half8 {
         V8 v;
     };
     const int lane = threadIdx.x & 63, g = lane >> 5, n = lane & 31;
     constexpr int MO = GATED ? MT / 2 : MT, TILES = MO * NT, kAhead = TILES < 4 ? TILES : 4;
+    const int first = o0 + (GATED ? r0 / 2 : r0);            // output
+    const int rows = (int)(row1 - row < 32 * NT ? row1 - row : 32 * NT);  // may be 0 or less
+    const int outs = p.out - first;
     const int oc = 8 * (lane & 3), rl = lane >> 2;  // this lane's outputs and (of 16 at a time) row
-    auto out_of = [&](int t) { return o0 + (GATED ? r0 / 2 : r0) + 32 * (t % MO) + oc; };
-    auto row_of = [&](int t, int i) { return row + 32 * (t / MO) + 16 * i + rl; };
     const bool half_res = p.residual && !p.y_fp32;
+    T *const y16 = (T *)p.y + row * p.ldy + first;
+    float *const y32 = (float *)p.y + row * p.ldy + first;
+    const T *const r16 = (const T *)p.residual + row * p.ldr + first;
+    const float *const r32 = (const float *)p.residual + row * p.ldr + first;
+    const int ldy = (int)p.ldy, ldr = (int)p.ldr;  // below 2^25
+    // this lane's offset in rows 16 i + rl of a tile; tile t begins at row 32 (t / MO), output 32 (t % MO)
+    const unsigned y_at[2] = {(unsigned)(rl * ldy + oc), (unsigned)((16 + rl) * ldy + oc)};
+    const unsigned r_at[2] = {(unsigned)(rl * ldr + oc), (unsigned)((16 + rl) * ldr + oc)};
     Half8 res[TILES][2];
     auto fetch = [&](int t) {
+        const T *const base = r16 + (int64_t)(32 * (t / MO)) * ldr + 32 * (t % MO);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (row_of(t, i) < row1 && out_of(t) + 8 <= p.out)
-                res[t][i] = *(const Half8 *)((const T *)p.residual + row_of(t, i) * p.ldr + out_of(t));
+            if (32 * (t / MO) + 16 * i + rl < rows && 32 * (t % MO) + oc + 8 <= outs)
+                res[t][i] = *(const Half8 *)(base + r_at[i]);
     };
     if (half_res)
 #pragma unroll
@@ -298,6 +321,8 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][N
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
         const int mt = (t % MO) * (GATED ? 2 : 1), nt = t / MO;
+        if (32 * nt >= rows || 32 * (t % MO) >= outs)
+            continue;
         f16x z = acc[mt][nt];
         with_activation(p.act, [&](auto act) {
 #pragma unroll
@@ -306,28 +331,53 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][N
         });
         if constexpr (GATED)
             z *= acc[mt + 1][nt];
+        const int left = outs - 32 * (t % MO) - oc;  // outputs from this lane's first on
+        const int64_t y_tile = (int64_t)(32 * nt) * ldy + 32 * (t % MO), r_tile = (int64_t)(32 * nt) * ldr + 32 * (t % MO);
+        if (!p.residual && !p.y_fp32) {
+            const int ws = 2 * ((n >> 2) & 3);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f4 v = {z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
+                *(V4 *)(ob + n * 64 + 8 * ((2 * q + g) ^ ws)) = __builtin_convertvector(v, V4);  // nearest even
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int rt = 16 * i + rl;
+                const u4 v = *(const u4 *)(ob + rt * 64 + 8 * ((oc / 4) ^ (2 * ((rt >> 2) & 3))));
+                if (32 * nt + rt >= rows || left <= 0)
+                    continue;
+                T *const y = y16 + y_tile + y_at[i];
+                if (left >= 8) {
+                    ((Unaligned16 *)y)->v = v;
+                } else {  // the last outputs of a width that is no multiple of 8
+#pragma unroll
+                    for (int j = 0; j < 7; ++j)
+                        if (j < left)
+                            y[j] = __builtin_bit_cast(V8, v)[j];
+                }
+            }
+            continue;
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             *(f4 *)(ob + n * 128 + 16 * ((2 * q + g) ^ ((n >> 1) & 7))) = f4{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
         if (half_res && t + kAhead < TILES)
             fetch(t + kAhead);
         __builtin_amdgcn_sched_barrier(0);
-        const int o = out_of(t);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int rt = 16 * i + rl;
-            const int64_t yr = row_of(t, i);
-            if (yr >= row1 || o >= p.out)
+            if (32 * nt + rt >= rows || left <= 0)
                 continue;
             const uint8_t *lr = ob + rt * 128;
             const int sw = (rt >> 1) & 7;
-            const int64_t at = yr * p.ldy + o;
-            if (o + 8 <= p.out) {
+            if (left >= 8) {
                 const f4 lo = *(const f4 *)(lr + 16 * ((oc / 4) ^ sw)), hi = *(const f4 *)(lr + 16 * ((oc / 4 + 1) ^ sw));
                 f8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
                 if (p.y_fp32) {
                     if (p.residual) {
-                        const Float8 r = *(const Float8 *)((const float *)p.residual + yr * p.ldr + o);
+                        const Float8 r = *(const Float8 *)(r32 + r_tile + r_at[i]);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             v[j] += r.v[j];
@@ -336,25 +386,22 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][N
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         y.v[j] = v[j];
-                    *(Float8 *)((float *)p.y + at) = y;
+                    *(Float8 *)(y32 + y_tile + y_at[i]) = y;
                 } else {
-                    if (half_res)
-                        v += __builtin_convertvector(res[t][i].v, f8);
                     Half8 y;
-                    y.v = __builtin_convertvector(v, V8);  // nearest even
-                    *(Half8 *)((T *)p.y + at) = y;
+                    y.v = __builtin_convertvector(v + __builtin_convertvector(res[t][i].v, f8), V8);  // nearest even
+                    *(Half8 *)(y16 + y_tile + y_at[i]) = y;
                 }
-            } else {  // the last outputs of a width that is no multiple of 8
+            } else {
 #pragma unroll 1
-                for (int j = 0; o + j < p.out; ++j) {
-                    float z = *(const float *)(lr + 16 * ((oc / 4 + j / 4) ^ sw) + 4 * (j % 4));
-                    const int64_t ar = yr * p.ldr + o + j;
+                for (int j = 0; j < left; ++j) {
+                    float v = *(const float *)(lr + 16 * ((oc / 4 + j / 4) ^ sw) + 4 * (j % 4));
                     if (p.residual)
-                        z += p.y_fp32 ? ((const float *)p.residual)[ar] : (float)((const T *)p.residual)[ar];
+                        v += p.y_fp32 ? r32[r_tile + r_at[i] + j] : (float)r16[r_tile + r_at[i] + j];
                     if (p.y_fp32)
-                        ((float *)p.y)[at + j] = z;
+                        y32[y_tile + y_at[i] + j] = v;
                     else
-                        ((T *)p.y)[at + j] = (T)z;
+                        y16[y_tile + y_at[i] + j] = (T)v;
                 }
             }
         }
@@ -362,7 +409,8 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][N
 }
 
 // WM x WN waves, each MT x NT MFMA tiles of 32 weight rows x 32 rows, K advancing 64 per stage through two
-// stages of LDS: each thread loads its chunks of stage s + 1 into registers while stage s is multiplied.
+// stages of LDS: each thread loads its chunks of stage s + 1 into registers while stage s is multiplied (requesting
+// s + 2 as well gained nothing: 5,003 x 1,001 -> 777 38 against 34 us).
 // 128 bytes a row; chunk c (16 bytes) of row r sits at slot c ^ ((r / 2) % 8): the 16 rows that one 256-byte
 // LDS cycle of a fragment read serves fall in 16 different slots.
 template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int WPE>
@@ -381,7 +429,7 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
     Tile<T> tile;
     if (!take_tile<T, GROUPED, GATED, (GATED ? BM / 2 : BM), BN>(p, tile))
         return;  // whole workgroup, before any barrier
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;
     const int g = lane >> 5, n = lane & 31;
     const int c = tid % 8, r_in = tid / 8;
@@ -627,6 +675,74 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
     epilogue<T, GATED>(p, acc, l0 + wave * 4096, tile.o0, wm * MT * 32, tile.row0 + wn * NT * 32, tile.row1);
 }
 
+// Narrow layers over many rows, up to 64 weight rows and 64 columns: bound by the bytes of x and y.  A wave
+// keeps the whole weight matrix and the bias in registers, as MFMA operands, and takes kRounds tiles of 32 rows, each
+// straight from memory as the other operand (lane (g, n) loads the 16 bytes of row n at columns 16 kb + 8 g), two tiles
+// ahead.  No barrier anywhere; LDS only turns the outputs into rows.
+template <class T, bool GROUPED, bool GATED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void product_narrow(ProductArgs p)
+{
+    typedef typename Vec8<T>::type V8;
+    constexpr int MT = 2, KB = 4, BO = GATED ? 16 * MT : 32 * MT, kRounds = 4, kAhead = 2, BN = 4 * 32 * kRounds;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[4 * 4096];
+    Tile<T> tile;
+    if (!take_tile<T, GROUPED, GATED, BO, BN>(p, tile))
+        return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 5, n = lane & 31;
+    const int64_t first = tile.row0 + wave * (32 * kRounds);
+    if (first >= tile.row1)
+        return;
+
+    int64_t rows[kRounds];  // of x: known before the first is needed, the routed ones are looked up
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+        rows[i] = input_row<GROUPED>(p, first + 32 * i + n, tile.row1);
+    V8 a[MT][KB];
+    f16x bias[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const T *w = tile.w + (int64_t)weight_row<GATED>(tile.o0, 32 * mt + n, p.out) * p.ldw;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+            a[mt][kb] = __builtin_bit_cast(V8, load16_tail(w, 16 * kb + 8 * g, p.in));
+        bias[mt] = bias_tile<T, GATED>(tile.bias, tile.o0, 32 * mt, g, p.out);
+    }
+    const bool whole = p.in == 16 * KB;
+    u4 b[kRounds][KB];
+    auto load = [&](int i) {
+        const T *x = (const T *)p.x + rows[i] * p.ldx;
+        if (whole) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                b[i][kb] = load16(x + 16 * kb + 8 * g);
+        } else {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                b[i][kb] = load16_tail(x, 16 * kb + 8 * g, p.in);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        load(i);
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int64_t row = first + 32 * i;
+        if (row >= tile.row1)
+            break;
+        if (i + kAhead < kRounds)
+            load(i + kAhead);
+        f16x acc[MT][1];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            acc[mt][0] = bias[mt];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                acc[mt][0] = mfma32(a[mt][kb], __builtin_bit_cast(V8, b[i][kb]), acc[mt][0]);
+        }
+        epilogue<T, GATED>(p, acc, lds + wave * 4096, tile.o0, 0, row, tile.row1);
+    }
+}
+
 // Few rows: a workgroup of NW waves (blockDim / 64, at most 16) takes 16 * MA weight rows and up to 16 rows of
 // x, and its waves share K: each multiplies a run of columns straight from memory (16 x 16 x 32 MFMA, weights = A,
 // x = B; lane (g, n) loads the 16 bytes of row n at columns 8 g), kDepth steps requested at once, and the waves'
@@ -762,12 +878,13 @@ __global__ __launch_bounds__(256) void combine_rows(CombineArgs c)
 // ---- which kernel ---------------------------------------------------------------------------------
 
 // kBig 256 weight rows x 256 rows, kMid 128 x 128, kSmall 128 x 64 (all three straight into LDS), kTile 64 x 128 through
-// registers, kFew 16 x 16, kFewWide 32 x 16.
-enum Form { kBig, kMid, kSmall, kTile, kFew, kFewWide };
+// registers, kFew 16 x 16, kFewWide 32 x 16, kNarrow 64 x 512 (K up to 64).
+enum Form { kBig, kMid, kSmall, kTile, kFew, kFewWide, kNarrow };
 struct Shape {
     int bm, bn, threads;
 };
-constexpr Shape kShapes[] = {{256, 256, 512}, {128, 128, 256}, {128, 64, 256}, {64, 128, 256}, {16, 16, 1024}, {32, 16, 1024}};
+constexpr Shape kShapes[] = {{256, 256, 512}, {128, 128, 256}, {128, 64, 256}, {64, 128, 256}, {16, 16, 1024}, {32, 16, 1024},
+                             {64, 512, 256}};
 
 // Row tiles of bn rows there can be at most.
 int64_t row_tiles(const ProductArgs &p, bool grouped, int bn)
@@ -783,17 +900,19 @@ int64_t tiles_most(const ProductArgs &p, bool gated, bool grouped, Form f)
     return f == kFew || f == kFewWide ? tiles : (tiles + 7) / 8 * 8;  // the XCDs' runs are equally long
 }
 
-// Chosen by how many tiles there are for 256 CUs (MI355X), us measured in BF16:
-//   - fewer than 1,024 tiles of 16 x 16: kFew, whose waves share K (1 x 1,024 -> 1,024: 3 against 11 with 128 x 64
+// Chosen by how many tiles there are for 256 CUs (MI355X); us measured in BF16, narrow layers in FP16:
+//   - fewer than 1,024 tiles of 16 x 16: kFew, whose waves share K (1 x 1,024 -> 1,024: 4.4 against 11 with 128 x 64
 //     tiles; 64 x 4,096 -> 1,024: 10 against 41; 300 x 1,024 -> 1,024, 1,216 tiles: 13 both), from 512 on 32 weight
 //     rows at a time (32 x 4,096 -> 4,096: 14 against 17);
-//   - at most 64 weight rows, or rows that are not 16-byte aligned (which kTile alone takes): kTile (262,144 rows
-//     64 -> 64: 19 against 30 with 128 x 128);
-//   - more than 512 tiles of 128 x 128, two per CU: kBig (8,192 x 4,096 -> 4,096: 232 against 281; 65,536 x 1,024 ->
-//     1,024: 146 against 191), 192 and more: kMid (5,003 x 1,008 -> 776: 23 against 28 with kSmall; 2,048^3: 27
-//     against 48 with kBig), else kSmall (512 x 1,024 -> 4,096: 12 against 16).
+//   - at most 64 weight rows: kTile (262,144 rows 64 -> 64: 19 against 32 with 128 x 128), or kNarrow from 1,024 of its
+//     tiles on (1,048,576 rows 32 -> 32: 59 against 106; at 262,144 rows 64 -> 64 both 19, by expert 29 against 26);
+//   - rows that are not 16-byte aligned: kTile, which takes them;
+//   - more than 512 tiles of 128 x 128, two per CU: kBig (8,192 x 4,096 -> 4,096: 225 against 281; 65,536 x 1,024 ->
+//     1,024: 143 against 191; 262,144 x 64 -> 256: 63 against 67), but kMid where half of each would be empty
+//     (1,048,576 x 64 -> 128: 133 against 207); from 192 on: kMid (5,003 x 1,008 -> 776: 23 against 28 with kSmall;
+//     2,048^3: 27 against 48 with kBig), else kSmall (512 x 1,024 -> 4,096: 12 against 16).
 // The experts' rows fill their last tiles by half: kBig and kMid only from 192 and 96 rows per expert on (2,048
-// assignments over 32 experts, 1,024 -> 2 x 1,024: 35 with kSmall, 46 with kMid; 32,768: 363 with kMid, 310 with kBig).
+// assignments over 32 experts, 1,024 -> 2 x 1,024: 35 with kSmall, 46 with kMid; 32,768: 363 with kMid, 302 with kBig).
 Form choose_form(const ProductArgs &p, bool gated, bool grouped)
 {
     const bool a16 = p.ldx % 8 == 0 && p.ldw % 8 == 0 && p.w_stride % 8 == 0 && (((uintptr_t)p.x | (uintptr_t)p.w) & 15) == 0;
@@ -801,11 +920,13 @@ Form choose_form(const ProductArgs &p, bool gated, bool grouped)
     const int64_t few = row_tiles(p, grouped, 16) * ((wide + 15) / 16);
     if (few < 1024)
         return gated || few >= 512 ? kFewWide : kFew;
+    if (wide <= 64 && p.in <= 64 && row_tiles(p, false, 512) >= 1024)
+        return kNarrow;
     if (!a16 || wide <= 64)
         return kTile;
     const int64_t used = grouped ? (p.rows < p.experts ? p.rows : p.experts) : 1, each = p.rows / used;
     const int64_t mid = (p.rows / 128 + (used + 1) / 2) * ((wide + 127) / 128);
-    if (mid > 512 && (!grouped || each >= 192))
+    if (mid > 512 && wide > 128 && (!grouped || each >= 192))
         return kBig;
     return mid >= 192 && (!grouped || each >= 96) ? kMid : kSmall;
 }
@@ -827,6 +948,9 @@ hipError_t launch(const ProductArgs &p, hipStream_t stream)
         break;
     case kTile:
         hipLaunchKernelGGL((product_tile<T, GROUPED, GATED, 1, 4, 2, 1, 3>), grid, block, 0, stream, p);
+        break;
+    case kNarrow:
+        hipLaunchKernelGGL((product_narrow<T, GROUPED, GATED>), grid, block, 0, stream, p);
         break;
     default:
         // 64 columns or more for each of up to 16 waves

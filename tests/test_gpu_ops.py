@@ -61,7 +61,8 @@ def test_linear(rows, k, n, dtype):
 LARGE = [(5000, 200, 1800, False), (5000, 40, 1801, False), (4864, 128, 2048, False), (2600, 264, 1700, True),
          (2500, 72, 1500, False), (2048, 64, 2048, False), (1300, 200, 1100, True), (600, 136, 700, False), (640, 192, 640, False),
          (300, 64, 650, True), (9000, 72, 64, False), (9001, 33, 50, False), (4000, 64, 32, True), (700, 101, 903, False),
-         (513, 77, 455, True), (150, 1040, 1000, False)]
+         (513, 77, 455, True), (150, 1040, 1000, False), (524300, 24, 20, False), (524289, 33, 16, True),
+         (20000, 64, 128, False)]
 
 
 @pytest.mark.parametrize("dtype", HALF)
@@ -293,7 +294,7 @@ def test_dispatch_large():
 
 EXPERT_SIZES = [(1, 1, 1, 8, 8), (1, 2, 3, 40, 24), (3, 4, 9, 33, 17), (8, 4, 32, 128, 96), (64, 2, 4, 64, 64), (37, 3, 5, 200, 130),
                 (300, 1, 16, 64, 64), (500, 2, 3, 96, 264), (260, 6, 70, 72, 40), (20, 2, 200, 16, 16), (3000, 2, 4, 72, 1200),
-                (900, 2, 5, 136, 700), (4000, 1, 16, 64, 64), (1000, 3, 20, 40, 264), (700, 2, 6, 33, 300)]
+                (900, 2, 5, 136, 700), (4000, 1, 16, 64, 64), (1000, 3, 20, 40, 264), (700, 2, 6, 33, 300), (530000, 1, 5, 40, 12)]
 
 
 def routed(g, tokens, k, experts, drop=True):

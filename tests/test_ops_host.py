@@ -90,6 +90,8 @@ REFUSED = [
     ("mlp_linear", dict(bias=3 * P + 8), "overlaps"), ("mlp_linear", dict(residual=3 * P + 16, ldr=8), "residual"),
     ("mlp_linear", dict(residual=3 * P, ldr=16), "residual"), ("mlp_linear", dict(residual=4 * P, ldr=7), "stride"),
     ("mlp_linear", dict(x=3 * P + 14, ldx=16, ldy=16), "overlaps"),  # one column too many beside y
+    ("mlp_linear", dict(ldy=(1 << 24) + 1), "larger"), ("mlp_linear", dict(residual=1 << 40, ldr=(1 << 24) + 1), "larger"),
+    ("mlp_expert_linear", dict(ldy=(1 << 24) + 1, y=1 << 40), "larger"),
     ("mlp_route", dict(tokens=-1), "tokens"), ("mlp_route", dict(experts=0), "experts"),
     ("mlp_route", dict(experts=1025), "experts"), ("mlp_route", dict(k=0), "k must"), ("mlp_route", dict(k=9), "k must"),
     ("mlp_route", dict(experts=64, ld=64, k=33), "k must"), ("mlp_route", dict(dtype=3), "dtype"),
