@@ -69,12 +69,8 @@ typedef struct mlp_linear_args {
     int64_t ldr;
     void *y; /* [rows][out_width]; overlaps no input but such a residual                        */
     int64_t ldy;
-    void *workspace; /* mlp_linear_workspace bytes, 16-byte aligned (NULL where that is 0)          */
-    uint64_t workspace_bytes;
 } mlp_linear_args;
 
-/* Bytes of workspace mlp_linear needs for these sizes and types (pointers are not looked at). */
-int mlp_linear_workspace(const mlp_linear_args *args, uint64_t *bytes);
 /* Errors: INVALID_ARGUMENT, UNSUPPORTED (more tiles than one launch holds), HIP. */
 int mlp_linear(const mlp_linear_args *args, void *stream);
 
@@ -126,10 +122,11 @@ typedef struct mlp_dispatch_args {
     int32_t *offsets;     /* [experts + 1]                                                            */
     int32_t *slots;       /* [tokens * k]: the assignment in each slot; -1 from offsets[experts] on   */
     int32_t *places;      /* [tokens * k]: the slot of each assignment, -1 if dropped                 */
-    void *workspace;
+    void *workspace; /* mlp_dispatch_workspace bytes, 16-byte aligned (NULL where that is 0)         */
     uint64_t workspace_bytes;
 } mlp_dispatch_args;
 
+/* Bytes of workspace mlp_dispatch needs for these sizes (pointers are not looked at). */
 int mlp_dispatch_workspace(const mlp_dispatch_args *args, uint64_t *bytes);
 int mlp_dispatch(const mlp_dispatch_args *args, void *stream);
 
@@ -163,10 +160,11 @@ typedef struct mlp_expert_linear_args {
     int64_t ldr;
     void *y; /* [tokens * k or tokens][out_width]                                               */
     int64_t ldy;
-    void *workspace;
+    void *workspace; /* mlp_expert_linear_workspace bytes, 16-byte aligned (NULL where that is 0)    */
     uint64_t workspace_bytes;
 } mlp_expert_linear_args;
 
+/* Bytes of workspace mlp_expert_linear needs for these sizes: the FP32 outputs by slot where it combines. */
 int mlp_expert_linear_workspace(const mlp_expert_linear_args *args, uint64_t *bytes);
 int mlp_expert_linear(const mlp_expert_linear_args *args, void *stream);
 

@@ -136,8 +136,6 @@ int check_linear(const mlp_linear_args *a)
     return check_layer(a->in_width, a->out_width, a->dtype, a->out_dtype, a->act, a->gated);
 }
 
-uint64_t linear_need(const mlp_linear_args *) { return 0; }
-
 int check_expert_linear(const mlp_expert_linear_args *a)
 {
     if (!a)
@@ -173,15 +171,6 @@ uint64_t dispatch_need(const mlp_dispatch_args *a)
 
 extern "C" {
 
-int mlp_linear_workspace(const mlp_linear_args *a, uint64_t *bytes)
-{
-    if (!bytes)
-        return fail(MLP_ERR_INVALID_ARGUMENT, "bytes is NULL");
-    MLP_TRY(check_linear(a));
-    *bytes = linear_need(a);
-    return ok();
-}
-
 int mlp_linear(const mlp_linear_args *a, void *stream)
 {
     MLP_TRY(check_linear(a));
@@ -206,7 +195,6 @@ int mlp_linear(const mlp_linear_args *a, void *stream)
             overlap(y, span(a->residual, a->rows, a->out_width, a->ldr, out_size)))
             return fail(MLP_ERR_INVALID_ARGUMENT, "y overlaps residual without being it");
     }
-    MLP_TRY(check_workspace(a->workspace, a->workspace_bytes, linear_need(a)));
     mlpk::ProductArgs p{};
     p.x = a->x;
     p.ldx = a->ldx;

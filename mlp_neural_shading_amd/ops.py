@@ -28,8 +28,8 @@ MLP_OPS_MAX_WIDTH = 1 << 20
 MLP_OPS_MAX_EXPERTS = 1024
 MLP_OPS_MAX_TOPK = 32
 
-EXPORTED = ("mlp_linear_workspace", "mlp_linear", "mlp_route", "mlp_dispatch_workspace", "mlp_dispatch",
-            "mlp_expert_linear_workspace", "mlp_expert_linear")
+EXPORTED = ("mlp_linear", "mlp_route", "mlp_dispatch_workspace", "mlp_dispatch", "mlp_expert_linear_workspace",
+            "mlp_expert_linear")
 
 _p, _i32, _i64, _u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
 
@@ -37,8 +37,7 @@ _p, _i32, _i64, _u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c
 class LinearArgs(ctypes.Structure):
     _fields_ = [("rows", _i64), ("in_width", _i32), ("out_width", _i32), ("dtype", _i32), ("out_dtype", _i32),
                 ("act", _i32), ("gated", _i32), ("x", _p), ("ldx", _i64), ("w", _p), ("ldw", _i64), ("bias", _p),
-                ("residual", _p), ("ldr", _i64), ("y", _p), ("ldy", _i64), ("workspace", _p),
-                ("workspace_bytes", _u64)]
+                ("residual", _p), ("ldr", _i64), ("y", _p), ("ldy", _i64)]
 
 
 class RouteArgs(ctypes.Structure):
@@ -166,6 +165,7 @@ def _out_dtype(dtype, out_dtype):
 
 
 _HALF = (torch.float16, torch.bfloat16)
+_FLOATS = tuple(DTYPES)
 
 
 def linear(x, w, bias=None, *, residual=None, act="none", gated=False, out=None, out_dtype=None):
@@ -185,7 +185,7 @@ def linear(x, w, bias=None, *, residual=None, act="none", gated=False, out=None,
     n = wide // 2 if gated else wide
     out_dtype = _out_dtype(dtype, out_dtype)
     if out is None:
-        out = torch.empty((rows, n), dtype=out_dtype, device=device)
+        out = torch.empty(rows, n, dtype=out_dtype, device=device)
         ldy = max(n, 1)
     else:
         ldy = _matrix("out", out, (out_dtype,), device, rows, n)
@@ -193,10 +193,8 @@ def linear(x, w, bias=None, *, residual=None, act="none", gated=False, out=None,
     a = LinearArgs(rows, k, n, DTYPES[dtype], DTYPES[out_dtype], _choice("act", act, ACTIVATIONS), 1 if gated else 0,
                    x.data_ptr(), ldx, w.data_ptr(), ldw,
                    None if bias is None else _vector("bias", bias, dtype, device, wide),
-                   None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy, None, 0)
-    ws = _workspace("mlp_linear_workspace", a, device)
+                   None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy)
     _call("mlp_linear", a, device)
-    del ws
     return out
 
 
@@ -207,12 +205,14 @@ def route(logits, k, *, score="softmax", bias=None, groups=1, topk_groups=None, 
     ``logits`` [tokens, experts] float32, float16 or bfloat16 with contiguous rows; ``bias`` float32 [experts]
     enters the choice only; ``groups`` of consecutive experts, of which the ``topk_groups`` with the largest sum
     of their ``group_top`` (1 or 2) best are chosen from.  -inf and NaN logits are never chosen."""
-    ld = _matrix("logits", logits, tuple(DTYPES))
+    ld = _matrix("logits", logits, _FLOATS)
     tokens, experts = logits.shape
     device = logits.device
-    index = torch.empty((tokens, max(int(k), 0)), dtype=torch.int32, device=device)
-    weight = torch.empty((tokens, max(int(k), 0)), dtype=torch.float32, device=device)
-    a = RouteArgs(tokens, experts, int(k), DTYPES[logits.dtype], _choice("score", score, SCORES), groups,
+    k = int(k)
+    room = k if 0 < k <= MLP_OPS_MAX_TOPK else 0  # others are refused below
+    index = torch.empty(tokens, room, dtype=torch.int32, device=device)
+    weight = torch.empty(tokens, room, dtype=torch.float32, device=device)
+    a = RouteArgs(tokens, experts, k, DTYPES[logits.dtype], _choice("score", score, SCORES), groups,
                   groups if topk_groups is None else topk_groups, group_top, 1 if renormalise else 0, scale,
                   logits.data_ptr(), ld, None if bias is None else _vector("bias", bias, torch.float32, device, experts),
                   index.data_ptr(), weight.data_ptr())
@@ -227,11 +227,11 @@ def dispatch(index, experts) -> Dispatch:
     if not index.is_contiguous():
         raise ValueError("index must be contiguous")
     tokens, k = index.shape
-    device, n = index.device, index.numel()
-    offsets = torch.empty(int(experts) + 1 if int(experts) >= 0 else 0, dtype=torch.int32, device=device)
+    device, n, experts = index.device, index.numel(), int(experts)
+    offsets = torch.empty(experts + 1 if 0 < experts <= MLP_OPS_MAX_EXPERTS else 0, dtype=torch.int32, device=device)
     slots = torch.empty(n, dtype=torch.int32, device=device)
     places = torch.empty(n, dtype=torch.int32, device=device)
-    a = DispatchArgs(tokens, k, int(experts), index.data_ptr(), offsets.data_ptr(), slots.data_ptr(),
+    a = DispatchArgs(tokens, k, experts, index.data_ptr(), offsets.data_ptr(), slots.data_ptr(),
                      places.data_ptr(), None, 0)
     ws = _workspace("mlp_dispatch_workspace", a, device)
     _call("mlp_dispatch", a, device)
@@ -268,7 +268,7 @@ def expert_linear(x, w, plan: Dispatch, bias=None, *, k, act="none", gated=False
     out_dtype = _out_dtype(dtype, out_dtype)
     y_rows = tokens if combine else total
     if out is None:
-        out = torch.empty((y_rows, n), dtype=out_dtype, device=device)
+        out = torch.empty(y_rows, n, dtype=out_dtype, device=device)
         ldy = max(n, 1)
     else:
         ldy = _matrix("out", out, (out_dtype,), device, y_rows, n)

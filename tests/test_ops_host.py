@@ -46,7 +46,7 @@ def test_structs_match_the_header(tmp_path):
 
 def linear_args(**over):
     a = dict(rows=4, in_width=8, out_width=8, dtype=0, out_dtype=0, act=0, gated=0, x=P, ldx=8, w=2 * P, ldw=8,
-             bias=None, residual=None, ldr=0, y=3 * P, ldy=8, workspace=None, workspace_bytes=0)
+             bias=None, residual=None, ldr=0, y=3 * P, ldy=8)
     a.update(over)
     return ops.LinearArgs(**a)
 
