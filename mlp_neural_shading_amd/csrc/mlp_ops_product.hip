@@ -524,7 +524,7 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
     epilogue<T, GATED>(p, acc, lds + wave * 4096, tile.o0, wm * MT * 32, tile.row0 + wn * NT * 32, tile.row1);
 }
 
-// The same for rows of whole 16-byte chunks: the stages go from memory into LDS directly, NS of them in flight.
+// The same for rows that are 4-byte aligned: the stages go from memory into LDS directly, NS of them in flight.
 // A stage is 64 columns, 128 bytes of every row: whole cache lines (at 32 columns each line came from L2 twice).
 // A stage's last quarter is multiplied after the barrier that frees it, while the next stage's first fragments are
 // read, so the matrix unit does not wait for LDS there.
@@ -900,35 +900,52 @@ int64_t tiles_most(const ProductArgs &p, bool gated, bool grouped, Form f)
     return f == kFew || f == kFewWide ? tiles : (tiles + 7) / 8 * 8;  // the XCDs' runs are equally long
 }
 
-// Chosen by how many tiles there are for 256 CUs (MI355X); us measured in BF16, narrow layers in FP16:
-//   - fewer than 1,024 tiles of 16 x 16: kFew, whose waves share K (1 x 1,024 -> 1,024: 4.4 against 11 with 128 x 64
+// Rounds of tiles over the chip, `at_once` of them per round; where a CU runs two, a last round that is at most half
+// full takes 0.6 of one.
+float rounds(int64_t tiles, int at_once, bool two_per_cu)
+{
+    const float whole = (float)(tiles / at_once), rest = (float)(tiles % at_once) / at_once;
+    return whole + (rest == 0.0f ? 0.0f : two_per_cu && rest <= 0.5f ? 0.6f : 1.0f);
+}
+
+// The kernel, for 256 CUs (MI355X); times in BF16, narrow layers in FP16:
+//   - fewer than 1,024 tiles of 16 x 16: kFew, whose waves share K (1 x 1,024 -> 1,024: 4.4 us against 11 with 128 x 64
 //     tiles; 64 x 4,096 -> 1,024: 10 against 41; 300 x 1,024 -> 1,024, 1,216 tiles: 13 both), from 512 on 32 weight
 //     rows at a time (32 x 4,096 -> 4,096: 14 against 17);
 //   - at most 64 weight rows: kTile (262,144 rows 64 -> 64: 19 against 32 with 128 x 128), or kNarrow from 1,024 of its
 //     tiles on (1,048,576 rows 32 -> 32: 59 against 106; at 262,144 rows 64 -> 64 both 19, by expert 29 against 26);
-//   - rows that are not 16-byte aligned: kTile, which takes them;
-//   - more than 512 tiles of 128 x 128, two per CU: kBig (8,192 x 4,096 -> 4,096: 225 against 281; 65,536 x 1,024 ->
-//     1,024: 143 against 191; 262,144 x 64 -> 256: 63 against 67), but kMid where half of each would be empty
-//     (1,048,576 x 64 -> 128: 133 against 207); from 192 on: kMid (5,003 x 1,008 -> 776: 23 against 28 with kSmall;
-//     2,048^3: 27 against 48 with kBig), else kSmall (512 x 1,024 -> 4,096: 12 against 16).
-// The experts' rows fill their last tiles by half: kBig and kMid only from 192 and 96 rows per expert on (2,048
-// assignments over 32 experts, 1,024 -> 2 x 1,024: 35 with kSmall, 46 with kMid; 32,768: 363 with kMid, 302 with kBig).
+//   - rows that are not 4-byte aligned (an odd width): kTile, which takes them;
+//   - else the one of kBig, kMid and kSmall that takes the least time by its rounds, each of so much per 1,024 columns
+//     and so much for its start and epilogue, as fitted to 65,536 x 1,024 -> 1,024 (139, 191 and 226 us),
+//     8,192 x 4,096 -> 4,096 (222, 281 and 363) and 1,048,576 x 64 -> 128 (207, 133 and 192).  It gives kSmall for
+//     512 x 1,024 -> 4,096 (11; kMid 16), kMid for 2,048^3 (27; kBig 48), kBig for 262,144 x 64 -> 256 (62; kMid 67).
+//     The experts' last tiles count as half full, and kBig and kMid are for 192 and 96 rows per expert and more: 32,768
+//     assignments over 32 experts, 2,048 -> 2 x 1,024, 297 with kBig, 363 with kMid; 2,048 assignments, 1,024 ->
+//     2 x 1,024, 33 with kSmall, 44 with kMid.
 Form choose_form(const ProductArgs &p, bool gated, bool grouped)
 {
-    const bool a16 = p.ldx % 8 == 0 && p.ldw % 8 == 0 && p.w_stride % 8 == 0 && (((uintptr_t)p.x | (uintptr_t)p.w) & 15) == 0;
+    const bool even = p.ldx % 2 == 0 && p.ldw % 2 == 0 && p.w_stride % 2 == 0 && (((uintptr_t)p.x | (uintptr_t)p.w) & 3) == 0;
     const int64_t wide = (int64_t)p.out * (gated ? 2 : 1);
     const int64_t few = row_tiles(p, grouped, 16) * ((wide + 15) / 16);
     if (few < 1024)
         return gated || few >= 512 ? kFewWide : kFew;
     if (wide <= 64 && p.in <= 64 && row_tiles(p, false, 512) >= 1024)
         return kNarrow;
-    if (!a16 || wide <= 64)
+    if (!even || wide <= 64)
         return kTile;
-    const int64_t used = grouped ? (p.rows < p.experts ? p.rows : p.experts) : 1, each = p.rows / used;
-    const int64_t mid = (p.rows / 128 + (used + 1) / 2) * ((wide + 127) / 128);
-    if (mid > 512 && wide > 128 && (!grouped || each >= 192))
+    const int64_t used = !grouped ? 0 : p.rows < p.experts ? p.rows : p.experts;
+    auto tiles = [&](Form f) {
+        const int64_t bm = kShapes[f].bm, bn = kShapes[f].bn;
+        return (grouped ? p.rows / bn + (used + 1) / 2 : (p.rows + bn - 1) / bn) * ((wide + bm - 1) / bm);
+    };
+    const float k = (float)p.in / 1024.0f;
+    const float big = rounds(tiles(kBig), 256, false) * (26.5f * k + 9.5f);
+    const float mid = rounds(tiles(kMid), 512, true) * (15.5f * k + 8.5f);
+    const float small = rounds(tiles(kSmall), 512, true) * (10.4f * k + 5.5f);
+    const int64_t each = used ? p.rows / used : INT64_MAX;  // rows per expert
+    if (each >= 192 && big <= mid && big <= small)
         return kBig;
-    return mid >= 192 && (!grouped || each >= 96) ? kMid : kSmall;
+    return each >= 96 && mid <= small ? kMid : kSmall;
 }
 
 template <class T, bool GROUPED, bool GATED>

@@ -62,7 +62,7 @@ LARGE = [(5000, 200, 1800, False), (5000, 40, 1801, False), (4864, 128, 2048, Fa
          (2500, 72, 1500, False), (2048, 64, 2048, False), (1300, 200, 1100, True), (600, 136, 700, False), (640, 192, 640, False),
          (300, 64, 650, True), (9000, 72, 64, False), (9001, 33, 50, False), (4000, 64, 32, True), (700, 101, 903, False),
          (513, 77, 455, True), (150, 1040, 1000, False), (524300, 24, 20, False), (524289, 33, 16, True),
-         (20000, 64, 128, False)]
+         (20000, 64, 128, False), (5000, 202, 1800, False), (2500, 130, 1500, True), (700, 102, 640, False)]
 
 
 @pytest.mark.parametrize("dtype", HALF)
