@@ -292,7 +292,12 @@ int mlp_dispatch(const mlp_dispatch_args *a, void *stream)
                 if (overlap(s[i], s[j]))
                     return fail(MLP_ERR_INVALID_ARGUMENT, "index, slots, places and offsets overlap");
     }
-    MLP_TRY(check_workspace(a->workspace, a->workspace_bytes, dispatch_need(a)));
+    const uint64_t need = dispatch_need(a);
+    MLP_TRY(check_workspace(a->workspace, a->workspace_bytes, need));
+    const Span ws = span(need ? a->workspace : nullptr, 1, (int64_t)need, (int64_t)need, 1);
+    if (overlap(ws, span(a->index, 1, n, n, 4)) || overlap(ws, span(a->slots, 1, n, n, 4)) ||
+        overlap(ws, span(a->places, 1, n, n, 4)) || overlap(ws, span(a->offsets, 1, a->experts + 1, a->experts + 1, 4)))
+        return fail(MLP_ERR_INVALID_ARGUMENT, "workspace overlaps another buffer");
     mlpk::DispatchArgs d{};
     d.index = a->index;
     d.offsets = a->offsets;
@@ -356,7 +361,12 @@ int mlp_expert_linear(const mlp_expert_linear_args *a, void *stream)
             overlap(y, span(a->residual, y_rows, a->out_width, a->ldr, out_size)))
             return fail(MLP_ERR_INVALID_ARGUMENT, "y overlaps residual without being it");
     }
-    MLP_TRY(check_workspace(a->workspace, a->workspace_bytes, expert_linear_need(a)));
+    const uint64_t need = expert_linear_need(a);
+    MLP_TRY(check_workspace(a->workspace, a->workspace_bytes, need));
+    const Span ws = span(need ? a->workspace : nullptr, 1, (int64_t)need, (int64_t)need, 1);
+    if (overlap(ws, y) || overlap(ws, span(a->x, x_rows, a->in_width, a->ldx, 2)) || overlap(ws, span(a->w, 1, w_cols, w_cols, 2)) ||
+        (a->residual && overlap(ws, span(a->residual, y_rows, a->out_width, a->ldr, out_size))))
+        return fail(MLP_ERR_INVALID_ARGUMENT, "workspace overlaps another buffer");
     mlpk::ProductArgs p{};
     p.x = a->x;
     p.ldx = a->ldx;

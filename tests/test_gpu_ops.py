@@ -224,6 +224,20 @@ def test_route_choices_closer_than_fp32_tells_apart():
     check_route(-logits * 2, 8, score="softmax", bias=bias)
 
 
+@pytest.mark.parametrize("experts,groups", [(64, 8), (128, 4), (256, 8), (500, 1), (512, 16), (900, 1)])
+def test_route_near_choices(experts, groups):
+    """The same for every layout of experts over lanes, and rows of which only some are near."""
+    g = gen(experts)
+    base = torch.linspace(14.0, 18.0, experts)[torch.randperm(experts, generator=g)]
+    logits = torch.where(torch.arange(37)[:, None] % 3 == 1, base, rnd(g, 37, experts, scale=2.0))
+    bias = torch.full((experts,), 0.25)
+    for k in (1, 8, 20):
+        check_route(logits, k, score="sigmoid", bias=bias, renormalise=True)
+        check_route(logits * 3, k, score="softmax", bias=bias)
+    if groups > 1:
+        check_route(logits, 6, score="sigmoid", bias=bias, groups=groups, topk_groups=groups // 2, group_top=2)
+
+
 def test_route_masks():
     """Experts masked by -inf or NaN are never chosen; rows with fewer left than k, or none, end in -1; the
     lowest finite value is a logit like any other."""
@@ -356,6 +370,47 @@ def test_expert_linear_all_rows_to_one_expert_or_none():
         plan = R.dispatch64(index, 9)
         y = ops.expert_linear(gpu(x), gpu(w), ops.Dispatch(*map(gpu, plan)), k=1, combine=True)
         R.check(y, *R.experts64(x, w, plan, 1, combine=True)[:2], t, value)
+
+
+@pytest.mark.parametrize("k", [1, 2, 5, 9])
+def test_combine_every_assignment_count(k):
+    """Odd output widths and counts of experts per token, some tokens without any, the same expert twice, and NaN in
+    the outputs of no consequence: the rows behind the last slot."""
+    g, t = gen(k), torch.float16
+    tokens, experts, k_in, n = 90, 4, 40, 37
+    index = torch.randint(-1, experts, (tokens, k), generator=g, dtype=torch.int32)
+    index[5] = -1
+    index[6] = 2
+    plan = R.dispatch64(index, experts)
+    x, w = rnd(g, tokens, k_in, dtype=t), rnd(g, experts, n, k_in, dtype=t, scale=k_in ** -0.5)
+    weight = torch.randn(tokens, k, generator=g)
+    for residual in (None, rnd(g, tokens, n)):
+        y = ops.expert_linear(gpu(x), gpu(w), ops.Dispatch(*map(gpu, plan)), k=k, combine=True, weight=gpu(weight),
+                              residual=gpu(residual), out_dtype=torch.float32)
+        want, bound, _ = R.experts64(x, w, plan, k, combine=True, weight=weight, residual=residual)
+        R.check(y, want, bound, torch.float32)
+        assert torch.equal(y[5].cpu(), torch.zeros(n) if residual is None else residual[5])
+
+
+def test_expert_linear_bad_plans_stay_in_bounds():
+    """Offsets, slots and places that no dispatch gives: clamped, the rows that are right stay right.  (Shown by
+    reading first: every index is clamped to its buffer before use.)"""
+    g, t = gen(77), torch.float16
+    x, w = rnd(g, 40, 64, dtype=t), rnd(g, 3, 32, 64, dtype=t, scale=0.125)
+    index = torch.randint(0, 3, (40, 2), generator=g, dtype=torch.int32)
+    offsets, slots, places = R.dispatch64(index, 3)
+    y = ops.expert_linear(gpu(x), gpu(w), ops.Dispatch(gpu(offsets), gpu(slots), gpu(places)), k=2)
+    far = slots.clone()
+    far[-3:] = torch.tensor([-7, 80, 2 ** 31 - 1], dtype=torch.int32)
+    bad = ops.expert_linear(gpu(x), gpu(w), ops.Dispatch(gpu(offsets), gpu(far), gpu(places)), k=2)
+    assert torch.equal(bad[:-3], y[:-3])
+    wide = offsets.clone()
+    wide[0], wide[3] = -5, 2 ** 31 - 1
+    assert torch.equal(ops.expert_linear(gpu(x), gpu(w), ops.Dispatch(gpu(wide), gpu(slots), gpu(places)), k=2), y)
+    out = places.clone()
+    out[10], out[11] = -9, 80  # token 5: both dropped
+    z = ops.expert_linear(gpu(x), gpu(w), ops.Dispatch(gpu(offsets), gpu(slots), gpu(out)), k=2, combine=True)
+    assert bool((z[5] == 0).all())
 
 
 # ---- together ----------------------------------------------------------------------------------------
