@@ -180,11 +180,19 @@ __global__ __launch_bounds__(64) void route_tokens(RouteArgs r)
 // between the token's smallest and largest above the expert's index counted down, so that every key differs and
 // equal ones go to the lower index.  The next best key below b is then the largest key - b mod 2^32: one
 // subtraction and half a maximum per expert and pick, against a comparison, a search and a removal.  Where
-// neighbours among the k + 1 best (or two groups' values) lie within the error that a key may have, and are not the
-// same logit and bias, the order is not certain, and the wave chooses once more on keys in 64 bits.  The chosen
-// scores themselves are computed in 64 bits (the softmax's sum in FP32).
+// neighbours among the k + 1 best lie within the error that a key may have, and are not the same logit and bias, the
+// order is not certain: some more are picked, one per lane, and these are ranked by their choices in 64 bits.  Where
+// even that may leave one out, or two groups' values are too near, the wave chooses once more on 64-bit keys of all
+// experts (done each time, that cost 11 us of 42).  The chosen scores themselves are computed in 64 bits (the softmax's
+// sum in FP32).  65,536 tokens x 256 experts, sigmoid, 8 groups, k = 8: 38 us, bound by the instructions of the
+// picks, groups and scores; the logits' bytes alone take 7.
 
 constexpr float kLow = -__builtin_huge_valf();
+
+// Of numbers, no NaN among them: the median of three is one instruction, fmaxf two (it quiets its operands first).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -kLow); }
+__device__ __forceinline__ float smaller(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, kLow); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
 
 // Reductions over a token's lanes, the result in all of them: rotations within a row of 16 lanes, then swaps of
 // rows and of halves.
@@ -207,7 +215,7 @@ template <int L>
 __device__ __forceinline__ float lanes_max(float v)
 {
     return __builtin_bit_cast(float, lanes_reduce<L>(__builtin_bit_cast(unsigned, v), [](unsigned a, unsigned b) {
-                                  return __builtin_bit_cast(unsigned, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+                                  return __builtin_bit_cast(unsigned, larger(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
                               }));
 }
 template <int L>
@@ -259,8 +267,6 @@ __device__ __forceinline__ void load_logits(const T *logit, int e0, int experts,
         x[v] = fmaxf(x[v], kLow);  // the maximum of a NaN and a number is the number
 }
 
-__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
-__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
 // The middle one of first >= second and v.
 __device__ __forceinline__ float middle(float first, float second, float v) { return __builtin_amdgcn_fmed3f(first, second, v); }
 __device__ __forceinline__ double middle(double first, double second, double v) { return fmax(second, fmin(first, v)); }
@@ -272,6 +278,27 @@ __device__ __forceinline__ double exp_near(double v)
     const double n = rint(v * 1.4426950408889634);
     const double r = fma(n, -0.6931471805599453, v);
     double q = 1.0 / 40320;
+    q = fma(q, r, 1.0 / 5040);
+    q = fma(q, r, 1.0 / 720);
+    q = fma(q, r, 1.0 / 120);
+    q = fma(q, r, 1.0 / 24);
+    q = fma(q, r, 1.0 / 6);
+    q = fma(q, r, 0.5);
+    q = fma(q, r, 1.0);
+    q = fma(q, r, 1.0);
+    return ldexp(q, (int)n);
+}
+// exp to a few parts of 2^-52, for v <= 0: degree 13.
+__device__ __forceinline__ double exp_exact(double v)
+{
+    const double n = rint(fmax(v, -800.0) * 1.4426950408889634);
+    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, fmax(v, -800.0)));  // ln 2 in two parts
+    double q = 1.0 / 6227020800;
+    q = fma(q, r, 1.0 / 479001600);
+    q = fma(q, r, 1.0 / 39916800);
+    q = fma(q, r, 1.0 / 3628800);
+    q = fma(q, r, 1.0 / 362880);
+    q = fma(q, r, 1.0 / 40320);
     q = fma(q, r, 1.0 / 5040);
     q = fma(q, r, 1.0 / 720);
     q = fma(q, r, 1.0 / 120);
@@ -311,10 +338,25 @@ __device__ __forceinline__ void mask_groups(const RouteArgs &r, K (&key)[VPL], K
     }
     const K value = r.group_top == 2 && second > none ? first + second : first;
     int better = 0;  // groups before this one
-    for (int d = lanes; d < L; d += lanes) {
-        const int at = (me + d) & (L - 1);  // a lane of the group d / lanes further
-        const K other = __shfl(value, row + at);
-        better += at < me ? other >= value : other > value;
+    if constexpr (L == 16 && sizeof(K) == 4) {
+        // By rotations: every group's first lane offers its value to the 15 others, and a lane that is not the first
+        // meets that of its own group too.
+        const float offer = me % lanes ? kLow : (float)value;
+#define MLP_RANK(n)                                                                                            \
+    {                                                                                                          \
+        const float o = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, offer), 0x120 + n, 0xf, 0xf, true)); \
+        better += me >= n ? o >= value : o > value; /* from lane me - n, or me - n + 16 */                     \
+    }
+        MLP_RANK(1) MLP_RANK(2) MLP_RANK(3) MLP_RANK(4) MLP_RANK(5) MLP_RANK(6) MLP_RANK(7) MLP_RANK(8)
+        MLP_RANK(9) MLP_RANK(10) MLP_RANK(11) MLP_RANK(12) MLP_RANK(13) MLP_RANK(14) MLP_RANK(15)
+#undef MLP_RANK
+        better -= me % lanes ? 1 : 0;
+    } else {
+        for (int d = lanes; d < L; d += lanes) {
+            const int at = (me + d) & (L - 1);  // a lane of the group d / lanes further
+            const K other = __shfl(value, row + at);
+            better += at < me ? other >= value : other > value;
+        }
     }
     const bool out = better >= r.topk_groups || !(value > none);
     if (near > 0) {  // FP32: the worst group taken and the best one left
@@ -393,7 +435,7 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &r, const T *logit
 template <class T, int L, int VPL>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void route_lanes(RouteArgs r)
 {
-    const int lane = threadIdx.x & 63, me = lane & (L - 1), e0 = me * VPL;
+    const int lane = threadIdx.x & 63, me = lane & (L - 1), row = lane - me, e0 = me * VPL;
     constexpr unsigned kIndex = L * VPL - 1;             // the bits of the index
     // Places for the keys, as many as FP32 counts and 31 bits hold; 0 for masked ones.
     constexpr unsigned kPlaces = L * VPL <= 256 ? 1u << 23 : 1u << 22;
@@ -417,6 +459,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
         for (int v = 0; v < VPL; ++v)
             bias[v] = r.bias[e0 + v < r.experts ? e0 + v : r.experts - 1];
     }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+        bias[v] = fmaxf(bias[v], kLow);  // a NaN masks
     // One round of tokens per wave: in a loop over rounds, the compiler moves the constants of the 64-bit exp before
     // it, and the common path spills.
     const int64_t t = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * (64 / L) + lane / L;
@@ -428,19 +473,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
     float near = 0.0f;
     if (r.sigmoid) {
         if (!by_logit) {
-            // A score is off by less than 2^-22: its argument's rounding through a slope of |x| s (1 - s) < 0.23,
-            // exp and the reciprocal.
-            near = 1.0f / (1 << 20);
+            // A score is off by less than 2^-22: its argument's roundings through a slope of |x| s (1 - s) < 0.23,
+            // a step of exp through a quarter, half a one of the sum and one of the reciprocal; two keys by 2^-21.
+            near = 1.0f / (1 << 21);
 #pragma unroll
             for (int v = 0; v < VPL; ++v) {
                 const float s = __builtin_amdgcn_rcpf(1.0f + exp_of(-key[v])) + bias[v];
-                key[v] = fmaxf(key[v] > kLow ? s : kLow, kLow);  // a NaN is masked
+                key[v] = key[v] > kLow ? s : kLow;
             }
         }
     } else {
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
-            top = fmaxf(top, key[v]);
+            top = larger(top, key[v]);
         top = lanes_max<L>(top);
         const bool infinite = top == __builtin_huge_valf();  // the others' scores are then exactly 0
         if (!by_logit || !r.renormalise || infinite) {
@@ -459,7 +504,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
 #pragma unroll
                 for (int v = 0; v < VPL; ++v) {
                     const float s = e[v] * scale + bias[v];
-                    key[v] = fmaxf(key[v] > kLow ? s : kLow, kLow);  // a NaN is masked
+                    key[v] = key[v] > kLow ? s : kLow;
                 }
             } else if (infinite) {
 #pragma unroll
@@ -475,8 +520,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
     float high = kLow, low = -kLow;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-        high = fmaxf(high, key[v]);
-        low = fminf(low, key[v] > kLow ? key[v] : -kLow);
+        high = larger(high, key[v]);
+        low = smaller(low, key[v] > kLow ? key[v] : -kLow);
     }
     high = lanes_max<L>(high);
     low = fmaxf(-lanes_max<L>(-low), high - 64.0f);  // what lies further off shares the last place
@@ -486,28 +531,82 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
     unsigned place[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-        const unsigned q = (unsigned)(fmaxf(key[v] - low, 0.0f) * step + 1.0f);
-        place[v] = key[v] > kLow ? (q * (L * VPL)) + (kIndex - (unsigned)(e0 + v)) : 0u;
+        // all of it without a branch, which the compiler would otherwise make of each
+        const unsigned q = (unsigned)(__builtin_amdgcn_fmed3f(key[v] - low, 0.0f, 1e30f) * step + 1.0f);
+        const unsigned keep = key[v] > kLow ? ~0u : 0u;
+        place[v] = (q * (L * VPL) + (kIndex - (unsigned)(e0 + v))) & keep;
     }
-    unsigned best = 0x80000000u, mine = 0u, next = 0u;
-    for (int j = 0; j <= r.k; ++j) {
-        unsigned below = place[0] - best;
+    unsigned best = 0x80000000u, picked = 0u;
+    auto pick = [&](int from, int to) {  // lane j gets the j-th best place
+        for (int j = from; j < to; ++j) {
+            unsigned below = place[0] - best;
 #pragma unroll
-        for (int v = 1; v < VPL; ++v)
-            below = max(below, place[v] - best);
-        below = lanes_max<L>(below);
-        best = best ? best + below : 0u;  // 0: none is left
-        mine = me == j ? best : mine;
-        next = me == j - 1 ? best : next;
-    }
-    int index = mine ? (int)(kIndex - (mine & kIndex)) : -1;
-    if (mine && next && me < r.k) {
-        // places are off by 1 each, and by what the keys are off
-        const float apart = (float)(mine / (L * VPL) - next / (L * VPL));
-        if (!(apart > 3.0f + step * (near + fmaxf(fabsf(high), fabsf(low)) * (1.0f / (1 << 22))))) {
-            const int after = (int)(kIndex - (next & kIndex));
-            sure = sure && logit[index] == logit[after] && (!r.bias || r.bias[index] == r.bias[after]);
+            for (int v = 1; v < VPL; ++v)
+                below = max(below, place[v] - best);
+            best += lanes_max<L>(below);
+            picked = me == j ? best : picked;
         }
+    };
+    auto valid = [&]() {  // 0, a masked key's place, is the last of a token; behind it they begin again
+        const unsigned long long ends = __ballot(picked == 0u) >> row;
+        return ends & ((2ull << me) - 1) ? 0u : picked;
+    };
+    auto expert_at = [&](unsigned place) { return place ? (int)(kIndex - (place & kIndex)) : -1; };
+    pick(0, r.k + 1);
+    const unsigned mine = valid(), next = __shfl(mine, row + ((me + 1) & (L - 1)));
+    int index = expert_at(mine);
+    // places are off by 1 each, and by what the keys are off
+    const float doubt = 3.0f + step * (near + fmaxf(fabsf(high), fabsf(low)) * (1.0f / (1 << 22)));
+    auto apart = [&](unsigned a, unsigned b) { return (float)(a / (L * VPL) - b / (L * VPL)); };
+    bool ordered = true;
+    if (mine && next && me < r.k && !(apart(mine, next) > doubt)) {
+        const int after = expert_at(next);
+        ordered = logit[index] == logit[after] && (!r.bias || r.bias[index] == r.bias[after]);
+    }
+    if (__any(!ordered) && !__any(!sure)) {
+        const int count = r.k + 8 < L - 1 ? r.k + 8 : L - 1;  // candidates
+        pick(r.k + 1, count);
+        const unsigned place_of = valid();
+        const int candidate = me < count ? expert_at(place_of) : -1;
+        const unsigned kth = __shfl(place_of, row + r.k - 1), end = __shfl(place_of, row + count - 1);
+        if (end && !(apart(kth, end) > 2.0f * doubt))
+            sure = false;  // one that was not picked may be as good
+        double exact = kNone;
+        if (candidate >= 0) {
+            const double z = (double)(float)logit[candidate], b = r.bias ? (double)r.bias[candidate] : 0.0;
+            if (r.sigmoid) {
+                const double e = exp_exact(-fabs(z));
+                exact = (z < 0.0 ? e : 1.0) / (1.0 + e) + b;
+            } else {
+                exact = z == (double)top ? 1.0 : exp_exact(z - (double)top);
+            }
+        }
+        if (!r.sigmoid) {
+            float x[VPL];
+            load_logits<T, VPL>(logit, e0, r.experts, x);
+            double sum = 0.0;
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) {
+                const double e = exp_exact((double)x[v] - (double)top);
+                sum += !(x[v] > kLow) ? 0.0 : x[v] == top ? 1.0 : e;
+            }
+            sum = lanes_sum<L>(sum);
+            if (candidate >= 0)
+                exact = exact / sum + (r.bias ? (double)r.bias[candidate] : 0.0);
+        }
+        int rank = 0;
+        for (int j = 0; j < count; ++j) {
+            const double other = __shfl(exact, row + j);
+            const int of = __shfl(candidate, row + j);
+            rank += other > exact || (other == exact && of < candidate);
+        }
+        // to the lane of its rank; those that are none all rank behind the candidates
+        const int to = candidate >= 0 ? rank : L - 1;
+        const int moved = __builtin_amdgcn_ds_permute((row + to) * 4, candidate);
+        // a lane that nobody sends to reads 0
+        const unsigned long long sent = __ballot(candidate >= 0) >> row;
+        const int held = __popcll(L < 64 ? sent & ((1ull << (L & 63)) - 1) : sent);
+        index = me < held ? moved : -1;
     }
     if (me >= r.k)
         index = -1;
