@@ -58,6 +58,7 @@ struct RouteArgs {
     float *weight;
     int64_t tokens;
     int experts, k, groups, topk_groups, group_top;
+    int lanes;  // of a group, set at the launch
     bool sigmoid, renormalise;
     float scale;
 };

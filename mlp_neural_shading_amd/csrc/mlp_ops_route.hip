@@ -174,8 +174,8 @@ __global__ __launch_bounds__(64) void route_tokens(RouteArgs r)
 
 // ---- the same, L lanes per token ------------------------------------------------------------------
 //
-// For up to L * VPL experts: lane i of a token's L = 16 or 64 lanes holds the experts VPL i .. VPL i + VPL - 1, so
-// 64 / L tokens share a wave and a group of experts is a run of whole lanes.  The choice runs on FP32 keys first
+// For up to L * VPL experts: a token has L = 16 or 64 lanes, so 64 / L tokens share a wave, and a group of experts a run
+// of r.lanes of them, a power of two (without groups, all L); lane i of a group holds its experts VPL i .. VPL i + VPL - 1.  The choice runs on FP32 keys first
 // (the logits where they give the order, else score + bias), brought to whole numbers of 31 bits: the key's place
 // between the token's smallest and largest above the expert's index counted down, so that every key differs and
 // equal ones go to the lower index.  The next best key below b is then the largest key - b mod 2^32: one
@@ -246,11 +246,26 @@ struct __attribute__((packed, aligned(2))) Packed {
     T v[N];
 };
 
-// This lane's VPL logits; -infinity for NaN and past the last expert.
-template <class T, int VPL>
-__device__ __forceinline__ void load_logits(const T *logit, int e0, int experts, float (&x)[VPL])
+// The experts of a token's lane `me`: [e0, end), none where end <= e0.
+__device__ __forceinline__ void experts_of(const RouteArgs &r, int me, int vpl, int &e0, int &end)
 {
-    if (e0 + VPL <= experts) {
+    const int g = me / r.lanes, per = r.experts / r.groups;
+    const bool grouped = r.topk_groups < r.groups;
+    e0 = grouped ? g * per + (me - g * r.lanes) * vpl : me * vpl;
+    end = grouped ? (g < r.groups ? (g + 1) * per : 0) : r.experts;
+}
+// The expert number v of lane i.
+__device__ __forceinline__ int expert_of(const RouteArgs &r, int i, int vpl, int v)
+{
+    const int g = i / r.lanes;
+    return r.topk_groups < r.groups ? g * (r.experts / r.groups) + (i - g * r.lanes) * vpl + v : i * vpl + v;
+}
+
+// This lane's logits, of the experts [e0, end); -infinity for NaN and past the last one.
+template <class T, int VPL>
+__device__ __forceinline__ void load_logits(const T *logit, int e0, int end, float (&x)[VPL])
+{
+    if (e0 + VPL <= end) {
         const Packed<T, VPL> p = *(const Packed<T, VPL> *)(logit + e0);
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
@@ -258,8 +273,8 @@ __device__ __forceinline__ void load_logits(const T *logit, int e0, int experts,
     } else {
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
-            const float z = (float)logit[e0 + v < experts ? e0 + v : experts - 1];
-            x[v] = e0 + v < experts ? z : kLow;
+            const float z = (float)logit[e0 + v < end ? e0 + v : 0];
+            x[v] = e0 + v < end ? z : kLow;
         }
     }
 #pragma unroll
@@ -323,7 +338,7 @@ __device__ __forceinline__ void mask_groups(const RouteArgs &r, K (&key)[VPL], K
 {
     const int lane = threadIdx.x & 63, me = lane & (L - 1), row = lane - me;
     const K none = -__builtin_huge_valf();
-    const int lanes = r.experts / r.groups / VPL;  // of a group: a power of two
+    const int lanes = r.lanes;  // of a group
     K first = none, second = none;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
@@ -373,9 +388,11 @@ __device__ __forceinline__ void mask_groups(const RouteArgs &r, K (&key)[VPL], K
 template <class T, int L, int VPL>
 __device__ __forceinline__ int choose_exactly(const RouteArgs &r, const T *logit)
 {
-    const int lane = threadIdx.x & 63, me = lane & (L - 1), e0 = me * VPL;
+    const int lane = threadIdx.x & 63, me = lane & (L - 1);
+    int e0, end;
+    experts_of(r, me, VPL, e0, end);
     float x[VPL];
-    load_logits<T, VPL>(logit, e0, r.experts, x);
+    load_logits<T, VPL>(logit, e0, end, x);
     double key[VPL], scale = 1.0;
     if (r.sigmoid) {
 #pragma unroll
@@ -398,7 +415,7 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &r, const T *logit
     }
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-        key[v] = key[v] * scale + (r.bias ? (double)r.bias[e0 + v < r.experts ? e0 + v : r.experts - 1] : 0.0);
+        key[v] = key[v] * scale + (r.bias ? (double)r.bias[e0 + v < end ? e0 + v : 0] : 0.0);
         key[v] = x[v] > kLow && key[v] > kNone ? key[v] : kNone;
     }
     bool unused;
@@ -435,8 +452,10 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &r, const T *logit
 template <class T, int L, int VPL>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void route_lanes(RouteArgs r)
 {
-    const int lane = threadIdx.x & 63, me = lane & (L - 1), row = lane - me, e0 = me * VPL;
-    constexpr unsigned kIndex = L * VPL - 1;             // the bits of the index
+    const int lane = threadIdx.x & 63, me = lane & (L - 1), row = lane - me;
+    int e0, last;
+    experts_of(r, me, VPL, e0, last);
+    constexpr unsigned kIndex = L * VPL - 1;             // the bits of the lane and number
     // Places for the keys, as many as FP32 counts and 31 bits hold; 0 for masked ones.
     constexpr unsigned kPlaces = L * VPL <= 256 ? 1u << 23 : 1u << 22;
     static_assert((uint64_t)kPlaces * (L * VPL) <= 1u << 31, "31 bits");
@@ -446,7 +465,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
         bias[v] = 0.0f;
-    if (r.bias && e0 + VPL <= r.experts) {
+    if (r.bias && e0 + VPL <= last) {
         struct __attribute__((packed, aligned(4))) Floats {
             float v[VPL];
         };
@@ -457,7 +476,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
     } else if (r.bias) {
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
-            bias[v] = r.bias[e0 + v < r.experts ? e0 + v : r.experts - 1];
+            bias[v] = r.bias[e0 + v < last ? e0 + v : 0];
     }
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
@@ -468,7 +487,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
     const bool live = t < r.tokens;
     const T *logit = (const T *)r.logits + (live ? t : r.tokens - 1) * r.ld;
     float key[VPL];
-    load_logits<T, VPL>(logit, e0, r.experts, key);
+    load_logits<T, VPL>(logit, e0, last, key);
     float top = kLow, total = 0.0f;  // softmax: largest logit, sum of exp(logit - top)
     float near = 0.0f;
     if (r.sigmoid) {
@@ -534,7 +553,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
         // all of it without a branch, which the compiler would otherwise make of each
         const unsigned q = (unsigned)(__builtin_amdgcn_fmed3f(key[v] - low, 0.0f, 1e30f) * step + 1.0f);
         const unsigned keep = key[v] > kLow ? ~0u : 0u;
-        place[v] = (q * (L * VPL) + (kIndex - (unsigned)(e0 + v))) & keep;
+        place[v] = (q * (L * VPL) + (kIndex - (unsigned)(me * VPL + v))) & keep;
     }
     unsigned best = 0x80000000u, picked = 0u;
     auto pick = [&](int from, int to) {  // lane j gets the j-th best place
@@ -551,7 +570,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
         const unsigned long long ends = __ballot(picked == 0u) >> row;
         return ends & ((2ull << me) - 1) ? 0u : picked;
     };
-    auto expert_at = [&](unsigned place) { return place ? (int)(kIndex - (place & kIndex)) : -1; };
+    auto expert_at = [&](unsigned place) {
+        const int at = (int)(kIndex - (place & kIndex));
+        return place ? expert_of(r, at / VPL, VPL, at % VPL) : -1;
+    };
     pick(0, r.k + 1);
     const unsigned mine = valid(), next = __shfl(mine, row + ((me + 1) & (L - 1)));
     int index = expert_at(mine);
@@ -583,7 +605,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
         }
         if (!r.sigmoid) {
             float x[VPL];
-            load_logits<T, VPL>(logit, e0, r.experts, x);
+            load_logits<T, VPL>(logit, e0, last, x);
             double sum = 0.0;
 #pragma unroll
             for (int v = 0; v < VPL; ++v) {
@@ -632,25 +654,28 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
     }
 }
 
-// Whether `lanes` lanes of vpl experts each serve this router: room for the experts and for k + 1 picks, and
-// groups of whole lanes, a power of two of them, filling the lanes in use evenly.
-bool lanes_serve(const RouteArgs &r, int lanes, int vpl)
+// Lanes per group where `lanes` lanes of vpl experts each serve this router (room for k + 1 picks, and for every
+// group's lanes), else 0.
+int lanes_per_group(const RouteArgs &r, int lanes, int vpl)
 {
-    if (r.experts > lanes * vpl || r.k >= lanes)
-        return false;
+    if (r.k >= lanes)
+        return 0;
     if (r.topk_groups == r.groups)
-        return true;
-    const int per = r.experts / r.groups;
-    return r.experts == lanes * vpl && per % vpl == 0 && (per / vpl & (per / vpl - 1)) == 0;
+        return r.experts <= lanes * vpl ? lanes : 0;
+    int each = 1;
+    while (each * vpl < r.experts / r.groups)
+        each *= 2;
+    return r.groups * each <= lanes ? each : 0;
 }
 
 template <class T, int L, int VPL>
-hipError_t launch_lanes(const RouteArgs &r, hipStream_t stream)
+hipError_t launch_lanes(const RouteArgs &r, int each, hipStream_t stream)
 {
     constexpr int64_t kMost = (int64_t)1 << 25;  // tokens per launch: a grid counts its threads in 32 bits
     hipError_t err = hipSuccess;
     for (int64_t t = 0; t < r.tokens && err == hipSuccess; t += kMost) {
         RouteArgs part = r;
+        part.lanes = each;
         part.tokens = r.tokens - t < kMost ? r.tokens - t : kMost;
         part.logits = (const T *)r.logits + t * r.ld;
         part.index += t * r.k;
@@ -667,14 +692,14 @@ hipError_t launch_route_typed(const RouteArgs &r, hipStream_t stream)
 {
     const dim3 grid((unsigned)(r.tokens < 256 * 64 ? r.tokens : 256 * 64));
     const size_t lds = (size_t)(r.experts + r.groups) * sizeof(double);
-    if (lanes_serve(r, 16, 4))
-        return launch_lanes<T, 16, 4>(r, stream);
-    if (lanes_serve(r, 16, 8))
-        return launch_lanes<T, 16, 8>(r, stream);
-    if (lanes_serve(r, 16, 16))
-        return launch_lanes<T, 16, 16>(r, stream);
-    if (lanes_serve(r, 64, 8))
-        return launch_lanes<T, 64, 8>(r, stream);
+    if (const int each = lanes_per_group(r, 16, 4))
+        return launch_lanes<T, 16, 4>(r, each, stream);
+    if (const int each = lanes_per_group(r, 16, 8))
+        return launch_lanes<T, 16, 8>(r, each, stream);
+    if (const int each = lanes_per_group(r, 16, 16))
+        return launch_lanes<T, 16, 16>(r, each, stream);
+    if (const int each = lanes_per_group(r, 64, 8))
+        return launch_lanes<T, 64, 8>(r, each, stream);
     const int vpl = (r.experts + 63) / 64;
     if (vpl <= 1)
         hipLaunchKernelGGL((route_tokens<T, 1>), grid, dim3(64), lds, stream, r);

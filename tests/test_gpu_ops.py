@@ -191,7 +191,8 @@ def test_route(tokens, experts, k, dtype):
 
 
 @pytest.mark.parametrize("experts,groups,topk_groups", [(8, 2, 1), (64, 8, 4), (256, 8, 3), (160, 5, 2), (96, 96, 7), (512, 4, 4),
-                                                        (1024, 128, 9), (12, 6, 2)])
+                                                        (1024, 128, 9), (12, 6, 2), (264, 2, 1), (10, 2, 1), (63, 3, 2),
+                                                        (160, 8, 3), (330, 6, 2), (500, 10, 4), (640, 8, 4)])
 @pytest.mark.parametrize("group_top", [1, 2])
 def test_route_groups(experts, groups, topk_groups, group_top):
     g = gen(experts + groups)
