@@ -40,7 +40,7 @@ __device__ __forceinline__ f4 mfma16(b8 a, b8 b, f4 c) { return __builtin_amdgcn
 // a polynomial of degree 8, fitted to log2 h on [0, 5.5] by weighted least squares, the weights moved until the error
 // is level: h is off by at most 1e-5 of itself, the result by at most 0.5 (2^-20 of itself + 2^-22 |v|).  P falls ever
 // faster beyond.  One exponential and 11 full-rate operations; the activation of a 256 x 256 tile is not hidden by
-// its matrix products, and a formula with a reciprocal too took 45 us of 200 for 65,536 x 1,024 -> 1,024.
+// its matrix products: 29 us of 194 for 65,536 x 1,024 -> 1,024 (45 by a formula with a reciprocal too).
 __device__ __forceinline__ float gelu(float v)
 {
     const float a = fabsf(v);
@@ -411,6 +411,8 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][N
 // WM x WN waves, each MT x NT MFMA tiles of 32 weight rows x 32 rows, K advancing 64 per stage through two
 // stages of LDS: each thread loads its chunks of stage s + 1 into registers while stage s is multiplied (requesting
 // s + 2 as well gained nothing: 5,003 x 1,001 -> 777 38 against 34 us).
+// Bound by its loads' latency: 5,003 x 1,001 -> 777 FP16 35 us, where rows lie at odd elements; by the rows' bytes in
+// 262,144 rows 64 -> 64 by expert, 25 us, 67 MB.
 // 128 bytes a row; chunk c (16 bytes) of row r sits at slot c ^ ((r / 2) % 8): the 16 rows that one 256-byte
 // LDS cycle of a fragment read serves fall in 16 different slots.
 template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int WPE>
@@ -528,6 +530,10 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 // A stage is 64 columns, 128 bytes of every row: whole cache lines (at 32 columns each line came from L2 twice).
 // A stage's last quarter is multiplied after the barrier that frees it, while the next stage's first fragments are
 // read, so the matrix unit does not wait for LDS there.
+// Bound by the matrix unit and the power it may draw: 8,192 x 4,096 -> 4,096 BF16 222 us, 1,240 TFLOP/s of the 1,519 that
+// the largest library product reaches; the unit is busy 65 % of the cycles at 1.82 GHz, LDS 26 %, L2 serves 80 %.
+// A wave's 128 x 64 sums take 6 operands from LDS for 8 products; two stages of 64 columns were faster than
+// four or five of 32 (222 against 237 and 240).
 template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int NS, int WPE>
 __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void product_big(ProductArgs p)
 {
@@ -678,7 +684,7 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 // Narrow layers over many rows, up to 64 weight rows and 64 columns: bound by the bytes of x and y.  A wave
 // keeps the whole weight matrix and the bias in registers, as MFMA operands, and takes kRounds tiles of 32 rows, each
 // straight from memory as the other operand (lane (g, n) loads the 16 bytes of row n at columns 16 kb + 8 g), two tiles
-// ahead.  No barrier anywhere; LDS only turns the outputs into rows.
+// ahead.  No barrier anywhere; LDS only turns the outputs into rows (1,048,576 rows 32 -> 32 FP16: 59 us).
 template <class T, bool GROUPED, bool GATED>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void product_narrow(ProductArgs p)
 {
@@ -747,8 +753,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // x, and its waves share K: each multiplies a run of columns straight from memory (16 x 16 x 32 MFMA, weights = A,
 // x = B; lane (g, n) loads the 16 bytes of row n at columns 8 g), kDepth steps requested at once, and the waves'
 // sums meet in LDS.  Every wave's loads are independent, with no LDS or barrier between them; the weights' bytes are
-// the floor (7 x 2,048 -> 2 x 4,096 gated: 33.6 MB).  Taking 32 or 64 rows at once instead of several workgroups that
-// read the same weights from L2 was slower (32 x 4,096 -> 4,096: 20 against 14 us; 64 x 4,096 -> 1,024: 27 against 10).
+// the floor (7 x 2,048 -> 2 x 4,096 gated: 33.6 MB, 9.4-10.8 us; 1 x 1,024 -> 1,024: 4.3, two latencies).  Taking 32 or
+// 64 rows at once instead of several workgroups that read the same weights from L2 was slower (32 x 4,096 -> 4,096: 20
+// against 14 us; 64 x 4,096 -> 1,024: 27 against 10).
 template <class T, bool GROUPED, bool GATED, int MA>
 __global__ __launch_bounds__(1024) void product_few(ProductArgs p)
 {
