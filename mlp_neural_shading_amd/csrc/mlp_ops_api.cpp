@@ -365,6 +365,9 @@ int mlp_expert_linear(const mlp_expert_linear_args *a, void *stream)
     MLP_TRY(check_workspace(a->workspace, a->workspace_bytes, need));
     const Span ws = span(need ? a->workspace : nullptr, 1, (int64_t)need, (int64_t)need, 1);
     if (overlap(ws, y) || overlap(ws, span(a->x, x_rows, a->in_width, a->ldx, 2)) || overlap(ws, span(a->w, 1, w_cols, w_cols, 2)) ||
+        overlap(ws, span(a->bias, 1, wide * a->experts, wide * a->experts, 2)) || overlap(ws, span(a->slots, 1, n, n, 4)) ||
+        overlap(ws, span(a->offsets, 1, a->experts + 1, a->experts + 1, 4)) || overlap(ws, span(a->places, 1, n, n, 4)) ||
+        overlap(ws, span(a->weight, 1, n, n, 4)) ||
         (a->residual && overlap(ws, span(a->residual, y_rows, a->out_width, a->ldr, out_size))))
         return fail(MLP_ERR_INVALID_ARGUMENT, "workspace overlaps another buffer");
     mlpk::ProductArgs p{};

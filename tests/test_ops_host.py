@@ -120,6 +120,11 @@ REFUSED = [
     ("mlp_expert_linear", dict(combine=1, workspace=8 * P + 8, workspace_bytes=256), "16-byte"),
     ("mlp_expert_linear", dict(combine=1, workspace=2 * P + 16, workspace_bytes=256), "workspace overlaps"),
     ("mlp_expert_linear", dict(combine=1, workspace=3 * P - 16, workspace_bytes=256), "workspace overlaps"),
+    ("mlp_expert_linear", dict(combine=1, workspace=4 * P + 32, workspace_bytes=256), "workspace overlaps"),
+    ("mlp_expert_linear", dict(combine=1, workspace=5 * P, workspace_bytes=256), "workspace overlaps"),
+    ("mlp_expert_linear", dict(combine=1, workspace=6 * P + 16, workspace_bytes=256), "workspace overlaps"),
+    ("mlp_expert_linear", dict(combine=1, workspace=8 * P, workspace_bytes=256, weight=8 * P + 252), "workspace overlaps"),
+    ("mlp_expert_linear", dict(combine=1, workspace=8 * P, workspace_bytes=256, bias=8 * P + 128), "workspace overlaps"),
     ("mlp_dispatch", dict(tokens=1 << 20, slots=64 * P, places=128 * P, index=256 * P, offsets=500 * P, workspace=128 * P + 16, workspace_bytes=1 << 20), "workspace overlaps"),
     ("mlp_expert_linear", dict(y=P), "overlaps"), ("mlp_expert_linear", dict(y=4 * P), "overlaps"),
 ]
