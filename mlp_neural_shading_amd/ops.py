@@ -14,6 +14,7 @@ require gradients are refused while autograd records.  A run of them together, a
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -59,6 +60,27 @@ class ExpertLinearArgs(ctypes.Structure):
                 ("ldr", _i64), ("y", _p), ("ldy", _i64), ("workspace", _p), ("workspace_bytes", _u64)]
 
 
+_FORMAT = {_p: "P", _i32: "i", _i64: "q", _u64: "Q", ctypes.c_float: "f"}
+
+
+def _packer(cls):
+    """The bytes of a ``cls`` of these fields: a third of the time that ctypes takes to fill one, and a number that
+    does not fit its field is refused instead of cut."""
+    packed = struct.Struct("@" + "".join(_FORMAT[t] for _, t in cls._fields_))
+    assert packed.size == ctypes.sizeof(cls)
+
+    def pack(*fields):
+        try:
+            return packed.pack(*fields)
+        except struct.error as e:
+            raise ValueError("%s: %s" % (cls.__name__, e)) from None
+    return pack
+
+
+_linear_args, _route_args, _dispatch_args, _expert_linear_args = map(
+    _packer, (LinearArgs, RouteArgs, DispatchArgs, ExpertLinearArgs))
+
+
 class Routing(NamedTuple):
     """``index`` int32 [tokens, k], -1 where no expert was left; ``weight`` float32 [tokens, k]."""
     index: torch.Tensor
@@ -88,30 +110,27 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _call(name: str, args: ctypes.Structure, device) -> None:
+def _call(name: str, args: bytes, device) -> None:
     """Enqueue on the current stream of the tensors' device."""
     f = getattr(_lib or lib(), name)
-    stream = torch._C._cuda_getCurrentRawStream(device.index)  # torch.cuda.current_stream takes longer than the launch
-    if torch._C._cuda_getDevice() == device.index:
-        rc = f(ctypes.addressof(args), stream)
+    at = device.index
+    stream = torch._C._cuda_getCurrentRawStream(at)  # torch.cuda.current_stream takes longer than the launch
+    if torch._C._cuda_getDevice() == at:
+        rc = f(args, stream)
     else:
         with torch.cuda.device(device):
-            rc = f(ctypes.addressof(args), stream)
+            rc = f(args, stream)
     if rc != B.MLP_OK:
         raise B.MlpError(rc, name, B.mlp_last_error())
 
 
-def _workspace(name: str, args: ctypes.Structure, device):
+def _workspace(name: str, args: bytes, device):
     """Scratch memory for the call, from the current stream's allocator; None where it needs none."""
     need = _u64()
-    rc = getattr(_lib or lib(), name)(ctypes.addressof(args), ctypes.addressof(need))
+    rc = getattr(_lib or lib(), name)(args, ctypes.addressof(need))
     if rc != B.MLP_OK:
         raise B.MlpError(rc, name, B.mlp_last_error())
-    if not need.value:
-        return None
-    ws = torch.empty(need.value, dtype=torch.uint8, device=device)
-    args.workspace, args.workspace_bytes = ws.data_ptr(), need.value
-    return ws
+    return torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
 
 
 def _tensor(name, t, dims, dtypes, device=None):
@@ -131,7 +150,9 @@ def _tensor(name, t, dims, dtypes, device=None):
 
 def _matrix(name, t, dtypes, device=None, rows=None, cols=None):
     """The row stride of a 2-D tensor with contiguous rows, after checking it."""
-    _tensor(name, t, 2, dtypes, device)
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda or (
+            device is not None and t.device != device) or t.requires_grad:
+        _tensor(name, t, 2, dtypes, device)
     r, c = t.shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError("%s must be %s x %s, got %d x %d" % (name, "?" if rows is None else rows,
@@ -190,10 +211,10 @@ def linear(x, w, bias=None, *, residual=None, act="none", gated=False, out=None,
     else:
         ldy = _matrix("out", out, (out_dtype,), device, rows, n)
     ldr = _matrix("residual", residual, (out_dtype,), device, rows, n) if residual is not None else 0
-    a = LinearArgs(rows, k, n, DTYPES[dtype], DTYPES[out_dtype], _choice("act", act, ACTIVATIONS), 1 if gated else 0,
-                   x.data_ptr(), ldx, w.data_ptr(), ldw,
-                   None if bias is None else _vector("bias", bias, dtype, device, wide),
-                   None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy)
+    a = _linear_args(rows, k, n, DTYPES[dtype], DTYPES[out_dtype], _choice("act", act, ACTIVATIONS), 1 if gated else 0,
+                     x.data_ptr(), ldx, w.data_ptr(), ldw,
+                     0 if bias is None else _vector("bias", bias, dtype, device, wide),
+                     0 if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy)
     _call("mlp_linear", a, device)
     return out
 
@@ -212,9 +233,10 @@ def route(logits, k, *, score="softmax", bias=None, groups=1, topk_groups=None, 
     room = k if 0 < k <= MLP_OPS_MAX_TOPK else 0  # others are refused below
     index = torch.empty(tokens, room, dtype=torch.int32, device=device)
     weight = torch.empty(tokens, room, dtype=torch.float32, device=device)
-    a = RouteArgs(tokens, experts, k, DTYPES[logits.dtype], _choice("score", score, SCORES), groups,
-                  groups if topk_groups is None else topk_groups, group_top, 1 if renormalise else 0, scale,
-                  logits.data_ptr(), ld, None if bias is None else _vector("bias", bias, torch.float32, device, experts),
+    a = _route_args(tokens, experts, k, DTYPES[logits.dtype], _choice("score", score, SCORES),
+                  groups, groups if topk_groups is None else topk_groups, group_top,
+                  1 if renormalise else 0, scale,
+                  logits.data_ptr(), ld, 0 if bias is None else _vector("bias", bias, torch.float32, device, experts),
                   index.data_ptr(), weight.data_ptr())
     _call("mlp_route", a, device)
     return Routing(index, weight)
@@ -230,12 +252,11 @@ def dispatch(index, experts) -> Dispatch:
     device, n, experts = index.device, index.numel(), int(experts)
     offsets = torch.empty(experts + 1 if 0 < experts <= MLP_OPS_MAX_EXPERTS else 0, dtype=torch.int32, device=device)
     slots = torch.empty(n, dtype=torch.int32, device=device)
-    places = torch.empty(n, dtype=torch.int32, device=device)
-    a = DispatchArgs(tokens, k, experts, index.data_ptr(), offsets.data_ptr(), slots.data_ptr(),
-                     places.data_ptr(), None, 0)
-    ws = _workspace("mlp_dispatch_workspace", a, device)
-    _call("mlp_dispatch", a, device)
-    del ws
+    places = torch.empty_like(slots)
+    a = (tokens, k, experts, index.data_ptr(), offsets.data_ptr(), slots.data_ptr(), places.data_ptr())
+    packed = _dispatch_args(*a, 0, 0)
+    ws = _workspace("mlp_dispatch_workspace", packed, device)
+    _call("mlp_dispatch", packed if ws is None else _dispatch_args(*a, ws.data_ptr(), ws.numel()), device)
     return Dispatch(offsets, slots, places)
 
 
@@ -273,17 +294,17 @@ def expert_linear(x, w, plan: Dispatch, bias=None, *, k, act="none", gated=False
     else:
         ldy = _matrix("out", out, (out_dtype,), device, y_rows, n)
     ldr = _matrix("residual", residual, (out_dtype,), device, y_rows, n) if residual is not None else 0
-    a = ExpertLinearArgs(
+    a = (
         tokens, k, experts, k_in, n, DTYPES[dtype], DTYPES[out_dtype], _choice("act", act, ACTIVATIONS),
         1 if gated else 0, 1 if rows == "slots" else 0, 1 if combine else 0, x.data_ptr(), ldx, w.data_ptr(),
         w.stride(1) if wide > 1 else max(w.stride(1), k_in), w.stride(0) if experts > 1 else 0,
-        None if bias is None else _vector("bias", bias, dtype, device, experts * wide),
+        0 if bias is None else _vector("bias", bias, dtype, device, experts * wide),
         _vector("plan.offsets", plan.offsets, torch.int32, device, experts + 1),
         _vector("plan.slots", plan.slots, torch.int32, device, total),
         _vector("plan.places", plan.places, torch.int32, device, total),
-        None if weight is None else _vector("weight", weight, torch.float32, device, total),
-        None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy, None, 0)
-    ws = _workspace("mlp_expert_linear_workspace", a, device)
-    _call("mlp_expert_linear", a, device)
-    del ws
+        0 if weight is None else _vector("weight", weight, torch.float32, device, total),
+        0 if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy)
+    packed = _expert_linear_args(*a, 0, 0)
+    ws = _workspace("mlp_expert_linear_workspace", packed, device) if combine else None
+    _call("mlp_expert_linear", packed if ws is None else _expert_linear_args(*a, ws.data_ptr(), ws.numel()), device)
     return out

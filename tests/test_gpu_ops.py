@@ -505,3 +505,36 @@ def test_same_call_same_bits():
     x = gpu(rnd(gen(1), 777, 200, dtype=t))
     first = layer_of_experts(x, *weights, 3)[0]
     assert all(torch.equal(first, layer_of_experts(x, *weights, 3)[0]) for _ in range(5))
+
+
+def test_sizes_past_32_bits_are_refused():
+    logits = torch.zeros(2, 8, device=device())
+    for kw in (dict(groups=2 ** 32 + 1), dict(groups=2, topk_groups=2 ** 32 + 1), dict(group_top=2 ** 32 + 1), dict(groups=1 - 2 ** 32)):
+        with pytest.raises((ValueError, B.MlpError)):
+            ops.route(logits, 2, **kw)
+    for k in (2 ** 32 + 2, 2 - 2 ** 32):
+        with pytest.raises((ValueError, B.MlpError)):
+            ops.route(logits, k)
+    index = torch.zeros(2, 2, dtype=torch.int32, device=device())
+    for experts in (2 ** 32 + 2, 2 - 2 ** 32, 0, 1025):
+        with pytest.raises((ValueError, B.MlpError)):
+            ops.dispatch(index, experts)
+
+
+def test_experts_and_logits_far_apart():
+    """Experts' matrices, rows of x and rows of logits whose offsets pass 2^31 elements."""
+    far = (1 << 30) + 17
+    base = torch.zeros(3 * far, dtype=torch.bfloat16, device=device())
+    w = base.as_strided((3, 24, 40), (far, 40, 1))
+    w.copy_(torch.randn(3, 24, 40, generator=gen(70)))
+    x = base.as_strided((3, 40), (far, 1), 4096)
+    x.copy_(torch.randn(3, 40, generator=gen(71)))
+    logits = base.as_strided((3, 7), (far, 1), 8192)
+    logits.copy_(torch.randn(3, 7, generator=gen(72)))
+    near_x, near_w, near_logits = x.contiguous(), w.contiguous(), logits.contiguous()
+    index = torch.tensor([[2, 0], [1, 2], [0, 1]], dtype=torch.int32, device=device())
+    plan = ops.dispatch(index, 3)
+    for combine in (False, True):
+        assert torch.equal(ops.expert_linear(x, w, plan, k=2, combine=combine), ops.expert_linear(near_x, near_w, plan, k=2, combine=combine))
+    got, want = ops.route(logits, 3), ops.route(near_logits, 3)
+    assert torch.equal(got.index, want.index) and torch.equal(got.weight, want.weight)

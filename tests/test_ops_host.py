@@ -189,3 +189,13 @@ def test_torch_refusals():
                     (lambda: ops.expert_linear(x, w[None], plan, k=2, rows="both"), "rows")):
         with pytest.raises(ValueError, match=says):
             f()
+
+
+def test_numbers_that_do_not_fit_their_field_are_refused():
+    """The torch form writes the structs' bytes itself: as ctypes does, but a larger number is not cut."""
+    fields = dict(tokens=4, experts=8, k=2, dtype=2, score=0, groups=1, topk_groups=1, group_top=1, renormalise=0, scale=2.5,
+                  logits=P, ld=8, bias=0, index=2 * P, weight=3 * P)
+    assert ops._route_args(*fields.values()) == bytes(ops.RouteArgs(**fields))
+    for name, value in (("k", 2 ** 32 + 2), ("groups", 2 ** 31), ("experts", -2 ** 32 + 8), ("tokens", 2 ** 63)):
+        with pytest.raises(ValueError, match="RouteArgs"):
+            ops._route_args(*{**fields, name: value}.values())
