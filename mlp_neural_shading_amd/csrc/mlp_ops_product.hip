@@ -40,7 +40,7 @@ __device__ __forceinline__ f4 mfma16(b8 a, b8 b, f4 c) { return __builtin_amdgcn
 // a polynomial of degree 8, fitted to log2 h on [0, 5.5] by weighted least squares, the weights moved until the error
 // is level: h is off by at most 1e-5 of itself, the result by at most 0.5 (2^-20 of itself + 2^-22 |v|).  P falls ever
 // faster beyond.  One exponential and 11 full-rate operations; the activation of a 256 x 256 tile is not hidden by
-// its matrix products: 29 us of 194 for 65,536 x 1,024 -> 1,024 (45 by a formula with a reciprocal too).
+// its matrix products: 29 us of 195 for 65,536 x 1,024 -> 1,024 (45 by a formula with a reciprocal too).
 __device__ __forceinline__ float gelu(float v)
 {
     const float a = fabsf(v);
