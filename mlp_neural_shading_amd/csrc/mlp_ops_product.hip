@@ -529,7 +529,10 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 // The same for rows that are 4-byte aligned: the stages go from memory into LDS directly, NS of them in flight.
 // A stage is 64 columns, 128 bytes of every row: whole cache lines (at 32 columns each line came from L2 twice).
 // A stage's last quarter is multiplied after the barrier that frees it, while the next stage's first fragments are
-// read, so the matrix unit does not wait for LDS there.
+// read, so the matrix unit does not wait for LDS there.  A width that is no whole number of stages ends with one of the
+// row's last 64 columns, requested like the others and multiplied without what it has of the stage before (20,000 x
+// 1,008 -> 768 with 256 x 256, 128 x 128 and 128 x 64 tiles 34, 44 and 56 us; 38, 51 and 65 with the rest loaded when
+// the whole stages are done).
 // Bound by the matrix unit and the power it may draw: 8,192 x 4,096 -> 4,096 BF16 222 us, 1,240 TFLOP/s of the 1,519 that
 // the largest library product reaches; the unit is busy 65 % of the cycles at 1.82 GHz, LDS 26 %, L2 serves 80 %.
 // A wave's 128 x 64 sums take 6 operands from LDS for 8 products; two stages of 64 columns were faster than
@@ -565,10 +568,13 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
     for (int i = 0; i < CB; ++i)
         src[CA + i] = (const T *)p.x + input_row<GROUPED>(p, tile.row0 + r_in + i * RPP, tile.row1) * p.ldx + 8 * c;
 
-    const int full = p.in / BK;
-    int issued = 0;  // stages requested; past the last whole one it is requested again, unused
+    const int full = p.in / BK, rest = p.in - full * BK;
+    // After the whole stages come the row's last 64 columns, some of them a second time; past them they are requested
+    // again, unused, and so is the last whole stage where `rest` is 0, or odd (4-byte aligned loads cannot reach it).
+    const int last_step = rest % 2 ? 0 : rest;
+    int issued = 0;  // stages requested
     auto request = [&](uint8_t *dst) {
-        const int step = issued + 1 < full ? BK : 0;
+        const int step = issued + 1 < full ? BK : issued + 1 == full ? last_step : 0;
 #pragma unroll
         for (int i = 0; i < CA + CB; ++i) {
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src[i],
@@ -664,17 +670,36 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 #undef MLP_STAGE
     __builtin_amdgcn_s_waitcnt(0x0070);  // the requests past the end
     __syncthreads();
-    if (full * BK < p.in) {  // a partial last stage, through registers
+    if (rest) {
+        const uint8_t *d = NS == 2 ? (full % 2 ? l1 : l0) : full % 3 == 0 ? l0 : full % 3 == 1 ? l1 : l2;
+        int skip = BK - rest;  // columns of the last 64 that the whole stages have had
+        if (!full || !last_step) {  // the rest and zeros, through registers
 #pragma unroll
-        for (int i = 0; i < CA + CB; ++i) {
-            const T *row = src[i] - 8 * c - (full ? (full - 1) * BK : 0);
-            *(u4 *)(l0 + tid * 16 + i * (TH * 16)) = load16_tail(row, full * BK + 8 * c, p.in);
+            for (int i = 0; i < CA + CB; ++i) {
+                const T *row = src[i] - 8 * c - (full ? (full - 1) * BK : 0);
+                *(u4 *)(l0 + tid * 16 + i * (TH * 16)) = load16_tail(row, full * BK + 8 * c, p.in);
+            }
+            __syncthreads();
+            d = l0;
+            skip = 0;
         }
-        __syncthreads();
+#pragma unroll 1
+        for (int kb = skip / 16; kb < 4; ++kb) {
+            const int ch = 16 * ((2 * kb + g) ^ swz), first = skip - 8 * (2 * kb + g);
+            auto keep = [&](const uint8_t *at) {
+                u4 v = *(const u4 *)at;
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-            read(l0, kb);
-            multiply(kb);
+                for (int i = 0; i < 4; ++i)
+                    v[i] = 2 * i >= first ? v[i] : 0u;
+                return __builtin_bit_cast(V8, v);
+            };
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                fa[0][mt] = keep(d + a_rd + mt * 32 * 128 + ch);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                fb[0][nt] = keep(d + b_rd + nt * 32 * 128 + ch);
+            multiply(0);
         }
         __syncthreads();
     }

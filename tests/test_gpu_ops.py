@@ -79,6 +79,31 @@ def test_linear_large(rows, k, n, gated, dtype):
     R.check(y, *R.linear64(x, w, None, r, "none", gated), torch.float32, "fp32")
 
 
+@pytest.mark.parametrize("rows,n", [(5000, 1800), (4000, 900), (2500, 640)])
+@pytest.mark.parametrize("k", [64, 66, 72, 96, 126, 128, 130, 184, 190, 192, 194, 254, 65, 127, 129, 191, 34])
+def test_last_columns_count_once(rows, n, k):
+    """Whole numbers, whose sums are exact, for widths that end anywhere in a stage; a row stride beyond the width
+    holds NaN, and one row an infinity in the first column of its last 64."""
+    t = torch.bfloat16
+    ld = k + 6 + k % 2
+    x, w = (torch.full((r, ld), math.nan, dtype=t, device=device()) for r in (rows, n))
+    x[:, :k] = torch.randint(-3, 4, (rows, k), generator=gen(k)).to(device())
+    w[:, :k] = torch.randint(1, 4, (n, k), generator=gen(k + 1)).to(device())
+    want = x[:, :k].float().cpu() @ w[:, :k].float().cpu().T
+    got = ops.linear(x[:, :k], w[:, :k], out_dtype=torch.float32)
+    assert torch.equal(got.cpu(), want)
+    x[rows - 2, max(k - 64, 0)] = math.inf
+    want[rows - 2] = math.inf
+    assert torch.equal(ops.linear(x[:, :k], w[:, :k], out_dtype=torch.float32).cpu(), want)
+    index = (torch.arange(rows, device=device()) * 7 // rows % 3).int()[:, None]
+    plan = ops.dispatch(index, 3)
+    each = torch.stack([w, 2 * w, -w])[:, :, :k]
+    x[rows - 2, max(k - 64, 0)] = 1
+    want = x[:, :k].float().cpu() @ w[:, :k].float().cpu().T * torch.tensor([1., 2., -1.])[index.cpu().long()]
+    got = ops.expert_linear(x[:, :k], each, plan, k=1, combine=True, out_dtype=torch.float32)
+    assert torch.equal(got.cpu(), want)
+
+
 @pytest.mark.parametrize("act", ops.ACTIVATIONS)
 @pytest.mark.parametrize("rows,k,n", [(1, 96, 40), (9, 130, 33), (70, 64, 96), (260, 136, 200)])
 def test_linear_activations_and_gates(rows, k, n, act):
