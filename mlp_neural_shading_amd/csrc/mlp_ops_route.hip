@@ -175,17 +175,17 @@ __global__ __launch_bounds__(64) void route_tokens(RouteArgs r)
 // ---- the same, L lanes per token ------------------------------------------------------------------
 //
 // For up to L * VPL experts: a token has L = 16 or 64 lanes, so 64 / L tokens share a wave, and a group of experts a run
-// of r.lanes of them, a power of two (without groups, all L); lane i of a group holds its experts VPL i .. VPL i + VPL - 1.  The choice runs on FP32 keys first
-// (the logits where they give the order, else score + bias), brought to whole numbers of 31 bits: the key's place
-// between the token's smallest and largest above the expert's index counted down, so that every key differs and
-// equal ones go to the lower index.  The next best key below b is then the largest key - b mod 2^32: one
-// subtraction and half a maximum per expert and pick, against a comparison, a search and a removal.  Where
+// of r.lanes of them, a power of two (without groups, all L); lane i of a group holds its experts VPL i .. VPL i + VPL - 1.
+// The choice runs on FP32 keys first (the logits where they give the order, else score + bias), brought to whole numbers
+// of 31 bits: the key's place between the token's smallest and largest above the expert's index counted down, so that
+// every key differs and equal ones go to the lower index.  The next best key below b is then the largest key - b mod
+// 2^32: one subtraction and half a maximum per expert and pick, against a comparison, a search and a removal.  Where
 // neighbours among the k + 1 best lie within the error that a key may have, and are not the same logit and bias, the
-// order is not certain: some more are picked, one per lane, and these are ranked by their choices in 64 bits.  Where
-// even that may leave one out, or two groups' values are too near, the wave chooses once more on 64-bit keys of all
-// experts (done each time, that cost 11 us of 42).  The chosen scores themselves are computed in 64 bits (the softmax's
-// sum in FP32).  65,536 tokens x 256 experts, sigmoid, 8 groups, k = 8: 38 us, bound by the instructions of the
-// picks, groups and scores; the logits' bytes alone take 7.
+// order is not certain: some more are picked, one per lane, and these are ranked by their choices in 64 bits.  (Where
+// the k-th and the next are the same, all that lies near them is looked at.)  Where even that may leave one out, or two
+// groups' values are too near, the wave chooses once more on 64-bit keys of all experts (done each time, that cost 11 us
+// of 42).  The chosen scores themselves are computed in 64 bits (the softmax's sum in FP32).  65,536 tokens x 256 experts,
+// sigmoid, 8 groups, k = 8: 38 us, bound by the instructions of the picks, groups and scores; the logits' bytes alone take 7.
 
 constexpr float kLow = -__builtin_huge_valf();
 
@@ -580,10 +580,24 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
     // places are off by 1 each, and by what the keys are off
     const float doubt = 3.0f + step * (near + fmaxf(fabsf(high), fabsf(low)) * (1.0f / (1 << 22)));
     auto apart = [&](unsigned a, unsigned b) { return (float)(a / (L * VPL) - b / (L * VPL)); };
-    bool ordered = true;
+    bool ordered = true, equal = false;
     if (mine && next && me < r.k && !(apart(mine, next) > doubt)) {
         const int after = expert_at(next);
         ordered = logit[index] == logit[after] && (!r.bias || r.bias[index] == r.bias[after]);
+        equal = ordered && me == r.k - 1;
+    }
+    if (__any(equal)) {  // the k-th and the next are: what is near them has to be so too
+        const int edge = __shfl(equal ? index : -1, row + r.k - 1);
+        const unsigned kth = __shfl(mine, row + r.k - 1);
+        if (edge >= 0) {
+            const float x_edge = fmaxf((float)logit[edge], kLow), b_edge = r.bias ? r.bias[edge] : 0.0f;
+            float x[VPL];
+            load_logits<T, VPL>(logit, e0, last, x);
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                if (place[v] && place[v] < kth && !(apart(kth, place[v]) > doubt))
+                    ordered = ordered && x[v] == x_edge && (!r.bias || r.bias[e0 + v] == b_edge);
+        }
     }
     if (__any(!ordered) && !__any(!sure)) {
         const int count = r.k + 8 < L - 1 ? r.k + 8 : L - 1;  // candidates

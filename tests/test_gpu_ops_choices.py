@@ -1,0 +1,92 @@
+"""GPU tests of the router's choices where they are hard: keys that lie close together, equal ones at the last place,
+saturated scores, values of groups whose parts cancel or overflow, rows beside others.  The plain form is
+ops_reference.route64; where the logits alone give the order (no bias, and no group valued by two experts) it is
+given their ranks, since 64-bit scores of different logits can be equal (sigmoid(40) and sigmoid(50)).
+
+Sizes by layout of the experts over a wave: up to 64, 128 and 256 experts with k < 16 share it among four tokens,
+up to 512 take a wave, and more than that another kernel; 8, 300 and 500 fill theirs in part."""
+import math
+
+import pytest
+import torch
+
+import ops_reference as R
+from gpu_util import device, log
+from mlp_neural_shading_amd import ops
+
+pytestmark = pytest.mark.gpu
+
+LAYOUTS = [8, 64, 128, 256, 300, 500, 512, 900]
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def want(logits, k, score="softmax", bias=None, groups=1, topk_groups=None, group_top=1, renormalise=False):
+    kw = dict(score=score, groups=groups, topk_groups=topk_groups, group_top=group_top)
+    if bias is not None or (group_top == 2 and (topk_groups or groups) < groups):
+        return R.route64(logits, k, bias=bias, renormalise=renormalise, **kw)
+    x = logits.double()
+    ranks = x.clone()
+    for t in range(len(x)):
+        if score == "softmax" and bool((x[t] == math.inf).any()):
+            continue  # the others' scores are exactly 0
+        seen = x[t] > -math.inf
+        ranks[t, seen] = torch.unique(x[t, seen], return_inverse=True)[1].double() / 64 - 8
+    index, _ = R.route64(ranks, k, **kw)
+    weight = torch.zeros(len(x), k, dtype=torch.float64)
+    for t in range(len(x)):
+        seen = x[t] > -math.inf
+        on = index[t] >= 0
+        if not bool(on.any()):
+            continue
+        top = x[t, seen].max()
+        if score == "softmax":
+            s = torch.where(x[t] == top, torch.ones_like(x[t]), torch.exp(x[t] - top))
+            s = torch.where(seen, s, torch.zeros_like(s))
+            s = s / s.sum()
+        else:
+            s = torch.sigmoid(x[t])
+        w = s[index[t, on].long()]
+        if renormalise:
+            w = w / w.sum() if float(w.sum()) > 0 else torch.zeros_like(w)
+        weight[t, on] = w
+    return index, weight
+
+
+def check(logits, k, **kw):
+    index, weight = want(logits, k, **kw)
+    bias = kw.pop("bias", None)
+    got = ops.route(logits.to(device()), k, bias=None if bias is None else bias.to(device()), **kw)
+    bad = (got.index.cpu() != index).any(1).nonzero().flatten().tolist()
+    assert not bad, (logits.shape, k, kw, bad[:3], got.index[bad[0]].tolist(), index[bad[0]].tolist())
+    # 8 half-steps of FP32, as everywhere for the weights
+    assert bool(((got.weight.cpu().double() - weight).abs() <= 8 * 2.0 ** -24 * weight.abs() + 2.0 ** -149).all())
+
+
+def counts(experts):
+    return [k for k in ((1, 2, 4, 8, 15, 20, 32) if experts < 500 else (1, 8, 32)) if k <= experts]
+
+
+@pytest.mark.parametrize("experts", LAYOUTS)
+def test_equals_at_the_last_place(experts):
+    """The k-th and the next are equal, and behind them stands one that FP32 keys, or their places, do not tell from them,
+    and that is the better one."""
+    log("equals at the last place", experts)
+    zero = torch.zeros(experts)
+    for k in counts(experts):
+        run = min(k + 1, experts - 2)
+        for better in (1, 2):
+            up = torch.zeros(3, experts)
+            up[:, :run] = 17.0
+            up[0, run:run + better], up[1, experts - better:], up[2, 0] = 17.125, 17.125, 17.25
+            check(up, k, score="sigmoid", bias=zero)
+            check(up, k, score="sigmoid", bias=zero + 0.25, renormalise=True)
+            near = torch.full((2, experts), -60.0)
+            near[:, :run] = 1.0
+            near[0, run:run + better], near[1, experts - better:] = 1 + 2.0 ** -22, 1 + 2.0 ** -22
+            for score in ops.SCORES:
+                check(near, k, score=score)
+            check(near, k, score="softmax", bias=zero)
+            check(near, k, score="softmax", bias=zero + 16.0)
