@@ -84,7 +84,9 @@ enum {
  * weights.  With groups > 1 (consecutive experts, equally many in each) only the topk_groups groups of
  * largest value are chosen from; a group's value is the sum of its group_top largest choices (of as many
  * as it has).  Equal choices, and equal groups, go to the lower index.  Choices are compared as if computed
- * exactly (to about 50 bits).  The weight is the score (not the choice), divided by the sum of the token's
+ * exactly: without a bias and without group_top 2 by the logits themselves, whose order is the scores' (with a
+ * +infinite logit the softmax's other scores are 0, and equal), else to about 50 bits.  A token's choice and
+ * weights do not depend on the other tokens of the call.  The weight is the score (not the choice), divided by the sum of the token's
  * chosen scores if `renormalise` (0 where that sum is 0), times `scale`.
  * An expert whose logit is NaN or -infinity (a masked expert) or whose bias is NaN or -infinity is never
  * chosen, and a group without other experts neither; the softmax leaves NaN and -infinity out, and logits of

@@ -11,6 +11,10 @@ namespace {
 
 constexpr double kNone = -__builtin_huge_val();  // the choice of an expert that cannot be chosen
 
+// Without a bias, and without a sum of two scores, the logits give the order: a score rises with its logit, also where
+// two scores are equal in 64 bits.  (But beside a logit of +infinity the softmax's other scores are all 0.)
+__device__ __forceinline__ bool logits_order(const RouteArgs &r) { return !r.bias && (r.topk_groups == r.groups || r.group_top == 1); }
+
 __device__ __forceinline__ double wave_max(double v)
 {
 #pragma unroll
@@ -58,14 +62,17 @@ __global__ __launch_bounds__(64) void route_tokens(RouteArgs r)
             const int e = v * 64 + lane;
             score[v] = e < r.experts ? (double)(float)x[e] : kNone;
             open[v] = score[v] > kNone;  // neither NaN nor -infinity
+            choice[v] = score[v];
             m = open[v] ? fmax(m, score[v]) : m;
         }
+        bool by_logit = logits_order(r);
         if (r.sigmoid) {
 #pragma unroll
             for (int v = 0; v < VPL; ++v)
                 score[v] = open[v] ? 1.0 / (1.0 + exp(-score[v])) : 0.0;
         } else {
             m = wave_max(m);
+            by_logit = by_logit && m < __builtin_huge_val();
             double sum = 0.0;
 #pragma unroll
             for (int v = 0; v < VPL; ++v) {
@@ -80,7 +87,8 @@ __global__ __launch_bounds__(64) void route_tokens(RouteArgs r)
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
             const int e = v * 64 + lane;
-            choice[v] = open[v] ? score[v] + (r.bias ? (double)r.bias[e] : 0.0) : kNone;
+            if (!by_logit)
+                choice[v] = open[v] ? score[v] + (r.bias ? (double)r.bias[e] : 0.0) : kNone;
             if (!(choice[v] > kNone))
                 choice[v] = kNone;
         }
@@ -181,9 +189,9 @@ __global__ __launch_bounds__(64) void route_tokens(RouteArgs r)
 // every key differs and equal ones go to the lower index.  The next best key below b is then the largest key - b mod
 // 2^32: one subtraction and half a maximum per expert and pick, against a comparison, a search and a removal.  Where
 // neighbours among the k + 1 best lie within the error that a key may have, and are not the same logit and bias, the
-// order is not certain: some more are picked, one per lane, and these are ranked by their choices in 64 bits.  (Where
+// order is not certain: some more are picked, one per lane, and these are ranked by their logits or choices in 64 bits.  (Where
 // the k-th and the next are the same, all that lies near them is looked at.)  Where even that may leave one out, or two
-// groups' values are too near, the wave chooses once more on 64-bit keys of all experts (done each time, that cost 11 us
+// groups' values are too near, the token chooses once more on 64-bit keys of all experts (done each time, that cost 11 us
 // of 42).  The chosen scores themselves are computed in 64 bits (the softmax's sum in FP32).  65,536 tokens x 256 experts,
 // sigmoid, 8 groups, k = 8: 38 us, bound by the instructions of the picks, groups and scores; the logits' bytes alone take 7.
 
@@ -384,7 +392,7 @@ __device__ __forceinline__ void mask_groups(const RouteArgs &r, K (&key)[VPL], K
         key[v] = out ? none : key[v];
 }
 
-// The choice on 64-bit keys: in lane j < k the j-th best expert, -1 where none is left.
+// The choice on exact logits or 64-bit keys: in lane j < k the j-th best expert, -1 where none is left.
 template <class T, int L, int VPL>
 __device__ __forceinline__ int choose_exactly(const RouteArgs &r, const T *logit)
 {
@@ -394,16 +402,17 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &r, const T *logit
     float x[VPL];
     load_logits<T, VPL>(logit, e0, end, x);
     double key[VPL], scale = 1.0;
+    float top = kLow;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+        top = fmaxf(top, x[v]);
+    top = lanes_max<L>(top);
+    const bool by_logit = logits_order(r) && (r.sigmoid || top < __builtin_huge_valf());  // the same in a token's lanes
     if (r.sigmoid) {
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
             key[v] = 1.0 / (1.0 + exp(-(double)x[v]));
     } else {
-        float top = kLow;
-#pragma unroll
-        for (int v = 0; v < VPL; ++v)
-            top = fmaxf(top, x[v]);
-        top = lanes_max<L>(top);
         double sum = 0.0;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
@@ -415,7 +424,7 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &r, const T *logit
     }
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-        key[v] = key[v] * scale + (r.bias ? (double)r.bias[e0 + v < end ? e0 + v : 0] : 0.0);
+        key[v] = by_logit ? (double)x[v] : key[v] * scale + (r.bias ? (double)r.bias[e0 + v < end ? e0 + v : 0] : 0.0);
         key[v] = x[v] > kLow && key[v] > kNone ? key[v] : kNone;
     }
     bool unused;
@@ -459,8 +468,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
     // Places for the keys, as many as FP32 counts and 31 bits hold; 0 for masked ones.
     constexpr unsigned kPlaces = L * VPL <= 256 ? 1u << 23 : 1u << 22;
     static_assert((uint64_t)kPlaces * (L * VPL) <= 1u << 31, "31 bits");
-    // Without a bias, and without a sum of two scores, the logits give the order: a score rises with its logit.
-    const bool by_logit = !r.bias && (r.topk_groups == r.groups || r.group_top == 1);
+    const bool by_logit = logits_order(r);
     float bias[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
@@ -489,6 +497,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
     float key[VPL];
     load_logits<T, VPL>(logit, e0, last, key);
     float top = kLow, total = 0.0f;  // softmax: largest logit, sum of exp(logit - top)
+    bool infinite = false;           // softmax: a logit of +infinity; the others' scores are then exactly 0
     float near = 0.0f;
     if (r.sigmoid) {
         if (!by_logit) {
@@ -506,7 +515,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
         for (int v = 0; v < VPL; ++v)
             top = larger(top, key[v]);
         top = lanes_max<L>(top);
-        const bool infinite = top == __builtin_huge_valf();  // the others' scores are then exactly 0
+        infinite = top == __builtin_huge_valf();
         if (!by_logit || !r.renormalise || infinite) {
             float e[VPL];
 #pragma unroll
@@ -599,25 +608,30 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
                     ordered = ordered && x[v] == x_edge && (!r.bias || r.bias[e0 + v] == b_edge);
         }
     }
-    if (__any(!ordered) && !__any(!sure)) {
+    // Each token takes what its own row needs, whatever its neighbours in the wave need.
+    const unsigned long long of_token = L < 64 ? ((1ull << (L & 63)) - 1) << row : ~0ull;
+    const bool near_ones = sure && (__ballot(!ordered) & of_token);
+    if (__any(near_ones)) {
         const int count = r.k + 8 < L - 1 ? r.k + 8 : L - 1;  // candidates
         pick(r.k + 1, count);
         const unsigned place_of = valid();
         const int candidate = me < count ? expert_at(place_of) : -1;
         const unsigned kth = __shfl(place_of, row + r.k - 1), end = __shfl(place_of, row + count - 1);
-        if (end && !(apart(kth, end) > 2.0f * doubt))
+        if (near_ones && end && !(apart(kth, end) > 2.0f * doubt))
             sure = false;  // one that was not picked may be as good
         double exact = kNone;
         if (candidate >= 0) {
             const double z = (double)(float)logit[candidate], b = r.bias ? (double)r.bias[candidate] : 0.0;
-            if (r.sigmoid) {
+            if (by_logit && !infinite) {
+                exact = z;
+            } else if (r.sigmoid) {
                 const double e = exp_exact(-fabs(z));
                 exact = (z < 0.0 ? e : 1.0) / (1.0 + e) + b;
             } else {
                 exact = z == (double)top ? 1.0 : exp_exact(z - (double)top);
             }
         }
-        if (!r.sigmoid) {
+        if (!r.sigmoid && !by_logit) {
             float x[VPL];
             load_logits<T, VPL>(logit, e0, last, x);
             double sum = 0.0;
@@ -640,14 +654,16 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
         const int to = candidate >= 0 ? rank : L - 1;
         const int moved = __builtin_amdgcn_ds_permute((row + to) * 4, candidate);
         // a lane that nobody sends to reads 0
-        const unsigned long long sent = __ballot(candidate >= 0) >> row;
-        const int held = __popcll(L < 64 ? sent & ((1ull << (L & 63)) - 1) : sent);
-        index = me < held ? moved : -1;
+        const int held = __popcll(__ballot(candidate >= 0) & of_token);
+        if (near_ones)
+            index = me < held ? moved : -1;
     }
     if (me >= r.k)
         index = -1;
-    if (__any(!sure))
-        index = choose_exactly<T, L, VPL>(r, logit);
+    if (__any(!sure)) {
+        const int chosen = choose_exactly<T, L, VPL>(r, logit);
+        index = sure ? index : chosen;
+    }
 
     // The chosen scores, in lane j the j-th.
     double score = 0.0;

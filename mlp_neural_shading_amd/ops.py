@@ -225,7 +225,9 @@ def route(logits, k, *, score="softmax", bias=None, groups=1, topk_groups=None, 
 
     ``logits`` [tokens, experts] float32, float16 or bfloat16 with contiguous rows; ``bias`` float32 [experts]
     enters the choice only; ``groups`` of consecutive experts, of which the ``topk_groups`` with the largest sum
-    of their ``group_top`` (1 or 2) best are chosen from.  -inf and NaN logits are never chosen."""
+    of their ``group_top`` (1 or 2) best are chosen from.  -inf and NaN logits are never chosen.  Without a bias and
+    without ``group_top`` 2 the logits themselves are compared, else the choices to about 50 bits; a token's row does
+    not depend on the others."""
     ld = _matrix("logits", logits, _FLOATS)
     tokens, experts = logits.shape
     device = logits.device

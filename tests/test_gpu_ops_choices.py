@@ -90,3 +90,41 @@ def test_equals_at_the_last_place(experts):
                 check(near, k, score=score)
             check(near, k, score="softmax", bias=zero)
             check(near, k, score="softmax", bias=zero + 16.0)
+
+
+@pytest.mark.parametrize("experts", [8, 64, 256, 300, 900])
+def test_a_row_is_the_same_beside_any_others(experts):
+    """Alone, in any place and beside rows that need a closer look: the same bits.  Among them logits whose 64-bit scores
+    are equal, though they are not."""
+    g = gen(experts)
+    log("beside others", experts)
+    rows = torch.randn(14, experts, generator=g)
+    rows[0, :2] = torch.tensor([40., 50.])
+    rows[1] = 36 + torch.arange(experts) % 7
+    rows[2] = -600 - 10.0 * (torch.arange(experts) % 9)
+    rows[2, 3] = 0
+    rows[3, :3] = torch.tensor([17., 17., 17.125])
+    rows[4] = 14 + 4 * torch.rand(experts, generator=g)
+    rows[5] = torch.randint(-2, 3, (experts,), generator=g).float()
+    rows[6, 4] = math.inf
+    rows[7] = 1.0
+    rows[7, 5] = 1 + 2.0 ** -23
+    rows[8] = -math.inf
+    rows[9, 1:] = math.nan
+    groups = 4 if experts % 4 == 0 else 1
+    for k in (1, 4, 8) if experts < 500 else (4,):
+        for kw in (dict(), dict(renormalise=True), dict(bias=torch.zeros(experts)), dict(bias=torch.full((experts,), 0.25)),
+                   dict(groups=groups, topk_groups=max(1, groups // 2)), dict(groups=groups, topk_groups=max(1, groups // 2), group_top=2)):
+            for score in ops.SCORES:
+                if kw.get("topk_groups", 1) * experts // kw.get("groups", 1) < k:
+                    continue
+                check(rows, k, score=score, **kw)
+                on_gpu = {**kw, "bias": kw["bias"].to(device())} if "bias" in kw else kw
+                x = rows.to(device())
+                whole = ops.route(x, k, score=score, **on_gpu)
+                order = torch.randperm(14, generator=g).to(device())
+                mixed = ops.route(x[order], k, score=score, **on_gpu)
+                assert torch.equal(mixed.index, whole.index[order]) and torch.equal(mixed.weight, whole.weight[order])
+                for t in range(12):
+                    alone = ops.route(x[t:t + 1], k, score=score, **on_gpu)
+                    assert torch.equal(alone.index[0], whole.index[t]) and torch.equal(alone.weight[0], whole.weight[t])
