@@ -553,7 +553,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
     }
     high = lanes_max<L>(high);
     low = fmaxf(-lanes_max<L>(-low), high - 64.0f);  // what lies further off shares the last place
-    const float step = high > low ? (float)(kPlaces - 4) / (high - low) : 0.0f;  // infinite keys: 0 or not sure
+    // Keys that all lie within 2^23 / 2^100 of each other fill fewer places: no step is infinite, and they count as near.
+    const float step = high > low ? fminf((float)(kPlaces - 4) / (high - low), 0x1p100f) : 0.0f;  // infinite keys: 0 or not sure
     if (!(high - low < -kLow) && high > kLow)
         sure = false;
     unsigned place[VPL];

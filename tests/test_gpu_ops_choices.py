@@ -128,3 +128,24 @@ def test_a_row_is_the_same_beside_any_others(experts):
                 for t in range(12):
                     alone = ops.route(x[t:t + 1], k, score=score, **on_gpu)
                     assert torch.equal(alone.index[0], whole.index[t]) and torch.equal(alone.weight[0], whole.weight[t])
+
+
+@pytest.mark.parametrize("experts", LAYOUTS)
+def test_keys_that_hardly_differ(experts):
+    """A token whose keys span less than 1e-32, but are not all equal."""
+    g = gen(experts)
+    log("tiny spans", experts)
+    one = torch.zeros(6, experts)
+    for t, v in enumerate((1e-33, 1e-35, 1e-38, 1e-42, -1e-35, 1.5e-45)):
+        one[t, 2 + t % 2] = v
+    few = torch.randint(-3, 4, (6, experts), generator=g).float() * 2.0 ** -140
+    low = -75 - 4.5 * torch.rand(6, experts, generator=g)
+    low[0], low[1] = torch.linspace(-78, -79.5, experts), torch.linspace(-79.5, -78, experts)
+    low[2, :8] = torch.tensor([-75., -80., -76., -82., -85., -79., -81., -78.])
+    for k in counts(experts):
+        for score in ops.SCORES:
+            check(one, k, score=score)
+            check(few, k, score=score)
+        check(low, k, score="sigmoid", bias=torch.zeros(experts))
+        check(low, k, score="sigmoid")
+        check(low * 3, k, score="softmax", bias=torch.full((experts,), 2.0 ** -120), renormalise=True)
