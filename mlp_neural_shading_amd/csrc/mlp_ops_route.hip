@@ -383,6 +383,10 @@ __device__ __forceinline__ void mask_groups(const RouteArgs &r, K (&key)[VPL], K
     }
     const bool out = better >= r.topk_groups || !(value > none);
     if (near > 0) {  // FP32: the worst group taken and the best one left
+        // A sum of two finite keys that is none in FP32 orders nothing.
+        const bool past = first > kLow && fabsf((float)first) < -kLow && !(fabsf((float)value) < -kLow);
+        if (__ballot(past) & (L < 64 ? ((1ull << (L & 63)) - 1) << row : ~0ull))
+            sure = false;
         const float taken = -lanes_max<L>(out ? kLow : -(float)value), left = lanes_max<L>(out ? (float)value : kLow);
         if (left > kLow && !(taken - left > 2 * near + fabsf(taken) * (1.0f / (1 << 22))))
             sure = false;

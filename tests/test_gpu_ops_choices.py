@@ -149,3 +149,18 @@ def test_keys_that_hardly_differ(experts):
         check(low, k, score="sigmoid", bias=torch.zeros(experts))
         check(low, k, score="sigmoid")
         check(low * 3, k, score="softmax", bias=torch.full((experts,), 2.0 ** -120), renormalise=True)
+
+
+@pytest.mark.parametrize("experts,groups", [(16, 8), (64, 8), (128, 4), (256, 8), (320, 8), (512, 16), (640, 8)])
+def test_values_of_groups_past_fp32(experts, groups):
+    """Biases of FP32's lowest value: the sum of two is no FP32 number, and their groups are still there."""
+    log("groups past fp32", experts, groups)
+    per, lowest = experts // groups, torch.finfo(torch.float32).min
+    logits = torch.randn(9, experts, generator=gen(experts))
+    bias = torch.full((experts,), lowest)
+    bias[2 * per:3 * per] = 0.1
+    for k in (2, min(per + 2, 12)):
+        for score in ops.SCORES:
+            check(logits, k, score=score, bias=bias, groups=groups, topk_groups=3, group_top=2)
+            check(logits, k, score=score, bias=-bias, groups=groups, topk_groups=3, group_top=2)
+            check(logits, k, score=score, bias=bias, groups=groups, topk_groups=groups - 1, group_top=2)
