@@ -340,7 +340,7 @@ __device__ __forceinline__ double one_over(double v)
 }
 
 // Masks the keys of the groups that are not among the topk_groups best.  In FP32 (`near`: how far two keys may lie
-// from their true distance, apart from the rounding of a sum; 0 for exact keys) clears `sure` where two groups are too near each other.
+// from their true distance, apart from the roundings of sums; 0 for exact keys) clears `sure` where two groups are too near each other.
 template <class K, int L, int VPL>
 __device__ __forceinline__ void mask_groups(const RouteArgs &r, K (&key)[VPL], K near, bool &sure)
 {
@@ -383,12 +383,16 @@ __device__ __forceinline__ void mask_groups(const RouteArgs &r, K (&key)[VPL], K
     }
     const bool out = better >= r.topk_groups || !(value > none);
     if (near > 0) {  // FP32: the worst group taken and the best one left
+        const float one = fabsf((float)first), two = r.group_top == 2 && second > none ? fabsf((float)second) : 0.0f;
         // A sum of two finite keys that is none in FP32 orders nothing.
-        const bool past = first > kLow && fabsf((float)first) < -kLow && !(fabsf((float)value) < -kLow);
+        const bool past = first > kLow && one < -kLow && !(one + two < -kLow);
         if (__ballot(past) & (L < 64 ? ((1ull << (L & 63)) - 1) << row : ~0ull))
             sure = false;
-        const float taken = -lanes_max<L>(out ? kLow : -(float)value), left = lanes_max<L>(out ? (float)value : kLow);
-        if (left > kLow && !(taken - left > 2 * near + fabsf(taken) * (1.0f / (1 << 22))))
+        // Half a step of each key for the addition of its bias, half a one of the sum, and of these bounds themselves;
+        // the parts may be far larger than the value.
+        const float off = one + two < -kLow ? (one + two) * (1.0f / (1 << 22)) : 0.0f;
+        const float taken = -lanes_max<L>(out ? kLow : off - (float)value), left = lanes_max<L>(out && first > kLow ? (float)value + off : kLow);
+        if (left > kLow && !(taken - left > 2 * near))
             sure = false;
     }
 #pragma unroll

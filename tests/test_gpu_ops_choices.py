@@ -164,3 +164,18 @@ def test_values_of_groups_past_fp32(experts, groups):
             check(logits, k, score=score, bias=bias, groups=groups, topk_groups=3, group_top=2)
             check(logits, k, score=score, bias=-bias, groups=groups, topk_groups=3, group_top=2)
             check(logits, k, score=score, bias=bias, groups=groups, topk_groups=groups - 1, group_top=2)
+
+
+@pytest.mark.parametrize("experts,groups", [(16, 8), (32, 16), (512, 4), (8, 4)])
+def test_values_of_groups_whose_parts_cancel(experts, groups):
+    """A large and a large negative bias in each group: the keys are rounded by steps of theirs, the values are small."""
+    log("groups that cancel", experts, groups)
+    per = experts // groups
+    for size in (30.0, 1000.0, 20000.0):
+        g = gen(int(size))
+        bias = torch.full((experts,), -2 * size)
+        bias[::per], bias[1::per] = size, -size
+        logits = torch.randn(1000 if per == 2 else 40, experts, generator=g)
+        for score in ops.SCORES:
+            for topk_groups in (1, groups // 2):
+                check(logits, 2, score=score, bias=bias, groups=groups, topk_groups=topk_groups, group_top=2)
