@@ -179,3 +179,26 @@ def test_values_of_groups_whose_parts_cancel(experts, groups):
         for score in ops.SCORES:
             for topk_groups in (1, groups // 2):
                 check(logits, 2, score=score, bias=bias, groups=groups, topk_groups=topk_groups, group_top=2)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("experts", LAYOUTS)
+def test_drawn_from_few_values(experts, dtype):
+    """Rows of few different logits, equal and one step apart, around -80, 0, 17 and 40."""
+    g = gen(experts + 1)
+    log("few values", experts, dtype)
+    near = torch.tensor([0, 1, 2, 3]) * torch.finfo(dtype).eps
+    rows = []
+    for middle in (-80.0, 0.5, 17.0, 40.0):
+        for spread in (1.0, 2000.0):
+            values = torch.cat([middle * (1 + near), middle + spread * torch.finfo(dtype).eps * torch.tensor([0., 1., 2., 16.])])
+            rows.append(values[torch.randint(0, 8, (2, experts), generator=g)])
+            rows[-1][1, : experts // 2] = 0.0
+    logits = torch.cat(rows).to(dtype)
+    for k in counts(experts):
+        for score in ops.SCORES:
+            check(logits, k, score=score)
+            check(logits, k, score=score, renormalise=True)
+            check(logits, k, score=score, bias=torch.zeros(experts))
+        check(logits, k, score="sigmoid", bias=torch.full((experts,), 0.25))
+        check(logits, k, score="sigmoid", bias=(torch.arange(experts) % 3) * 0.5, renormalise=True)
