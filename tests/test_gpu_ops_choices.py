@@ -202,3 +202,21 @@ def test_drawn_from_few_values(experts, dtype):
             check(logits, k, score=score, bias=torch.zeros(experts))
         check(logits, k, score="sigmoid", bias=torch.full((experts,), 0.25))
         check(logits, k, score="sigmoid", bias=(torch.arange(experts) % 3) * 0.5, renormalise=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("experts", [8, 64, 128, 256, 300, 512, 900])
+def test_softmax_weights_are_rounded_once(experts, dtype):
+    """Weights of the softmax over all experts: exponentials and their sum to 2^-30 of themselves, their quotient in 64
+    bits, and one rounding to FP32 of at most 2^-24 of the value."""
+    g = gen(experts + 2)
+    logits = (torch.randn(500, experts, generator=g) * 2).to(dtype)
+    logits[0], logits[1, 3] = 0.125, 60.0
+    x = logits.double()
+    score = torch.exp(x - x.max(1, keepdim=True).values)
+    score = score / score.sum(1, keepdim=True)
+    for bias in (None, torch.randn(experts, generator=g).to(device()) * 0.1):
+        got = ops.route(logits.to(device()), min(experts, 10), bias=bias, scale=1.0)
+        w = torch.gather(score, 1, got.index.cpu().long())
+        off = ((got.weight.cpu().double() - w).abs() / w).max()
+        assert float(off) <= 2.0 ** -24 + 2.0 ** -28, float(off) * 2 ** 24
