@@ -33,6 +33,10 @@ int mlp_testing_pack_device_on_host(int n_layers, const int32_t *widths, const u
  * Host only; no HIP call.  Errors: INVALID_ARGUMENT, UNSUPPORTED (as mlp_packed_size). */
 int mlp_testing_plan_kernel(int n_layers, const int32_t *widths, int layout, char *name, size_t cap);
 
+/* The slots [*row0, *row1) that tile `tile` of an expert with the slots [begin, end) takes in mlp_expert_linear, as the
+ * kernels compute them.  Host only; no HIP call.  Errors: INVALID_ARGUMENT (also where there is no such tile). */
+int mlp_testing_expert_tile(int32_t begin, int32_t end, int32_t rows_per_tile, int32_t tile, int32_t *row0, int32_t *row1);
+
 #ifdef __cplusplus
 }
 #endif

@@ -39,7 +39,7 @@ EXPORTED = (
     "mlp_infer_ex", "mlp_set_activation_mode", "mlp_kernel_name", "mlp_debug_read_packed",
     "mlp_last_error", "mlp_release",
     # include/mlp_testing.h
-    "mlp_testing_pack_device_on_host", "mlp_testing_plan_kernel",
+    "mlp_testing_pack_device_on_host", "mlp_testing_plan_kernel", "mlp_testing_expert_tile",
 )
 
 
@@ -75,6 +75,7 @@ def lib() -> ctypes.CDLL:
             "mlp_release": ([], None),
             "mlp_testing_pack_device_on_host": ([i32, p, p, p, i32, p, sz, p], i32),
             "mlp_testing_plan_kernel": ([i32, p, i32, p, sz], i32),
+            "mlp_testing_expert_tile": ([i32, i32, i32, i32, p, p], i32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -220,6 +221,14 @@ def mlp_testing_plan_kernel(widths, layout: int = MLP_LAYOUT_PACKED) -> str:
     buf = ctypes.create_string_buffer(256)
     _check(lib().mlp_testing_plan_kernel(len(w) - 1, w.ctypes.data, layout, buf, 256), "mlp_testing_plan_kernel")
     return buf.value.decode()
+
+
+def mlp_testing_expert_tile(begin: int, end: int, rows_per_tile: int, tile: int):
+    """The slots (row0, row1) of a tile of an expert's slots [begin, end) (host only)."""
+    row0, row1 = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().mlp_testing_expert_tile(begin, end, rows_per_tile, tile, ctypes.addressof(row0), ctypes.addressof(row1)),
+           "mlp_testing_expert_tile")
+    return row0.value, row1.value
 
 
 # ---- torch convenience ------------------------------------------------------------------------

@@ -6,6 +6,8 @@
 #include "mlp_error.h"
 #include "mlp_ops.h"
 #include "mlp_ops_kernels.h"
+#include "mlp_ops_tiles.h"
+#include "mlp_testing.h"
 
 using mlpk::fail;
 using mlpk::hip_fail;
@@ -411,6 +413,18 @@ int mlp_expert_linear(const mlp_expert_linear_args *a, void *stream)
         if (err != hipSuccess)
             return hip_fail(err, "launching the combination");
     }
+    return ok();
+}
+
+int mlp_testing_expert_tile(int32_t begin, int32_t end, int32_t rows_per_tile, int32_t tile, int32_t *row0, int32_t *row1)
+{
+    if (!row0 || !row1)
+        return fail(MLP_ERR_INVALID_ARGUMENT, "row0 or row1 is NULL");
+    MLP_TRY(check_range("begin", begin, 0, INT32_MAX));
+    MLP_TRY(check_range("rows_per_tile", rows_per_tile, 1, INT32_MAX));
+    MLP_TRY(check_range("tile", tile, 0, (int64_t)mlpk::tiles_in(begin, end, rows_per_tile) - 1));
+    *row0 = mlpk::tile_begin(begin, rows_per_tile, tile);
+    *row1 = mlpk::tile_end(*row0, end, rows_per_tile);
     return ok();
 }
 

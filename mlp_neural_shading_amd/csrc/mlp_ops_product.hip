@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include "mlp_ops_kernels.h"
+#include "mlp_ops_tiles.h"
 
 namespace mlpk {
 
@@ -126,7 +127,7 @@ __device__ __forceinline__ int tiles_of(const int32_t *offsets, int experts, int
         return 0;
     begin = min(max(offsets[e], 0), rows);
     end = min(max(offsets[e + 1], 0), rows);
-    return end > begin ? (end - begin - 1) / bn + 1 : 0;
+    return tiles_in(begin, end, bn);
 }
 
 // Inclusive sum over the wave: within rows of 16 lanes, then row 0 into row 1 and 2 into 3, then the first half into
@@ -163,8 +164,8 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int experts, i
         if (hit) {
             const int src = __ffsll((unsigned long long)hit) - 1;
             out.expert = base + src;
-            out.row0 = __builtin_amdgcn_readlane(begin + mine * bn, src);
-            out.row1 = min(out.row0 + bn, __builtin_amdgcn_readlane(end, src));
+            out.row0 = __builtin_amdgcn_readlane(tile_begin(begin, bn, mine), src);
+            out.row1 = tile_end(out.row0, __builtin_amdgcn_readlane(end, src), bn);
             return true;
         }
         before += __builtin_amdgcn_readlane(upto, 63);
