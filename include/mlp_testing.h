@@ -37,6 +37,18 @@ int mlp_testing_plan_kernel(int n_layers, const int32_t *widths, int layout, cha
  * kernels compute them.  Host only; no HIP call.  Errors: INVALID_ARGUMENT (also where there is no such tile). */
 int mlp_testing_expert_tile(int32_t begin, int32_t end, int32_t rows_per_tile, int32_t tile, int32_t *row0, int32_t *row1);
 
+/* The kernel that mlp_linear, mlp_expert_linear or mlp_route (mlp_ops.h) would launch for this call: of the products
+ * "big", "mid", "small", "tile", "few", "few wide" or "narrow", of the router "lanes LxV" or "wave"; "none" where there is
+ * nothing to do.  The call is checked as it would be there (the router's: its sizes); pointers are not read.
+ *   name  receives the NUL-terminated name (truncated to cap - 1 characters)
+ * Host only; no HIP call.  Errors: as the call's. */
+struct mlp_linear_args;
+struct mlp_expert_linear_args;
+struct mlp_route_args;
+int mlp_testing_linear_kernel(const struct mlp_linear_args *args, char *name, size_t cap);
+int mlp_testing_expert_linear_kernel(const struct mlp_expert_linear_args *args, char *name, size_t cap);
+int mlp_testing_route_kernel(const struct mlp_route_args *args, char *name, size_t cap);
+
 #ifdef __cplusplus
 }
 #endif

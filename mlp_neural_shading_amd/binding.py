@@ -40,6 +40,7 @@ EXPORTED = (
     "mlp_last_error", "mlp_release",
     # include/mlp_testing.h
     "mlp_testing_pack_device_on_host", "mlp_testing_plan_kernel", "mlp_testing_expert_tile",
+    "mlp_testing_linear_kernel", "mlp_testing_expert_linear_kernel", "mlp_testing_route_kernel",
 )
 
 
@@ -76,6 +77,9 @@ def lib() -> ctypes.CDLL:
             "mlp_testing_pack_device_on_host": ([i32, p, p, p, i32, p, sz, p], i32),
             "mlp_testing_plan_kernel": ([i32, p, i32, p, sz], i32),
             "mlp_testing_expert_tile": ([i32, i32, i32, i32, p, p], i32),
+            "mlp_testing_linear_kernel": ([p, p, sz], i32),
+            "mlp_testing_expert_linear_kernel": ([p, p, sz], i32),
+            "mlp_testing_route_kernel": ([p, p, sz], i32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)

@@ -2,6 +2,7 @@
 #include <hip/hip_runtime_api.h>
 #include <math.h>
 #include <stdint.h>
+#include <stdio.h>
 
 #include "mlp_error.h"
 #include "mlp_ops.h"
@@ -169,15 +170,12 @@ uint64_t dispatch_need(const mlp_dispatch_args *a)
     return 4 * (uint64_t)mlpk::dispatch_workspace_entries(a->tokens * a->k, a->experts);
 }
 
-}  // namespace
-
-extern "C" {
-
-int mlp_linear(const mlp_linear_args *a, void *stream)
+// The checked call as its product; rows are left 0 where there is nothing to do.
+int prepare_linear(const mlp_linear_args *a, mlpk::ProductArgs &p)
 {
     MLP_TRY(check_linear(a));
     if (a->rows == 0)
-        return ok();
+        return MLP_OK;
     const int64_t wide = (int64_t)a->out_width * (a->gated ? 2 : 1);
     const int out_size = elem_size(a->out_dtype);
     MLP_TRY(check_matrix("x", a->x, a->rows, a->in_width, a->ldx, 2));
@@ -197,7 +195,6 @@ int mlp_linear(const mlp_linear_args *a, void *stream)
             overlap(y, span(a->residual, a->rows, a->out_width, a->ldr, out_size)))
             return fail(MLP_ERR_INVALID_ARGUMENT, "y overlaps residual without being it");
     }
-    mlpk::ProductArgs p{};
     p.x = a->x;
     p.ldx = a->ldx;
     p.w = a->w;
@@ -215,11 +212,86 @@ int mlp_linear(const mlp_linear_args *a, void *stream)
     if (!mlpk::product_fits(p, a->gated, false))
         return fail(MLP_ERR_UNSUPPORTED, "%lld rows of %d outputs are more tiles than one launch holds", (long long)a->rows,
                     a->out_width);
-    const hipError_t err = mlpk::launch_product(p, a->dtype, a->gated, false, (hipStream_t)stream);
-    return err == hipSuccess ? ok() : hip_fail(err, "launching the layer");
+    return MLP_OK;
 }
 
-int mlp_route(const mlp_route_args *a, void *stream)
+// The checked call as its product; rows are left 0 where there is nothing to do.
+int prepare_expert_linear(const mlp_expert_linear_args *a, mlpk::ProductArgs &p)
+{
+    MLP_TRY(check_expert_linear(a));
+    if (!a->combine && (a->weight || a->residual))
+        return fail(MLP_ERR_INVALID_ARGUMENT, "weight and residual go with combine");
+    const int64_t n = a->tokens * a->k;
+    if (n == 0)
+        return MLP_OK;
+    const int64_t wide = (int64_t)a->out_width * (a->gated ? 2 : 1), x_rows = a->x_slots ? n : a->tokens;
+    const int64_t y_rows = a->combine ? a->tokens : n;
+    const int out_size = elem_size(a->out_dtype);
+    MLP_TRY(check_matrix("x", a->x, x_rows, a->in_width, a->ldx, 2));
+    MLP_TRY(check_matrix("w", a->w, wide, a->in_width, a->ldw, 2));
+    if (a->experts > 1 && (a->w_stride < wide * a->ldw - (a->ldw - a->in_width) ||
+                           a->w_stride > (INT64_MAX >> 3) / a->experts))
+        return fail(MLP_ERR_INVALID_ARGUMENT, "w_stride %lld does not hold an expert's %lld rows", (long long)a->w_stride,
+                    (long long)wide);
+    MLP_TRY(check_matrix("y", a->y, y_rows, a->out_width, a->ldy, out_size));
+    MLP_TRY(check_stride("y", a->ldy));
+    if (a->bias)
+        MLP_TRY(check_vector("bias", a->bias, 2));
+    MLP_TRY(check_vector("offsets", a->offsets, 4));
+    if (!a->x_slots)
+        MLP_TRY(check_vector("slots", a->slots, 4));
+    if (a->combine)
+        MLP_TRY(check_vector("places", a->places, 4));
+    if (a->weight)
+        MLP_TRY(check_vector("weight", a->weight, 4));
+    const Span y = span(a->y, y_rows, a->out_width, a->ldy, out_size);
+    const int64_t w_cols = (a->experts - 1) * (a->experts > 1 ? a->w_stride : 0) + (wide - 1) * a->ldw + a->in_width;
+    if (overlap(y, span(a->x, x_rows, a->in_width, a->ldx, 2)) || overlap(y, span(a->w, 1, w_cols, w_cols, 2)) ||
+        overlap(y, span(a->bias, 1, wide * a->experts, wide * a->experts, 2)) ||
+        overlap(y, span(a->offsets, 1, a->experts + 1, a->experts + 1, 4)) || overlap(y, span(a->slots, 1, n, n, 4)) ||
+        overlap(y, span(a->places, 1, n, n, 4)) || overlap(y, span(a->weight, 1, n, n, 4)))
+        return fail(MLP_ERR_INVALID_ARGUMENT, "y overlaps an input");
+    if (a->residual) {
+        MLP_TRY(check_matrix("residual", a->residual, y_rows, a->out_width, a->ldr, out_size));
+        MLP_TRY(check_stride("residual", a->ldr));
+        if (!(a->residual == a->y && (a->ldr == a->ldy || y_rows == 1)) &&
+            overlap(y, span(a->residual, y_rows, a->out_width, a->ldr, out_size)))
+            return fail(MLP_ERR_INVALID_ARGUMENT, "y overlaps residual without being it");
+    }
+    const uint64_t need = expert_linear_need(a);
+    MLP_TRY(check_workspace(a->workspace, a->workspace_bytes, need));
+    const Span ws = span(need ? a->workspace : nullptr, 1, (int64_t)need, (int64_t)need, 1);
+    if (overlap(ws, y) || overlap(ws, span(a->x, x_rows, a->in_width, a->ldx, 2)) || overlap(ws, span(a->w, 1, w_cols, w_cols, 2)) ||
+        overlap(ws, span(a->bias, 1, wide * a->experts, wide * a->experts, 2)) || overlap(ws, span(a->slots, 1, n, n, 4)) ||
+        overlap(ws, span(a->offsets, 1, a->experts + 1, a->experts + 1, 4)) || overlap(ws, span(a->places, 1, n, n, 4)) ||
+        overlap(ws, span(a->weight, 1, n, n, 4)) ||
+        (a->residual && overlap(ws, span(a->residual, y_rows, a->out_width, a->ldr, out_size))))
+        return fail(MLP_ERR_INVALID_ARGUMENT, "workspace overlaps another buffer");
+    p.x = a->x;
+    p.ldx = a->ldx;
+    p.w = a->w;
+    p.ldw = a->ldw;
+    p.w_stride = a->w_stride;
+    p.bias = a->bias;
+    p.y = a->combine ? a->workspace : a->y;
+    p.ldy = a->combine ? part_stride(a->out_width) : a->ldy;
+    p.rows = n;
+    p.in = a->in_width;
+    p.out = a->out_width;
+    p.act = a->act;
+    p.y_fp32 = a->combine || a->out_dtype == MLP_DTYPE_FP32;
+    p.offsets = a->offsets;
+    p.slots = a->x_slots ? nullptr : a->slots;
+    p.experts = a->experts;
+    p.k = a->k;
+    if (!mlpk::product_fits(p, a->gated, true))
+        return fail(MLP_ERR_UNSUPPORTED, "%lld slots of %d outputs are more tiles than one launch holds", (long long)n,
+                    a->out_width);
+    return MLP_OK;
+}
+
+// The route call's sizes, without its buffers.
+int check_route(const mlp_route_args *a)
 {
     if (!a)
         return fail(MLP_ERR_INVALID_ARGUMENT, "args is NULL");
@@ -236,6 +308,34 @@ int mlp_route(const mlp_route_args *a, void *stream)
     MLP_TRY(check_range("renormalise", a->renormalise, 0, 1));
     if (!isfinite(a->scale))
         return fail(MLP_ERR_INVALID_ARGUMENT, "scale is not finite");
+    return MLP_OK;
+}
+
+int put_name(const char *text, char *name, size_t cap)
+{
+    if (!name || cap == 0)
+        return fail(MLP_ERR_INVALID_ARGUMENT, "name is NULL or empty");
+    snprintf(name, cap, "%s", text);
+    return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int mlp_linear(const mlp_linear_args *a, void *stream)
+{
+    mlpk::ProductArgs p{};
+    MLP_TRY(prepare_linear(a, p));
+    if (p.rows == 0)
+        return ok();
+    const hipError_t err = mlpk::launch_product(p, a->dtype, a->gated, false, (hipStream_t)stream);
+    return err == hipSuccess ? ok() : hip_fail(err, "launching the layer");
+}
+
+int mlp_route(const mlp_route_args *a, void *stream)
+{
+    MLP_TRY(check_route(a));
     if (a->tokens == 0)
         return ok();
     MLP_TRY(check_matrix("logits", a->logits, a->tokens, a->experts, a->ld, elem_size(a->dtype)));
@@ -323,76 +423,10 @@ int mlp_expert_linear_workspace(const mlp_expert_linear_args *a, uint64_t *bytes
 
 int mlp_expert_linear(const mlp_expert_linear_args *a, void *stream)
 {
-    MLP_TRY(check_expert_linear(a));
-    if (!a->combine && (a->weight || a->residual))
-        return fail(MLP_ERR_INVALID_ARGUMENT, "weight and residual go with combine");
-    const int64_t n = a->tokens * a->k;
-    if (n == 0)
-        return ok();
-    const int64_t wide = (int64_t)a->out_width * (a->gated ? 2 : 1), x_rows = a->x_slots ? n : a->tokens;
-    const int64_t y_rows = a->combine ? a->tokens : n;
-    const int out_size = elem_size(a->out_dtype);
-    MLP_TRY(check_matrix("x", a->x, x_rows, a->in_width, a->ldx, 2));
-    MLP_TRY(check_matrix("w", a->w, wide, a->in_width, a->ldw, 2));
-    if (a->experts > 1 && (a->w_stride < wide * a->ldw - (a->ldw - a->in_width) ||
-                           a->w_stride > (INT64_MAX >> 3) / a->experts))
-        return fail(MLP_ERR_INVALID_ARGUMENT, "w_stride %lld does not hold an expert's %lld rows", (long long)a->w_stride,
-                    (long long)wide);
-    MLP_TRY(check_matrix("y", a->y, y_rows, a->out_width, a->ldy, out_size));
-    MLP_TRY(check_stride("y", a->ldy));
-    if (a->bias)
-        MLP_TRY(check_vector("bias", a->bias, 2));
-    MLP_TRY(check_vector("offsets", a->offsets, 4));
-    if (!a->x_slots)
-        MLP_TRY(check_vector("slots", a->slots, 4));
-    if (a->combine)
-        MLP_TRY(check_vector("places", a->places, 4));
-    if (a->weight)
-        MLP_TRY(check_vector("weight", a->weight, 4));
-    const Span y = span(a->y, y_rows, a->out_width, a->ldy, out_size);
-    const int64_t w_cols = (a->experts - 1) * (a->experts > 1 ? a->w_stride : 0) + (wide - 1) * a->ldw + a->in_width;
-    if (overlap(y, span(a->x, x_rows, a->in_width, a->ldx, 2)) || overlap(y, span(a->w, 1, w_cols, w_cols, 2)) ||
-        overlap(y, span(a->bias, 1, wide * a->experts, wide * a->experts, 2)) ||
-        overlap(y, span(a->offsets, 1, a->experts + 1, a->experts + 1, 4)) || overlap(y, span(a->slots, 1, n, n, 4)) ||
-        overlap(y, span(a->places, 1, n, n, 4)) || overlap(y, span(a->weight, 1, n, n, 4)))
-        return fail(MLP_ERR_INVALID_ARGUMENT, "y overlaps an input");
-    if (a->residual) {
-        MLP_TRY(check_matrix("residual", a->residual, y_rows, a->out_width, a->ldr, out_size));
-        MLP_TRY(check_stride("residual", a->ldr));
-        if (!(a->residual == a->y && (a->ldr == a->ldy || y_rows == 1)) &&
-            overlap(y, span(a->residual, y_rows, a->out_width, a->ldr, out_size)))
-            return fail(MLP_ERR_INVALID_ARGUMENT, "y overlaps residual without being it");
-    }
-    const uint64_t need = expert_linear_need(a);
-    MLP_TRY(check_workspace(a->workspace, a->workspace_bytes, need));
-    const Span ws = span(need ? a->workspace : nullptr, 1, (int64_t)need, (int64_t)need, 1);
-    if (overlap(ws, y) || overlap(ws, span(a->x, x_rows, a->in_width, a->ldx, 2)) || overlap(ws, span(a->w, 1, w_cols, w_cols, 2)) ||
-        overlap(ws, span(a->bias, 1, wide * a->experts, wide * a->experts, 2)) || overlap(ws, span(a->slots, 1, n, n, 4)) ||
-        overlap(ws, span(a->offsets, 1, a->experts + 1, a->experts + 1, 4)) || overlap(ws, span(a->places, 1, n, n, 4)) ||
-        overlap(ws, span(a->weight, 1, n, n, 4)) ||
-        (a->residual && overlap(ws, span(a->residual, y_rows, a->out_width, a->ldr, out_size))))
-        return fail(MLP_ERR_INVALID_ARGUMENT, "workspace overlaps another buffer");
     mlpk::ProductArgs p{};
-    p.x = a->x;
-    p.ldx = a->ldx;
-    p.w = a->w;
-    p.ldw = a->ldw;
-    p.w_stride = a->w_stride;
-    p.bias = a->bias;
-    p.y = a->combine ? a->workspace : a->y;
-    p.ldy = a->combine ? part_stride(a->out_width) : a->ldy;
-    p.rows = n;
-    p.in = a->in_width;
-    p.out = a->out_width;
-    p.act = a->act;
-    p.y_fp32 = a->combine || a->out_dtype == MLP_DTYPE_FP32;
-    p.offsets = a->offsets;
-    p.slots = a->x_slots ? nullptr : a->slots;
-    p.experts = a->experts;
-    p.k = a->k;
-    if (!mlpk::product_fits(p, a->gated, true))
-        return fail(MLP_ERR_UNSUPPORTED, "%lld slots of %d outputs are more tiles than one launch holds", (long long)n,
-                    a->out_width);
+    MLP_TRY(prepare_expert_linear(a, p));
+    if (p.rows == 0)
+        return ok();
     hipError_t err = mlpk::launch_product(p, a->dtype, a->gated, true, (hipStream_t)stream);
     if (err != hipSuccess)
         return hip_fail(err, "launching the experts' layer");
@@ -426,6 +460,31 @@ int mlp_testing_expert_tile(int32_t begin, int32_t end, int32_t rows_per_tile, i
     *row0 = mlpk::tile_begin(begin, rows_per_tile, tile);
     *row1 = mlpk::tile_end(*row0, end, rows_per_tile);
     return ok();
+}
+
+int mlp_testing_linear_kernel(const mlp_linear_args *a, char *name, size_t cap)
+{
+    mlpk::ProductArgs p{};
+    MLP_TRY(prepare_linear(a, p));
+    return put_name(p.rows ? mlpk::product_kernel(p, a->gated, false) : "none", name, cap);
+}
+
+int mlp_testing_expert_linear_kernel(const mlp_expert_linear_args *a, char *name, size_t cap)
+{
+    mlpk::ProductArgs p{};
+    MLP_TRY(prepare_expert_linear(a, p));
+    return put_name(p.rows ? mlpk::product_kernel(p, a->gated, true) : "none", name, cap);
+}
+
+int mlp_testing_route_kernel(const mlp_route_args *a, char *name, size_t cap)
+{
+    MLP_TRY(check_route(a));
+    mlpk::RouteArgs r{};
+    r.experts = a->experts;
+    r.k = a->k;
+    r.groups = a->groups;
+    r.topk_groups = a->topk_groups;
+    return put_name(mlpk::route_kernel(r), name, cap);
 }
 
 }  // extern "C"

@@ -35,6 +35,9 @@ hipError_t launch_product(const ProductArgs &p, int dtype, bool gated, bool grou
 // Whether one launch holds the product's tiles.
 bool product_fits(const ProductArgs &p, bool gated, bool grouped);
 
+// The kernel that launch_product takes, for tests.
+const char *product_kernel(const ProductArgs &p, bool gated, bool grouped);
+
 // y[t] = round(sum_j weight[t][j] * part[places[t][j]] + residual[t]) over FP32 rows `part`.
 struct CombineArgs {
     const float *part;  // [slots][ldp], 16-byte aligned rows
@@ -63,6 +66,8 @@ struct RouteArgs {
     float scale;
 };
 hipError_t launch_route(const RouteArgs &r, int dtype, hipStream_t stream);
+// The kernel that launch_route takes, for tests.
+const char *route_kernel(const RouteArgs &r);
 
 struct DispatchArgs {
     const int32_t *index;

@@ -1061,6 +1061,12 @@ bool product_fits(const ProductArgs &p, bool gated, bool grouped)
     return tiles_most(p, gated, grouped, form) * kShapes[form].threads <= UINT32_MAX;  // a grid counts its threads in 32 bits
 }
 
+const char *product_kernel(const ProductArgs &p, bool gated, bool grouped)
+{
+    static const char *const names[] = {"big", "mid", "small", "tile", "few", "few wide", "narrow"};
+    return names[choose_form(p, gated, grouped)];
+}
+
 hipError_t launch_product(const ProductArgs &p, int dtype, bool gated, bool grouped, hipStream_t stream)
 {
     return dtype == kFp16 ? launch<_Float16>(p, gated, grouped, stream) : launch<__bf16>(p, gated, grouped, stream);

@@ -755,19 +755,39 @@ hipError_t launch_lanes(const RouteArgs &r, int each, hipStream_t stream)
     return err;
 }
 
+// The layout that serves this router, and its lanes per group in `each`.
+enum RouteForm { kLanes16x4, kLanes16x8, kLanes16x16, kLanes64x8, kWave };
+RouteForm choose_route(const RouteArgs &r, int &each)
+{
+    if ((each = lanes_per_group(r, 16, 4)))
+        return kLanes16x4;
+    if ((each = lanes_per_group(r, 16, 8)))
+        return kLanes16x8;
+    if ((each = lanes_per_group(r, 16, 16)))
+        return kLanes16x16;
+    if ((each = lanes_per_group(r, 64, 8)))
+        return kLanes64x8;
+    return kWave;
+}
+
 template <class T>
 hipError_t launch_route_typed(const RouteArgs &r, hipStream_t stream)
 {
+    int each;
+    switch (choose_route(r, each)) {
+    case kLanes16x4:
+        return launch_lanes<T, 16, 4>(r, each, stream);
+    case kLanes16x8:
+        return launch_lanes<T, 16, 8>(r, each, stream);
+    case kLanes16x16:
+        return launch_lanes<T, 16, 16>(r, each, stream);
+    case kLanes64x8:
+        return launch_lanes<T, 64, 8>(r, each, stream);
+    case kWave:
+        break;
+    }
     const dim3 grid((unsigned)(r.tokens < 256 * 64 ? r.tokens : 256 * 64));
     const size_t lds = (size_t)(r.experts + r.groups) * sizeof(double);
-    if (const int each = lanes_per_group(r, 16, 4))
-        return launch_lanes<T, 16, 4>(r, each, stream);
-    if (const int each = lanes_per_group(r, 16, 8))
-        return launch_lanes<T, 16, 8>(r, each, stream);
-    if (const int each = lanes_per_group(r, 16, 16))
-        return launch_lanes<T, 16, 16>(r, each, stream);
-    if (const int each = lanes_per_group(r, 64, 8))
-        return launch_lanes<T, 64, 8>(r, each, stream);
     const int vpl = (r.experts + 63) / 64;
     if (vpl <= 1)
         hipLaunchKernelGGL((route_tokens<T, 1>), grid, dim3(64), lds, stream, r);
@@ -967,6 +987,13 @@ __global__ __launch_bounds__(kThreads) void dispatch_place(DispatchArgs d, int64
 }
 
 }  // namespace
+
+const char *route_kernel(const RouteArgs &r)
+{
+    static const char *const names[] = {"lanes 16x4", "lanes 16x8", "lanes 16x16", "lanes 64x8", "wave"};
+    int each;
+    return names[choose_route(r, each)];
+}
 
 hipError_t launch_route(const RouteArgs &r, int dtype, hipStream_t stream)
 {

@@ -1,12 +1,179 @@
 """GPU tests of the single operators' kernels one by one, at what each has of its own: its tiles' borders, the
 strides and the aliases that its epilogue allows, its activations."""
+import math
+
 import pytest
 import torch
 
+import ops_kernels as K
+import ops_reference as R
 from gpu_util import device, log
 from mlp_neural_shading_amd import ops
+from test_ops_kernels_host import EXPERTS, GATED, LINEAR
 
 pytestmark = pytest.mark.gpu
+
+ALL = [(name, size) for sizes in (LINEAR, GATED) for name, size in sizes.items()]
+IDS = ["%s%s" % (name, "-gated" if size[3] else "") for name, size in ALL]
+BOTH = pytest.mark.parametrize("name,size", ALL, ids=IDS)
+HALF = {"fp16": torch.float16, "bf16": torch.bfloat16}
+
+
+def gen(seed):
+    return torch.Generator(device=device()).manual_seed(seed)
+
+
+def rnd(g, *shape, dtype, scale=1.0):
+    return (torch.randn(*shape, generator=g, device=device()) * scale).to(dtype)
+
+
+def ran(name, x, w, gated):
+    """Asserts that the layer of these operands is the kernel's that the test speaks of."""
+    rows, k = x.shape
+    n = w.shape[0] // (2 if gated else 1)
+    assert K.linear_kernel(rows, k, n, gated, x.stride(0) if rows > 1 else k, w.stride(0), x.data_ptr() % 16 + K.FAR,
+                           w.data_ptr() % 16 + 2 * K.FAR) == name
+
+
+def block(t, left, right, fill):
+    """t as a column block of a wider matrix, whose other columns hold `fill`."""
+    wide = torch.full((t.shape[0], left + t.shape[1] + right), fill, dtype=t.dtype, device=t.device)
+    wide[:, left:left + t.shape[1]] = t
+    return wide, wide[:, left:left + t.shape[1]]
+
+
+def layer(name, size, t, seed):
+    rows, k, n, gated = size
+    g, wide = gen(seed), n * (2 if gated else 1)
+    x, w = rnd(g, rows, k, dtype=t), rnd(g, wide, k, dtype=t, scale=k ** -0.5)
+    ran(name, x, w, gated)
+    return x, w, rnd(g, wide, dtype=t), rnd(g, rows, n, dtype=t)
+
+
+@BOTH
+def test_strides_and_residual_in_place(name, size):
+    """y, residual, x and w as column blocks of wider matrices, which hold NaN around the inputs and keep what they
+    hold around the outputs; the residual beside y and as y itself.  The bits are those of the plain matrices, whose
+    values are checked against 64 bits."""
+    rows, k, n, gated = size
+    log("strides", name, size)
+    for t in HALF.values():
+        for out in (t, torch.float32):
+            x, w, b, r = layer(name, size, t, 1)
+            r = r.to(out)
+            want = ops.linear(x, w, b, residual=r, act="leaky_relu", gated=gated, out_dtype=out)
+            if out == t:
+                some = torch.cat([torch.arange(0, min(rows, 300)), torch.arange(max(0, rows - 300), rows)])
+                R.check(want[some.to(device())], *R.linear64(x[some], w, b, r[some], "leaky_relu", gated), t, "plain")
+            for left, right in ((8, 8), (2, 4)):
+                _, xv = block(x, left, right, math.nan)
+                _, wv = block(w, left, right + 2, math.nan)
+                ran(name, xv, wv, gated)
+                for l2, r2 in ((left, right), (1, 2), (3, 0)):
+                    _, rv = block(r, l2, r2, math.nan)
+                    whole, y = block(torch.zeros_like(r), l2 + 1, r2, 7.0)
+                    ops.linear(xv, wv, b, residual=rv, act="leaky_relu", gated=gated, out=y, out_dtype=out)
+                    assert torch.equal(y, want)
+                    keep = torch.cat([whole[:, :l2 + 1], whole[:, l2 + 1 + n:]], 1)
+                    assert bool((keep == 7).all())
+                    whole, y = block(r, l2, r2, 7.0)
+                    ops.linear(xv, wv, b, residual=y, act="leaky_relu", gated=gated, out=y, out_dtype=out)
+                    assert torch.equal(y, want)
+                    keep = torch.cat([whole[:, :l2], whole[:, l2 + n:]], 1)
+                    assert bool((keep == 7).all())
+
+
+@pytest.mark.parametrize("name", ["few", "few wide", "small", "mid", "big", "tile"])
+def test_the_largest_strides(name):
+    """Rows of y as far apart as they may be, the residual in place, and rows of x beyond 2^31 elements in all; a lane's
+    offset within a tile is 32 bits."""
+    rows, k, n, gated = {"big": (1100, 200, 8200, False), "tile": (1100, 200, 801, False)}.get(name, LINEAR[name])
+    t, ld = torch.float16, 1 << 24
+    g = gen(2)
+    x, w, r = rnd(g, rows, k, dtype=t), rnd(g, n, k, dtype=t, scale=k ** -0.5), rnd(g, rows, n, dtype=t)
+    far = torch.empty(rows * ld, dtype=t, device=device())
+    step = ld if name != "tile" else ld - 1
+    xv, y = far.as_strided((rows, k), (step, 1), 16384), far.as_strided((rows, n), (step, 1))
+    xv.copy_(x)
+    y.copy_(r)
+    ran(name, xv, w, gated)
+    log("largest strides", name, rows, k, n)
+    ops.linear(xv, w, residual=y, act="relu", out=y)
+    if name == "tile":
+        x = block(x, 1, 0, 0)[1]  # odd rows too
+    ran(name, x, w, gated)
+    assert torch.equal(y, ops.linear(x, w, residual=r, act="relu"))
+
+
+@BOTH
+def test_nan_and_infinity_stay_in_their_rows(name, size):
+    rows, k, n, gated = size
+    x, w, b, r = layer(name, size, torch.bfloat16, 3)
+    log("nan and infinity", name, size)
+    clean = ops.linear(x, w, b, residual=r, act="relu", gated=gated)
+    assert bool(torch.isfinite(clean).all())
+    bad = [1, rows // 2, rows - 1]
+    x[bad[0], k // 2], x[bad[1], k - 1], x[bad[2], 0] = math.nan, math.inf, -math.inf
+    y = ops.linear(x, w, b, residual=r, act="none", gated=gated)
+    assert bool(torch.isnan(y[bad[0]]).all()) and not bool(torch.isfinite(y[bad[1:]]).any())
+    y = ops.linear(x, w, b, residual=r, act="relu", gated=gated)
+    keep = torch.ones(rows, dtype=torch.bool, device=device())
+    keep[bad] = False
+    assert torch.equal(y[keep], clean[keep]) and bool(torch.isnan(y[bad[0]]).all())
+
+
+def values(t):
+    """Numbers of a type that an activation sees, to both sides: small, ordinary, large, zeros, subnormals."""
+    v = torch.cat([torch.linspace(-6, 6, 20001), torch.linspace(-30, 30, 9001), torch.linspace(-100, 100, 2001),
+                   2.0 ** torch.arange(-24, 15), -(2.0 ** torch.arange(-24, 15)), torch.tensor([0.0, -0.0, 1.0, -1.0])])
+    return v.to(t)
+
+
+def through_unit_weights(size, t, gated):
+    """A layer whose sums are single inputs, exactly: weight row o takes column o % K, and the row that it gates column
+    (o + 7) % K.  (x, w, the sums [rows, n], the factors or None)."""
+    rows, k, n, _ = size
+    v = values(t)
+    x = v[torch.arange(rows * k) % v.numel()].view(rows, k).to(device())
+    o = torch.arange(n, device=device())
+    wide = n * (2 if gated else 1)
+    w = torch.zeros(wide, k, dtype=t, device=device())
+    w[o, o % k] = 1
+    if gated:
+        w[n + o, (o + 7) % k] = 1
+    return x, w, x[:, o % k], x[:, (o + 7) % k] if gated else None
+
+
+def act64(z, act):
+    """(value, bound before the rounding): GELU within 0.5 (2^-20 |y| + 2^-22 |z|), leaky ReLU by half a step."""
+    z = z.double()
+    y = R.act64(z, act)
+    if act == "gelu":
+        return y, 0.5 * (2.0 ** -20 * y.abs() + 2.0 ** -22 * z.abs())
+    return y, y.abs() * 2.0 ** -24
+
+
+def close(got, want, bound, t, what):
+    lim = R.rounded(want, bound, t)
+    fine = ((got.double() - want).abs() <= lim) | (want.abs() > torch.finfo(t).max) & torch.isinf(got)
+    assert bool(fine.all()), (what, int((~fine).sum()), float(((got.double() - want).abs() / lim)[~fine].max()))
+
+
+@pytest.mark.parametrize("act", ["none", "leaky_relu", "relu", "gelu"])
+@BOTH
+def test_activations(name, size, act):
+    """Of exact sums, in each kernel, to both 16-bit types."""
+    rows, k, n, gated = size
+    log("activation", name, size, act)
+    for t in HALF.values():
+        x, w, z, u = through_unit_weights(size, t, gated)
+        ran(name, x, w, gated)
+        y = ops.linear(x, w, act=act, gated=gated)
+        want, bound = act64(z, act)
+        if gated:
+            u = u.double()
+            want, bound = want * u, bound * u.abs() + 2.0 ** -24 * (want * u).abs()
+        close(y, want, bound, t, act)
 
 
 def test_the_last_slots_of_2_to_the_31():
@@ -26,3 +193,37 @@ def test_the_last_slots_of_2_to_the_31():
         part = slice(i, min(i + (1 << 28), n - last))
         assert torch.equal(y[part], x[part] * 3)
     assert torch.equal(y[-last:], x[-last:] * 5)
+
+
+@pytest.mark.parametrize("name", EXPERTS)
+def test_experts_strides_and_residual_in_place(name):
+    """The same of the experts' layers, by slot and combined: the bits of the plain matrices, and nothing written around."""
+    tokens, k, experts, k_in, n, gated = EXPERTS[name]
+    log("experts", name, EXPERTS[name])
+    for t in HALF.values():
+        g, wide = gen(5), n * (2 if gated else 1)
+        x, w = rnd(g, tokens, k_in, dtype=t), rnd(g, experts, wide, k_in, dtype=t, scale=k_in ** -0.5)
+        b, r = rnd(g, experts, wide, dtype=t), rnd(g, tokens, n, dtype=t)
+        index = torch.randint(-1, experts, (tokens, k), generator=g, device=device(), dtype=torch.int32)
+        plan = ops.dispatch(index, experts)
+        used = int(plan.offsets[-1])
+        by_slot = ops.expert_linear(x, w, plan, b, k=k, act="relu", gated=gated)
+        combined = ops.expert_linear(x, w, plan, b, k=k, act="relu", gated=gated, combine=True, residual=r)
+        if tokens < 10000:
+            want, bound, _ = R.experts64(x, w, tuple(plan), k, b, "relu", gated)
+            R.check(by_slot[:used], want[:used], bound[:used], t, "by slot")
+        pad = 2 if k_in % 2 == 0 else 1  # odd rows stay odd
+        _, xv = block(x, pad, 2 * pad, math.nan)
+        around = torch.full((experts, wide + 3, k_in + 4), math.nan, dtype=t, device=device())
+        around[:, 1:wide + 1, 2:2 + k_in] = w
+        wv = around[:, 1:wide + 1, 2:2 + k_in]
+        assert K.expert_kernel(tokens, k, experts, k_in, n, gated, xv.stride(0), wv.stride(1), wv.stride(0) if name != "tile" else None,
+                               xv.data_ptr() % 16 + K.FAR, wv.data_ptr() % 16 + 2 * K.FAR) == name
+        whole, y = block(torch.zeros_like(by_slot), 3, 2, 7.0)
+        ops.expert_linear(xv, wv, plan, b, k=k, act="relu", gated=gated, out=y)
+        assert torch.equal(y[:used], by_slot[:used]) and bool((y[used:] == 0).all())
+        assert bool((whole[:, :3] == 7).all()) and bool((whole[:, 3 + n:] == 7).all())
+        whole, y = block(r, 1, 4, 7.0)
+        ops.expert_linear(xv, wv, plan, b, k=k, act="relu", gated=gated, combine=True, residual=y, out=y)
+        assert torch.equal(y, combined)
+        assert bool((whole[:, :1] == 7).all()) and bool((whole[:, 1 + n:] == 7).all())
