@@ -58,6 +58,14 @@ __device__ __forceinline__ float gelu(float v)
     return fmaf(-fminf(a, 100.0f), h, fmaxf(v, 0.0f));  // infinity times 0 would be NaN; a NaN is in h
 }
 
+// v / (1 + exp(-v)), as v (2^-32 / (2^-32 + 2^-32 exp(-v))): the reciprocal's argument stays below 2^126 down to v = -109, so
+// that its result, normal or 0, is 0 only where the quotient is below FP32 too.
+__device__ __forceinline__ float silu(float v)
+{
+    const float e = __builtin_amdgcn_exp2f(fmaf(v, -1.44269504088896340736f, -32.0f));
+    return v * (__builtin_amdgcn_rcpf(0x1p-32f + e) * 0x1p-32f);
+}
+
 // Calls f with the epilogue's activation (MLP_EPI_*), FP32 to FP32; NaN stays NaN.  The choice is made once for a
 // tile of sums.  (Once for all of a wave's tiles, the compiler merges 128 sums from five branches and spills them.)
 template <class F>
@@ -74,7 +82,7 @@ __device__ __forceinline__ void with_activation(int act, F f)
         f([](float v) { return gelu(v); });
         break;
     case 4:
-        f([](float v) { return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896340736f)); });
+        f([](float v) { return silu(v); });
         break;
     default:
         f([](float v) { return v; });

@@ -145,11 +145,15 @@ def through_unit_weights(size, t, gated):
 
 
 def act64(z, act):
-    """(value, bound before the rounding): GELU within 0.5 (2^-20 |y| + 2^-22 |z|), leaky ReLU by half a step."""
+    """(value, bound before the rounding): GELU within 0.5 (2^-20 |y| + 2^-22 |z|); SiLU's argument of exp2 is rounded
+    twice, by 2^-24 of |z| log2(e) and of 32 more, exp2, the sum, the reciprocal and the products by 2^-23 each at
+    most; leaky ReLU by half a step."""
     z = z.double()
     y = R.act64(z, act)
     if act == "gelu":
         return y, 0.5 * (2.0 ** -20 * y.abs() + 2.0 ** -22 * z.abs())
+    if act == "silu":
+        return y, y.abs() * 2.0 ** -24 * (2 * z.abs() + 32 + 8)
     return y, y.abs() * 2.0 ** -24
 
 
@@ -159,7 +163,7 @@ def close(got, want, bound, t, what):
     assert bool(fine.all()), (what, int((~fine).sum()), float(((got.double() - want).abs() / lim)[~fine].max()))
 
 
-@pytest.mark.parametrize("act", ["none", "leaky_relu", "relu", "gelu"])
+@pytest.mark.parametrize("act", ops.ACTIVATIONS)
 @BOTH
 def test_activations(name, size, act):
     """Of exact sums, in each kernel, to both 16-bit types."""
