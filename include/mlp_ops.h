@@ -35,7 +35,7 @@ enum {
     MLP_DTYPE_FP32 = 2
 };
 
-/* Activations of the epilogue, computed in FP32 on the FP32 sum. */
+/* Activations of the epilogue, computed in FP32 on the FP32 sum v: GELU is off by at most 3 * 2^-24 of |v|. */
 enum {
     MLP_EPI_NONE = 0,
     MLP_EPI_LEAKY_RELU = 1, /* v < 0 ? v * half(0.01) : v, the slope of mlp.h's networks */

@@ -145,13 +145,13 @@ def through_unit_weights(size, t, gated):
 
 
 def act64(z, act):
-    """(value, bound before the rounding): GELU within 0.5 (2^-20 |y| + 2^-22 |z|); SiLU's argument of exp2 is rounded
+    """(value, bound before the rounding): GELU within 3 * 2^-24 of |z|; SiLU's argument of exp2 is rounded
     twice, by 2^-24 of |z| log2(e) and of 32 more, exp2, the sum, the reciprocal and the products by 2^-23 each at
     most; leaky ReLU by half a step."""
     z = z.double()
     y = R.act64(z, act)
     if act == "gelu":
-        return y, 0.5 * (2.0 ** -20 * y.abs() + 2.0 ** -22 * z.abs())
+        return y, 3 * 2.0 ** -24 * z.abs()
     if act == "silu":
         return y, y.abs() * 2.0 ** -24 * (2 * z.abs() + 32 + 8)
     return y, y.abs() * 2.0 ** -24
@@ -197,6 +197,47 @@ def test_the_last_slots_of_2_to_the_31():
         part = slice(i, min(i + (1 << 28), n - last))
         assert torch.equal(y[part], x[part] * 3)
     assert torch.equal(y[-last:], x[-last:] * 5)
+
+
+@pytest.mark.parametrize("act", ["none", "leaky_relu", "relu", "gelu"])
+@BOTH
+def test_activations_into_fp32(name, size, act):
+    """FP32 outputs, to a few roundings of FP32.  GELU as max(v, 0) - |v| h: h = 2^P is off by the roundings of P (the last
+    by half a step of |P|, those before and the fit by as much again, all times ln 2) and by a step of exp2's, the
+    result by half a step."""
+    rows, k, n, gated = size
+    log("activation into fp32", name, size, act)
+    for t in HALF.values():
+        x, w, z, u = through_unit_weights(size, t, gated)
+        ran(name, x, w, gated)
+        y = ops.linear(x, w, act=act, gated=gated, out_dtype=torch.float32)
+        z = z.double()
+        want = R.act64(z, act)
+        if act == "gelu":
+            h = 0.5 * torch.erfc(z.abs() / math.sqrt(2))
+            want = z.clamp(min=0) - z.abs() * h  # 1 + erf cancels in 64 bits too
+            steps = 2.1 * (-torch.log2(h.clamp(min=2.0 ** -160))).clamp(min=1) + 2
+            bound = want.abs() * 2.0 ** -24 + z.abs() * h * torch.where(z.abs() < 5.6, 2.0 ** -24 * steps, 1)  # h < 2^-26
+        else:
+            bound = want.abs() * 2.0 ** -24
+        if gated:
+            u = u.double()
+            want, bound = want * u, bound * u.abs() + 2.0 ** -24 * (want * u).abs()
+        off = (y.double() - want).abs()
+        lim = bound + 2.0 ** -149
+        assert bool((off <= lim).all()), (int((off > lim).sum()), float((off / lim).max()))
+
+
+@pytest.mark.parametrize("act", ["gelu"])
+def test_activations_of_experts_into_fp32(act):
+    """By slot and combined: the layer's own bits for k = 1."""
+    x, w, z, _ = through_unit_weights((500, 64, 40, False), torch.bfloat16, False)
+    w = torch.stack([w, w])
+    plan = ops.dispatch((torch.arange(500, device=device()) % 2).int()[:, None], 2)
+    want = ops.linear(x, w[0], act=act, out_dtype=torch.float32)
+    by_slot = ops.expert_linear(x, w, plan, k=1, act=act, out_dtype=torch.float32)
+    assert torch.equal(by_slot[plan.places.long()], want)
+    assert torch.equal(ops.expert_linear(x, w, plan, k=1, act=act, combine=True, out_dtype=torch.float32), want)
 
 
 @pytest.mark.parametrize("name", EXPERTS)
