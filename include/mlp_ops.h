@@ -35,7 +35,8 @@ enum {
     MLP_DTYPE_FP32 = 2
 };
 
-/* Activations of the epilogue, computed in FP32 on the FP32 sum v: GELU is off by at most 3 * 2^-24 of |v|. */
+/* Activations of the epilogue, computed in FP32 on the FP32 sum v: GELU is off by at most 3 * 2^-24 of |v|, SiLU by
+ * 10 * 2^-24 of its value, but by (2 |v| + 40) * 2^-24 of it before the rounding to a 16-bit output. */
 enum {
     MLP_EPI_NONE = 0,
     MLP_EPI_LEAKY_RELU = 1, /* v < 0 ? v * half(0.01) : v, the slope of mlp.h's networks */

@@ -170,6 +170,12 @@ uint64_t dispatch_need(const mlp_dispatch_args *a)
     return 4 * (uint64_t)mlpk::dispatch_workspace_entries(a->tokens * a->k, a->experts);
 }
 
+// The kernels' activation.
+int activation(int act, int out_dtype)
+{
+    return act == MLP_EPI_SILU && out_dtype == MLP_DTYPE_FP32 ? mlpk::kSiluFull : act;
+}
+
 // The checked call as its product; rows are left 0 where there is nothing to do.
 int prepare_linear(const mlp_linear_args *a, mlpk::ProductArgs &p)
 {
@@ -207,7 +213,7 @@ int prepare_linear(const mlp_linear_args *a, mlpk::ProductArgs &p)
     p.rows = a->rows;
     p.in = a->in_width;
     p.out = a->out_width;
-    p.act = a->act;
+    p.act = activation(a->act, a->out_dtype);
     p.y_fp32 = a->out_dtype == MLP_DTYPE_FP32;
     if (!mlpk::product_fits(p, a->gated, false))
         return fail(MLP_ERR_UNSUPPORTED, "%lld rows of %d outputs are more tiles than one launch holds", (long long)a->rows,
@@ -278,7 +284,7 @@ int prepare_expert_linear(const mlp_expert_linear_args *a, mlpk::ProductArgs &p)
     p.rows = n;
     p.in = a->in_width;
     p.out = a->out_width;
-    p.act = a->act;
+    p.act = activation(a->act, a->out_dtype);
     p.y_fp32 = a->combine || a->out_dtype == MLP_DTYPE_FP32;
     p.offsets = a->offsets;
     p.slots = a->x_slots ? nullptr : a->slots;

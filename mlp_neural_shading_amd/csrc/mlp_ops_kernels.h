@@ -21,13 +21,15 @@ struct ProductArgs {
     int64_t ldy;
     int64_t rows;  // dense: rows; grouped: slots, in use or not (tokens * k)
     int in, out;   // widths; a gated layer's w has 2 * out rows
-    int act;       // MLP_EPI_*
+    int act;       // MLP_EPI_*, or kSiluFull
     int y_fp32;    // 1: y and residual are FP32, 0: of the inputs' type
     // grouped only
     const int32_t *offsets;  // [experts + 1]
     const int32_t *slots;    // the assignment of each slot, or NULL: x is by slot
     int experts, k;
 };
+
+enum { kSiluFull = 5 };  // SiLU for FP32 outputs: the other form is exact to well below a 16-bit rounding only
 
 enum { kFp16 = 0, kBf16 = 1, kFp32 = 2 };  // MLP_DTYPE_*
 

@@ -41,8 +41,7 @@ __device__ __forceinline__ f4 mfma16(b8 a, b8 b, f4 c) { return __builtin_amdgcn
 // a polynomial of degree 10, fitted to log2 h on [0, 5.6] by weighted least squares, the weights moved until the error is
 // level: 4e-8 of P, or where |P| < 1 of 1.  With P's roundings in FP32 and the exponential's, h is off by at most
 // (2.1 max(1, |P|) + 2) 2^-24 of itself: FP32's accuracy, and better than 1 + erf, which cancels, for negative v.  P falls
-// ever faster beyond 5.6.  (Degree 8, 2^-16 of h: 191 us for 65,536 x 1,024
-// -> 1,024 with a residual, 193 with this.)
+// ever faster beyond 5.6.  (Degree 8, 2^-16 of h: 191 us for 65,536 x 1,024 -> 1,024 with a residual, 193 with this.)
 // One exponential and 13 full-rate operations; the activation of a 256 x 256 tile is not hidden by its matrix products.
 __device__ __forceinline__ float gelu(float v)
 {
@@ -70,8 +69,25 @@ __device__ __forceinline__ float silu(float v)
     return v * (__builtin_amdgcn_rcpf(0x1p-32f + e) * 0x1p-32f);
 }
 
-// Calls f with the epilogue's activation (MLP_EPI_*), FP32 to FP32; NaN stays NaN.  The choice is made once for a
-// tile of sums, by comparisons: a table of jumps cost 5 us of 159 in 65,536 x 1,024 -> 1,024 with SiLU.  (Once for all of a wave's tiles, the compiler merges 128 sums from five branches and spills them.)
+// The same for FP32 outputs, to a few roundings: exp(-|v|) from exp2 of the product with log2(e) and of what that rounds
+// away, scaled where it is subnormal; the quotient with a step of Newton's.  (65,536 x 1,024 -> 1,024 into FP32: 205 us;
+// 218 as expf and a division, 190 with the other form.)
+__device__ __forceinline__ float silu_full(float v)
+{
+#pragma clang fp contract(off)  // p + 64 is of the rounded p
+    const float a = fminf(fabsf(v), 200.0f);  // a NaN is in the last product
+    const float p = a * -1.44269504088896340736f;
+    const float rest = fmaf(a, -1.92596299e-08f, fmaf(a, -1.44269504088896340736f, -p));  // log2(e) in two parts
+    const bool small = p < -120.0f;
+    float e = __builtin_amdgcn_exp2f(small ? p + 64.0f : p);
+    e = fmaf(e, rest * 0.693147180559945f, e) * (small ? 0x1p-64f : 1.0f);
+    const float d = 1.0f + e, r = __builtin_amdgcn_rcpf(d), n = v < 0.0f ? e : 1.0f, q = n * r;
+    return v * fmaf(fmaf(-d, q, n), r, q);
+}
+
+// Calls f with the epilogue's activation (MLP_EPI_*, kSiluFull), FP32 to FP32; NaN stays NaN.  The choice is made once
+// for a tile of sums, by comparisons: a table of jumps cost 5 us of 159 in 65,536 x 1,024 -> 1,024 with SiLU.  (Once for
+// all of a wave's tiles, the compiler merges 128 sums from six branches and spills them.)
 template <class F>
 __device__ __forceinline__ void with_activation(int act, F f)
 {
@@ -83,8 +99,10 @@ __device__ __forceinline__ void with_activation(int act, F f)
         f([](float v) { return v < 0.0f ? 0.0f : v; });
     else if (act == 3)
         f([](float v) { return gelu(v); });
-    else
+    else if (act == 4)
         f([](float v) { return silu(v); });
+    else
+        f([](float v) { return silu_full(v); });
 }
 
 template <int V>

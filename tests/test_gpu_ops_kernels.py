@@ -199,12 +199,13 @@ def test_the_last_slots_of_2_to_the_31():
     assert torch.equal(y[-last:], x[-last:] * 5)
 
 
-@pytest.mark.parametrize("act", ["none", "leaky_relu", "relu", "gelu"])
+@pytest.mark.parametrize("act", ops.ACTIVATIONS)
 @BOTH
 def test_activations_into_fp32(name, size, act):
     """FP32 outputs, to a few roundings of FP32.  GELU as max(v, 0) - |v| h: h = 2^P is off by the roundings of P (the last
     by half a step of |P|, those before and the fit by as much again, all times ln 2) and by a step of exp2's, the
-    result by half a step."""
+    result by half a step.  SiLU: exp by two steps, and the argument's second part, the sum, the reciprocal's step of
+    Newton's and two products by half a step each, and what lies below FP32's smallest normal number."""
     rows, k, n, gated = size
     log("activation into fp32", name, size, act)
     for t in HALF.values():
@@ -218,6 +219,8 @@ def test_activations_into_fp32(name, size, act):
             want = z.clamp(min=0) - z.abs() * h  # 1 + erf cancels in 64 bits too
             steps = 2.1 * (-torch.log2(h.clamp(min=2.0 ** -160))).clamp(min=1) + 2
             bound = want.abs() * 2.0 ** -24 + z.abs() * h * torch.where(z.abs() < 5.6, 2.0 ** -24 * steps, 1)  # h < 2^-26
+        elif act == "silu":
+            bound = want.abs() * 2.0 ** -24 * 10 + z.abs() * 2.0 ** -148
         else:
             bound = want.abs() * 2.0 ** -24
         if gated:
@@ -228,7 +231,7 @@ def test_activations_into_fp32(name, size, act):
         assert bool((off <= lim).all()), (int((off > lim).sum()), float((off / lim).max()))
 
 
-@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
 def test_activations_of_experts_into_fp32(act):
     """By slot and combined: the layer's own bits for k = 1."""
     x, w, z, _ = through_unit_weights((500, 64, 40, False), torch.bfloat16, False)
