@@ -4,7 +4,7 @@ the experts' layers on routed rows (``expert_linear``), beside ``binding.infer``
 
 Each checks its tensors, takes outputs and scratch memory from torch's allocator on the current stream and
 enqueues the HIP kernels there; nothing here computes, and nothing waits.  Inference only: inputs that
-require gradients are refused while autograd records.  A run of them together, a layer of experts::
+require gradients are refused while autograd records, and so are forward-mode duals.  A run of them together, a layer of experts::
 
     index, weight = ops.route(ops.linear(x, w_router, out_dtype=torch.float32), k)
     plan = ops.dispatch(index, experts)
@@ -18,6 +18,7 @@ import struct
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as B
 
@@ -139,19 +140,21 @@ def _tensor(name, t, dims, dtypes, device=None):
     if t.dim() != dims or t.dtype not in dtypes:
         raise ValueError("%s must be %d-D of type %s, got %d-D %s" % (name, dims, " or ".join(str(d) for d in dtypes),
                                                                     t.dim(), t.dtype))
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("%s requires a gradient: these operators are for inference (torch.no_grad())" % name)
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError("%s carries a tangent: these operators are for inference (forward_ad.unpack_dual)" % name)
     if not t.is_cuda:
         raise ValueError("%s must be on the GPU" % name)
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError("%s requires a gradient: these operators are for inference (torch.no_grad())" % name)
     return t
 
 
 def _matrix(name, t, dtypes, device=None, rows=None, cols=None):
     """The row stride of a 2-D tensor with contiguous rows, after checking it."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda or (
-            device is not None and t.device != device) or t.requires_grad:
+            device is not None and t.device != device) or t.requires_grad or forward_ad._current_level >= 0:
         _tensor(name, t, 2, dtypes, device)
     r, c = t.shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):

@@ -4,6 +4,7 @@ import math
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fa
 
 import ops_kernels as K
 import ops_reference as R
@@ -275,3 +276,28 @@ def test_experts_strides_and_residual_in_place(name):
         ops.expert_linear(xv, wv, plan, b, k=k, act="relu", gated=gated, combine=True, residual=y, out=y)
         assert torch.equal(y, combined)
         assert bool((whole[:, :1] == 7).all()) and bool((whole[:, 1 + n:] == 7).all())
+
+
+def test_forward_mode_duals_are_refused_anywhere():
+    t = torch.bfloat16
+    x, w, b = torch.ones(4, 8, dtype=t, device=device()), torch.ones(6, 8, dtype=t, device=device()), torch.ones(6, dtype=t, device=device())
+    r = torch.zeros(4, 6, dtype=t, device=device())
+    weight = torch.ones(4, 1, device=device())
+    plan = ops.dispatch(torch.zeros(4, 1, dtype=torch.int32, device=device()), 1)
+    want = ops.linear(x, w, b, residual=r)
+    calls = [lambda **d: ops.linear(d.get("x", x), d.get("w", w), d.get("b", b), residual=d.get("r", r)),
+             lambda **d: ops.expert_linear(d.get("x", x), d["w"][None] if "w" in d else w[None], plan, d["b"][None] if "b" in d else b[None],
+                                           k=1, combine=True, weight=d.get("weight", weight), residual=d.get("r", r))]
+    with fa.dual_level():
+        for call, names in zip(calls, ("x w b r", "x w b r weight")):
+            for name in names.split():
+                plain = locals()[name]
+                with pytest.raises(ValueError, match="tangent"):
+                    call(**{name: fa.make_dual(plain, torch.ones_like(plain))})
+            assert torch.equal(call(), want)
+            assert torch.equal(call(x=fa.unpack_dual(fa.make_dual(x, torch.ones_like(x))).primal), want)
+        logits = torch.zeros(2, 4, device=device())
+        with pytest.raises(ValueError, match="tangent"):
+            ops.route(fa.make_dual(logits, logits), 2)
+        with pytest.raises(ValueError, match="tangent"):
+            ops.route(logits, 2, bias=fa.make_dual(logits[0], logits[0]))

@@ -1,8 +1,11 @@
 """Host-side checks of what the single operators' kernels compute about sizes (no GPU needed)."""
 import pytest
+import torch
+import torch.autograd.forward_ad as fa
 
 import ops_kernels as K
 from mlp_neural_shading_amd import binding as B
+from mlp_neural_shading_amd import ops
 
 MOST = 2 ** 31 - 1
 
@@ -72,3 +75,17 @@ def test_kernel_names_are_checked_calls():
                  lambda: K.route_kernel(8, 9)):
         with pytest.raises(B.MlpError):
             call()
+
+
+def test_forward_mode_duals_are_refused():
+    """A dual tensor does not require a gradient, and its tangent would be lost."""
+    x, t = torch.ones(4, 8, dtype=torch.float16), torch.ones(4, 8, dtype=torch.float16)
+    with fa.dual_level():
+        dual = fa.make_dual(x, t)
+        for call in (lambda v: ops.linear(v, v), lambda v: ops.route(v, 2), lambda v: ops.expert_linear(v, v[None], None, k=2)):
+            with pytest.raises(ValueError, match="tangent"):
+                call(dual)
+            with pytest.raises(ValueError, match="on the GPU"):
+                call(x)
+            with torch.no_grad(), pytest.raises(ValueError, match="tangent"):
+                call(dual)
