@@ -14,6 +14,7 @@ require gradients are refused while autograd records, and so are forward-mode du
 from __future__ import annotations
 
 import ctypes
+import operator
 import struct
 from typing import NamedTuple, Optional
 
@@ -180,6 +181,13 @@ def _choice(name, value, choices):
         raise ValueError("%s must be one of %s, got %r" % (name, ", ".join(choices), value)) from None
 
 
+def _count(name, value):
+    try:
+        return operator.index(value)
+    except TypeError:
+        raise ValueError("%s must be a whole number, got %r" % (name, value)) from None
+
+
 def _out_dtype(dtype, out_dtype):
     if out_dtype is None:
         return dtype
@@ -231,10 +239,10 @@ def route(logits, k, *, score="softmax", bias=None, groups=1, topk_groups=None, 
     of their ``group_top`` (1 or 2) best are chosen from.  -inf and NaN logits are never chosen.  Without a bias and
     without ``group_top`` 2 the logits themselves are compared, else the choices to about 50 bits; a token's row does
     not depend on the others."""
+    k = _count("k", k)
     ld = _matrix("logits", logits, _FLOATS)
     tokens, experts = logits.shape
     device = logits.device
-    k = int(k)
     room = k if 0 < k <= MLP_OPS_MAX_TOPK else 0  # others are refused below
     index = torch.empty(tokens, room, dtype=torch.int32, device=device)
     weight = torch.empty(tokens, room, dtype=torch.float32, device=device)
@@ -250,11 +258,12 @@ def route(logits, k, *, score="softmax", bias=None, groups=1, topk_groups=None, 
 def dispatch(index, experts) -> Dispatch:
     """The order of the assignments in ``index`` (int32 [tokens, k], contiguous) by expert: a stable sort.
     Indices outside 0 .. experts - 1 take no slot."""
+    experts = _count("experts", experts)
     _tensor("index", index, 2, (torch.int32,))
     if not index.is_contiguous():
         raise ValueError("index must be contiguous")
     tokens, k = index.shape
-    device, n, experts = index.device, index.numel(), int(experts)
+    device, n = index.device, index.numel()
     offsets = torch.empty(experts + 1 if 0 < experts <= MLP_OPS_MAX_EXPERTS else 0, dtype=torch.int32, device=device)
     slots = torch.empty(n, dtype=torch.int32, device=device)
     places = torch.empty_like(slots)
@@ -275,6 +284,7 @@ def expert_linear(x, w, plan: Dispatch, bias=None, *, k, act="none", gated=False
     the sum of its experts' outputs by ``weight`` (float32 [tokens, k], or 1), plus ``residual``."""
     if rows not in ("tokens", "slots"):
         raise ValueError("rows must be tokens or slots, got %r" % (rows,))
+    k = _count("k", k)
     ldx = _matrix("x", x, _HALF)
     device, dtype, k_in = x.device, x.dtype, x.shape[1]
     _tensor("w", w, 3, (dtype,), device)
@@ -284,7 +294,6 @@ def expert_linear(x, w, plan: Dispatch, bias=None, *, k, act="none", gated=False
     if gated and wide % 2:
         raise ValueError("a gated layer's w has an even number of rows, got %d" % wide)
     n = wide // 2 if gated else wide
-    k = int(k)
     if not isinstance(plan.places, torch.Tensor) or k < 1 or plan.places.numel() % k:
         raise ValueError("plan.places must hold k = %d places for each token" % k)
     total = plan.places.numel()

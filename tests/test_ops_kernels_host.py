@@ -89,3 +89,15 @@ def test_forward_mode_duals_are_refused():
                 call(x)
             with torch.no_grad(), pytest.raises(ValueError, match="tangent"):
                 call(dual)
+
+
+def test_counts_are_whole_numbers():
+    """2.5 experts per token are not 2."""
+    x, index = torch.zeros(4, 8, dtype=torch.float16), torch.zeros(4, 2, dtype=torch.int32)
+    for bad in (2.5, 2.0, "2", None, torch.tensor([1, 2])):
+        for call in (lambda: ops.route(x, bad), lambda: ops.dispatch(index, bad), lambda: ops.expert_linear(x, x[None], None, k=bad)):
+            with pytest.raises(ValueError, match="whole number"):
+                call()
+    for good in (2, torch.tensor(2), True):
+        with pytest.raises(ValueError, match="on the GPU"):
+            ops.route(x, good)
