@@ -74,7 +74,7 @@ def _packer(cls):
     def pack(*fields):
         try:
             return packed.pack(*fields)
-        except (struct.error, OverflowError) as e:  # a scale past FP32 is the latter
+        except struct.error as e:
             raise ValueError("%s: %s" % (cls.__name__, e)) from None
     return pack
 
