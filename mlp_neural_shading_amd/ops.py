@@ -20,6 +20,7 @@ from typing import NamedTuple, Optional
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import binding as B
 
@@ -167,6 +168,12 @@ def _matrix(name, t, dtypes, device=None, rows=None, cols=None):
     return ld if r > 1 else max(ld, c)
 
 
+def _written(out):
+    """Tells autograd that a caller's tensor has new contents: a graph that kept the old ones refuses to use these."""
+    if not out.is_inference():
+        increment_version(out)
+
+
 def _vector(name, t, dtype, device, numel):
     _tensor(name, t, t.dim() if isinstance(t, torch.Tensor) else 1, (dtype,), device)
     if t.numel() != numel or not t.is_contiguous():
@@ -216,7 +223,8 @@ def linear(x, w, bias=None, *, residual=None, act="none", gated=False, out=None,
         raise ValueError("a gated layer's w has an even number of rows, got %d" % wide)
     n = wide // 2 if gated else wide
     out_dtype = _out_dtype(dtype, out_dtype)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(rows, n, dtype=out_dtype, device=device)
         ldy = max(n, 1)
     else:
@@ -227,6 +235,8 @@ def linear(x, w, bias=None, *, residual=None, act="none", gated=False, out=None,
                      0 if bias is None else _vector("bias", bias, dtype, device, wide),
                      0 if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy)
     _call("mlp_linear", a, device)
+    if given:
+        _written(out)
     return out
 
 
@@ -302,7 +312,8 @@ def expert_linear(x, w, plan: Dispatch, bias=None, *, k, act="none", gated=False
         raise ValueError("x has %d rows, the plan has %d tokens and %d slots" % (x.shape[0], tokens, total))
     out_dtype = _out_dtype(dtype, out_dtype)
     y_rows = tokens if combine else total
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(y_rows, n, dtype=out_dtype, device=device)
         ldy = max(n, 1)
     else:
@@ -321,4 +332,6 @@ def expert_linear(x, w, plan: Dispatch, bias=None, *, k, act="none", gated=False
     packed = _expert_linear_args(*a, 0, 0)
     ws = _workspace("mlp_expert_linear_workspace", packed, device) if combine else None
     _call("mlp_expert_linear", packed if ws is None else _expert_linear_args(*a, ws.data_ptr(), ws.numel()), device)
+    if given:
+        _written(out)
     return out

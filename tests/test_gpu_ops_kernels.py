@@ -301,3 +301,19 @@ def test_forward_mode_duals_are_refused_anywhere():
             ops.route(fa.make_dual(logits, logits), 2)
         with pytest.raises(ValueError, match="tangent"):
             ops.route(logits, 2, bias=fa.make_dual(logits[0], logits[0]))
+
+
+def test_autograd_sees_that_out_was_written():
+    """A graph that saved the old contents of `out` refuses its backward pass, as after torch's own products."""
+    t = torch.float16
+    x, w = torch.ones(4, 8, dtype=t, device=device()), torch.ones(6, 8, dtype=t, device=device())
+    plan = ops.dispatch(torch.zeros(4, 1, dtype=torch.int32, device=device()), 1)
+    for write in (lambda out: ops.linear(x, w, out=out), lambda out: ops.expert_linear(x, w[None], plan, k=1, out=out),
+                  lambda out: ops.linear(x, w, residual=out, out=out)):
+        leaf = torch.ones(4, 6, dtype=t, device=device(), requires_grad=True)
+        saved = leaf.exp()
+        write(saved.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            saved.sum().backward()
+        with torch.inference_mode():
+            assert float(write(torch.zeros(4, 6, dtype=t, device=device()))[0, 0]) == 8.0
