@@ -277,7 +277,7 @@ int prepare_expert_linear(const mlp_expert_linear_args *a, mlpk::ProductArgs &p)
     p.ldx = a->ldx;
     p.w = a->w;
     p.ldw = a->ldw;
-    p.w_stride = a->w_stride;
+    p.w_stride = a->experts > 1 ? a->w_stride : 0;  // of one expert it may be anything
     p.bias = a->bias;
     p.y = a->combine ? a->workspace : a->y;
     p.ldy = a->combine ? part_stride(a->out_width) : a->ldy;

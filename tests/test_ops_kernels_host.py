@@ -101,3 +101,9 @@ def test_counts_are_whole_numbers():
     for good in (2, torch.tensor(2), True):
         with pytest.raises(ValueError, match="on the GPU"):
             ops.route(x, good)
+
+
+def test_one_experts_stride_means_nothing():
+    """It decides no kernel: an odd one does not make the rows odd."""
+    for w_stride in (0, 7, -1, 2 ** 40 + 1):
+        assert K.expert_kernel(3000, 2, 1, 72, 1200, w_stride=w_stride) == "mid"
