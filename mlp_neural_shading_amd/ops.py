@@ -165,7 +165,7 @@ def _matrix(name, t, dtypes, device=None, rows=None, cols=None):
     ld, step = t.stride()
     if step != 1 and c > 1:
         raise ValueError("the rows of %s must be contiguous" % name)
-    return ld if r > 1 else max(ld, c)
+    return ld if r > 1 else c  # a single row has none to the next
 
 
 def _written(out):
@@ -322,7 +322,7 @@ def expert_linear(x, w, plan: Dispatch, bias=None, *, k, act="none", gated=False
     a = (
         tokens, k, experts, k_in, n, DTYPES[dtype], DTYPES[out_dtype], _choice("act", act, ACTIVATIONS),
         1 if gated else 0, 1 if rows == "slots" else 0, 1 if combine else 0, x.data_ptr(), ldx, w.data_ptr(),
-        w.stride(1) if wide > 1 else max(w.stride(1), k_in), w.stride(0) if experts > 1 else 0,
+        w.stride(1) if wide > 1 else k_in, w.stride(0) if experts > 1 else 0,
         0 if bias is None else _vector("bias", bias, dtype, device, experts * wide),
         _vector("plan.offsets", plan.offsets, torch.int32, device, experts + 1),
         _vector("plan.slots", plan.slots, torch.int32, device, total),

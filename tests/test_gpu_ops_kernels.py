@@ -317,3 +317,18 @@ def test_autograd_sees_that_out_was_written():
             saved.sum().backward()
         with torch.inference_mode():
             assert float(write(torch.zeros(4, 6, dtype=t, device=device()))[0, 0]) == 8.0
+
+
+def test_a_single_rows_stride_means_nothing():
+    """One row of a matrix whose rows lie farther apart than they may for y: there is no next row to step to."""
+    t, far = torch.float16, (1 << 24) + 8
+    wide = torch.zeros(2, far, dtype=t, device=device())
+    x, w = torch.ones(1, 8, dtype=t, device=device()), torch.ones(6, 8, dtype=t, device=device())
+    y = ops.linear(x, w, residual=wide[:1, :6], out=wide[1:, :6])
+    assert y.stride(0) == far and bool((y == 8).all())
+    plan = ops.dispatch(torch.zeros(1, 1, dtype=torch.int32, device=device()), 1)
+    y = ops.expert_linear(x, w[None], plan, k=1, combine=True, residual=wide[1:, :6], out=wide[:1, :6])
+    assert bool((y == 16).all())
+    narrow = torch.ones(1, 4, device=device()).expand(1, 4)
+    assert ops.route(narrow, 2).index.tolist() == [[0, 1]]
+    assert bool((ops.linear(torch.ones(3, 8, dtype=t, device=device()), w[:1].as_strided((1, 8), (1 << 30, 1))) == 8).all())
