@@ -996,20 +996,24 @@ float rounds(int64_t tiles, int at_once, bool two_per_cu)
     return whole + (rest == 0.0f ? 0.0f : two_per_cu && rest <= 0.5f ? 0.6f : 1.0f);
 }
 
-// The kernel, for 256 CUs (MI355X); times in BF16, narrow layers in FP16:
-//   - fewer than 1,024 tiles of 16 x 16: kFew, whose waves share K (1 x 1,024 -> 1,024: 4.4 us against 11 with 128 x 64
-//     tiles; 64 x 4,096 -> 1,024: 10 against 41; 300 x 1,024 -> 1,024, 1,216 tiles: 13 both), from 512 on 32 weight
-//     rows at a time (32 x 4,096 -> 4,096: 14 against 17);
-//   - at most 64 weight rows: kTile (262,144 rows 64 -> 64: 19 against 32 with 128 x 128), or kNarrow from 1,024 of its
-//     tiles on (1,048,576 rows 32 -> 32: 59 against 106; at 262,144 rows 64 -> 64 both 19, by expert 29 against 26);
+// The kernel, for 256 CUs (MI355X); times in us and BF16, narrow layers in FP16, of every kernel forced on the size:
+//   - fewer than 1,024 tiles of 16 x 16: kFew, whose waves share K, from 512 on 32 weight rows at a time.  Before that
+//     border: 64 x 4,096 -> 1,024 10 (kFewWide 14, kSmall 21), 32 x 4,096 -> 4,096 kFewWide 14 (17; 21), 100 x 256 ->
+//     2,000 6.6 (6.4; 6.4).  Behind it kSmall, though it fills few CUs: 300 x 1,024 -> 1,024 8 (kFewWide 11), 64 x
+//     1,024 -> 4,096 8.1 (8.3), 64 x 4,096 -> 4,096 21 (24), 17 x 4,096 -> 2 x 4,096 21 (23), 256 x 4,096 -> 4,096 22 (86);
+//   - at most 64 weight rows: kTile (262,144 rows 64 -> 64 18, kMid 26; 100,000 x 512 -> 64 29, kMid 35), or kNarrow from
+//     1,024 of its tiles on (1,048,576 rows 32 -> 32 47, kTile 76; 64 -> 64 by expert 80, kTile 108).  Below: 500,000 rows
+//     64 -> 64 kTile 29, kNarrow 35; by expert, 262,144 rows, 25 and 29; but 262,144 rows 32 -> 32 22 and 14;
 //   - rows that are not 4-byte aligned (an odd width): kTile, which takes them;
 //   - else the one of kBig, kMid and kSmall that takes the least time by its rounds, each of so much per 1,024 columns
 //     and so much for its start and epilogue, as fitted to 65,536 x 1,024 -> 1,024 (139, 191 and 226 us),
 //     8,192 x 4,096 -> 4,096 (222, 281 and 363) and 1,048,576 x 64 -> 128 (207, 133 and 192).  It gives kSmall for
-//     512 x 1,024 -> 4,096 (11; kMid 16), kMid for 2,048^3 (27; kBig 48), kBig for 262,144 x 64 -> 256 (62; kMid 67).
-//     The experts' last tiles count as half full, and kBig and kMid are for 192 and 96 rows per expert and more: 32,768
-//     assignments over 32 experts, 2,048 -> 2 x 1,024, 297 with kBig, 363 with kMid; 2,048 assignments, 1,024 ->
-//     2 x 1,024, 33 with kSmall, 44 with kMid.
+//     512 x 1,024 -> 4,096 (9; kMid 13) and 512 x 4,096 -> 4,096 (24; 39), kMid for 1,024 x 4,096 -> 4,096 (43; kSmall 45,
+//     kBig 75) and 2,048^3 (25; 25, 42).  One round of few tiles takes as long as one of all CUs: 64 to 512 x 4,096 ->
+//     4,096 all 21 to 24.
+//     The experts' last tiles count as half full, and kBig and kMid are for 192 and 96 rows per expert and more.  32 experts,
+//     2,048 -> 2 x 1,024, by rows per expert: 64 kSmall 70 (kMid 94), 128 kMid 96 (kSmall 90), 192 kMid 107 (113; kBig
+//     122), 256 kMid 126 (kBig 128), 512 kMid 206 (kBig 185), 1,024 kBig 309 (kMid 356).
 Form choose_form(const ProductArgs &p, bool gated, bool grouped)
 {
     const bool even = p.ldx % 2 == 0 && p.ldw % 2 == 0 && p.w_stride % 2 == 0 && (((uintptr_t)p.x | (uintptr_t)p.w) & 3) == 0;

@@ -330,11 +330,12 @@ __device__ __forceinline__ double exp_term(double v)
     const unsigned high = (unsigned)(bits >> 32) + ((unsigned)__builtin_bit_cast(unsigned long long, t) << 20);
     return __builtin_bit_cast(double, (unsigned long long)high << 32 | (unsigned)bits);
 }
-// exp to a few parts of 2^-52, for v <= 0: degree 13.
+// exp to a few parts of 2^-52, for v <= 0: degree 13.  The argument is reduced by Cody and Waite's method: ln 2 cut to its
+// first 32 bits, so that n times it is exact, and the rest.
 __device__ __forceinline__ double exp_exact(double v)
 {
     const double n = rint(fmax(v, -800.0) * 1.4426950408889634);
-    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, fmax(v, -800.0)));  // ln 2 in two parts
+    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, fmax(v, -800.0)));
     double q = 1.0 / 6227020800;
     q = fma(q, r, 1.0 / 479001600);
     q = fma(q, r, 1.0 / 39916800);
