@@ -379,7 +379,12 @@ __device__ __forceinline__ void mask_groups(const RouteArgs &r, K (&key)[VPL], K
         first = of > first ? of : first;
         second = low > high ? low : high;
     }
-    const K value = r.group_top == 2 && second > none ? first + second : first;
+    K value = first;
+    if (r.group_top == 2 && second > none) {
+        value = first + second;
+        if constexpr (sizeof(K) == 4)  // below FP32 it is still not none; two of them come out as too near
+            value = larger(value, -3.402823466e38f);
+    }
     int better = 0;  // groups before this one
     if constexpr (L == 16 && sizeof(K) == 4) {
         // By rotations: every group's first lane offers its value to the 15 others, and a lane that is not the first
@@ -403,14 +408,10 @@ __device__ __forceinline__ void mask_groups(const RouteArgs &r, K (&key)[VPL], K
     }
     const bool out = better >= r.topk_groups || !(value > none);
     if (near > 0) {  // FP32: the worst group taken and the best one left
-        const float one = fabsf((float)first), two = r.group_top == 2 && second > none ? fabsf((float)second) : 0.0f;
-        // A sum of two finite keys that is none in FP32 orders nothing.
-        const bool past = first > kLow && one < -kLow && !(one + two < -kLow);
-        if (__ballot(past) & (L < 64 ? ((1ull << (L & 63)) - 1) << row : ~0ull))
-            sure = false;
         // Half a step of each key for the addition of its bias, half a one of the sum, and of these bounds themselves;
         // the parts may be far larger than the value.
-        const float off = one + two < -kLow ? (one + two) * (1.0f / (1 << 22)) : 0.0f;
+        const float parts = fabsf((float)first) + (r.group_top == 2 && second > none ? fabsf((float)second) : 0.0f);
+        const float off = fminf(parts, 3.402823466e38f) * (1.0f / (1 << 22));
         const float taken = -lanes_max<L>(out ? kLow : off - (float)value), left = lanes_max<L>(out && first > kLow ? (float)value + off : kLow);
         if (left > kLow && !(taken - left > 2 * near))
             sure = false;
@@ -638,13 +639,24 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
         const int edge = __shfl(equal ? index : -1, row + r.k - 1);
         const unsigned kth = __shfl(mine, row + r.k - 1);
         if (edge >= 0) {
-            const float x_edge = fmaxf((float)logit[edge], kLow), b_edge = r.bias ? r.bias[edge] : 0.0f;
-            float x[VPL];
-            load_logits<T, VPL>(logit, e0, last, x);
+            // below the k-th place by at most `doubt`, and two more for what apart() cuts off
+            const unsigned reach = ((unsigned)fminf(doubt, (float)kPlaces) + 2u) * (L * VPL);
+            const float x_edge = fmaxf((float)logit[edge], kLow);
+            bool other = false;
+            if (by_logit && !infinite) {  // the keys are the logits
 #pragma unroll
-            for (int v = 0; v < VPL; ++v)
-                if (place[v] && place[v] < kth && !(apart(kth, place[v]) > doubt))
-                    ordered = ordered && x[v] == x_edge && (!r.bias || r.bias[e0 + v] == b_edge);
+                for (int v = 0; v < VPL; ++v)
+                    other |= (kth - 1u - place[v] < reach) & (key[v] != x_edge);
+            } else {
+                const float b_edge = r.bias ? r.bias[edge] : 0.0f;
+                float x[VPL];
+                load_logits<T, VPL>(logit, e0, last, x);
+#pragma unroll
+                for (int v = 0; v < VPL; ++v)
+                    if (place[v] && kth - 1u - place[v] < reach)
+                        other = other || x[v] != x_edge || (r.bias && r.bias[e0 + v] != b_edge);
+            }
+            ordered = ordered && !other;
         }
     }
     // Each token takes what its own row needs, whatever its neighbours in the wave need.
