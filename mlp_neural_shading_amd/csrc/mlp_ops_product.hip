@@ -436,8 +436,8 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][N
 // WM x WN waves, each MT x NT MFMA tiles of 32 weight rows x 32 rows, K advancing 64 per stage through two
 // stages of LDS: each thread loads its chunks of stage s + 1 into registers while stage s is multiplied (requesting
 // s + 2 as well gained nothing: 5,003 x 1,001 -> 777 38 against 34 us).
-// Bound by its loads' latency: 5,003 x 1,001 -> 777 FP16 35 us, where rows lie at odd elements; by the rows' bytes in
-// 262,144 rows 64 -> 64 by expert, 25 us, 67 MB.
+// Bound by its loads' latency: 5,003 x 1,001 -> 777 FP16 33 us, where rows lie at odd elements; by the rows' bytes in
+// 262,144 rows 64 -> 64 by expert, 24 us, 67 MB.
 // 128 bytes a row; chunk c (16 bytes) of row r sits at slot c ^ ((r / 2) % 8): the 16 rows that one 256-byte
 // LDS cycle of a fragment read serves fall in 16 different slots.
 template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int WPE>
@@ -734,7 +734,7 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 // Narrow layers over many rows, up to 64 weight rows and 64 columns: bound by the bytes of x and y.  A wave
 // keeps the whole weight matrix and the bias in registers, as MFMA operands, and takes kRounds tiles of 32 rows, each
 // straight from memory as the other operand (lane (g, n) loads the 16 bytes of row n at columns 16 kb + 8 g), two tiles
-// ahead.  No barrier anywhere; LDS only turns the outputs into rows (1,048,576 rows 32 -> 32 FP16: 59 us).
+// ahead.  No barrier anywhere; LDS only turns the outputs into rows (1,048,576 rows 32 -> 32 FP16: 47 us).
 template <class T, bool GROUPED, bool GATED>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void product_narrow(ProductArgs p)
 {
@@ -803,7 +803,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // x, and its waves share K: each multiplies a run of columns straight from memory (16 x 16 x 32 MFMA, weights = A,
 // x = B; lane (g, n) loads the 16 bytes of row n at columns 8 g), kDepth steps requested at once, and the waves'
 // sums meet in LDS.  Every wave's loads are independent, with no LDS or barrier between them; the weights' bytes are
-// the floor (7 x 2,048 -> 2 x 4,096 gated: 33.6 MB, 9.4-10.8 us; 1 x 1,024 -> 1,024: 4.3, two latencies).  Taking 32 or
+// the floor (7 x 2,048 -> 2 x 4,096 gated: 33.6 MB, 8.8-11 us; 1 x 1,024 -> 1,024: 4.2, two latencies).  Taking 32 or
 // 64 rows at once instead of several workgroups that read the same weights from L2 was slower (32 x 4,096 -> 4,096: 20
 // against 14 us; 64 x 4,096 -> 1,024: 27 against 10).
 template <class T, bool GROUPED, bool GATED, int MA>

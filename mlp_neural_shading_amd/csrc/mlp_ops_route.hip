@@ -193,7 +193,7 @@ __global__ __launch_bounds__(64) void route_tokens(RouteArgs r)
 // the k-th and the next are the same, all that lies near them is looked at.)  Where even that may leave one out, or two
 // groups' values are too near, the token chooses once more on 64-bit keys of all experts (done each time, that cost 11 us
 // of 42).  The chosen scores themselves, and the softmax's sum, are computed in 64 bits.  65,536 tokens x 256 experts,
-// sigmoid, 8 groups, k = 8: 38 us, bound by the instructions of the picks, groups and scores; the logits' bytes alone take 7.
+// sigmoid, 8 groups, k = 8: 35 to 40 us, bound by the instructions of the picks, groups and scores; the logits' bytes alone take 7.
 
 constexpr float kLow = -__builtin_huge_valf();
 
@@ -525,9 +525,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void r
     const T *logit = (const T *)r.logits + (live ? t : r.tokens - 1) * r.ld;
     float key[VPL];
     load_logits<T, VPL>(logit, e0, last, key);
-    float top = kLow;    // softmax: largest logit
-    double total = 1.0;  // what the scores are divided by without renormalisation
-    bool infinite = false;           // softmax: a logit of +infinity; the others' scores are then exactly 0
+    float top = kLow;       // softmax: largest logit
+    double total = 1.0;     // what the scores are divided by without renormalisation
+    bool infinite = false;  // softmax: a logit of +infinity; the others' scores are then exactly 0
     float near = 0.0f;
     if (r.sigmoid) {
         if (!by_logit) {
