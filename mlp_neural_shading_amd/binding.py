@@ -41,6 +41,7 @@ EXPORTED = (
     # include/mlp_testing.h
     "mlp_testing_pack_device_on_host", "mlp_testing_plan_kernel", "mlp_testing_expert_tile",
     "mlp_testing_linear_kernel", "mlp_testing_expert_linear_kernel", "mlp_testing_route_kernel",
+    "mlp_testing_norm_kernel", "mlp_testing_fp8_linear_kernel", "mlp_testing_fp8_expert_linear_kernel",
 )
 
 
@@ -80,6 +81,9 @@ def lib() -> ctypes.CDLL:
             "mlp_testing_linear_kernel": ([p, p, sz], i32),
             "mlp_testing_expert_linear_kernel": ([p, p, sz], i32),
             "mlp_testing_route_kernel": ([p, p, sz], i32),
+            "mlp_testing_norm_kernel": ([p, p, sz], i32),
+            "mlp_testing_fp8_linear_kernel": ([p, p, sz], i32),
+            "mlp_testing_fp8_expert_linear_kernel": ([p, p, sz], i32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)

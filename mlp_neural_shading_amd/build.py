@@ -27,7 +27,8 @@ COMMON = [
     "-mllvm", "-amdgpu-atomic-optimizer-strategy=None",
 ]
 SOURCES = ["mlp_kernels.hip", "mlp_kernels_fp8.hip", "mlp_layered.hip", "mlp_pack_device.hip", "mlp_api.cpp", "mlp_pack.cpp",
-           "mlp_ops_product.hip", "mlp_ops_route.hip", "mlp_ops_api.cpp"]
+           "mlp_ops_product.hip", "mlp_ops_route.hip", "mlp_ops_api.cpp", "mlp_ops_norm.hip", "mlp_ops_fp8.hip",
+           "mlp_ops_fp8_api.cpp"]
 CEILING_SOURCE = "mlp_ceiling.hip"
 CEILING_LIB = PKG / "libmlp_ceiling.so"
 

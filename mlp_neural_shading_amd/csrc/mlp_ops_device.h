@@ -210,6 +210,7 @@ template <class T>
 struct Tile {
     int64_t row0, row1;  // rows (slots) [row0, row1)
     int o0;              // first output
+    int expert;          // 0 in a dense product
     const T *w, *bias;
 };
 
@@ -220,6 +221,7 @@ template <class T, bool GROUPED, bool GATED, int BO, int BN>
 __device__ __forceinline__ bool take_tile(const ProductArgs &p, Tile<T> &tile)
 {
     const int n_out = (p.out + BO - 1) / BO;
+    tile.expert = 0;
     tile.w = (const T *)p.w;
     tile.bias = (const T *)p.bias;
     const int row_tiles = GROUPED ? total_tiles(p.offsets, p.experts, (int)p.rows, BN) : (int)((p.rows + BN - 1) / BN);
@@ -238,6 +240,7 @@ __device__ __forceinline__ bool take_tile(const ProductArgs &p, Tile<T> &tile)
             return false;
         tile.row0 = r.row0;
         tile.row1 = r.row1;
+        tile.expert = r.expert;
         tile.w += r.expert * p.w_stride;
         if (tile.bias)
             tile.bias += (int64_t)r.expert * p.out * (GATED ? 2 : 1);
@@ -308,7 +311,9 @@ struct __attribute__((packed, aligned(2))) Float8 {
 // n at n * 64 + 8 (k ^ 2 ((n / 4) % 4))); with one, or in FP32, after it and after the addition (chunk k of 16 bytes at
 // n * 128 + 16 (k ^ ((n / 2) % 8))).  The residual is requested kAhead tiles ahead: its latency would otherwise stand
 // once per tile.  Addresses are a base per tile plus 32 bits per lane (262,144 rows 64 -> 64: 20.4 -> 18.7 us with both).
-template <class T, bool GATED, int MT, int NT>
+// SIXTEEN: a tile is four of 16 x 16, of which lane (g, n) holds outputs 4 g .. 4 g + 3 of row n: element 4 e + i is that
+// of outputs 16 (e / 2) .. and rows 16 (e % 2) ..
+template <class T, bool GATED, bool SIXTEEN = false, int MT, int NT>
 __device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][NT], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
 {
     typedef typename Vec8<T>::type V8;
@@ -359,11 +364,11 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][N
         const int left = outs - 32 * (t % MO) - oc;  // outputs from this lane's first on
         const int64_t y_tile = (int64_t)(32 * nt) * ldy + 32 * (t % MO), r_tile = (int64_t)(32 * nt) * ldr + 32 * (t % MO);
         if (!p.residual && !p.y_fp32) {
-            const int ws = 2 * ((n >> 2) & 3);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const f4 v = {z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
-                *(V4 *)(ob + n * 64 + 8 * ((2 * q + g) ^ ws)) = __builtin_convertvector(v, V4);  // nearest even
+                const int r = SIXTEEN ? 16 * (q % 2) + (lane & 15) : n, k = SIXTEEN ? 4 * (q / 2) + (lane >> 4) : 2 * q + g;
+                *(V4 *)(ob + r * 64 + 8 * (k ^ (2 * ((r >> 2) & 3)))) = __builtin_convertvector(v, V4);  // nearest even
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -385,8 +390,10 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][N
             continue;
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            *(f4 *)(ob + n * 128 + 16 * ((2 * q + g) ^ ((n >> 1) & 7))) = f4{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
+        for (int q = 0; q < 4; ++q) {
+            const int r = SIXTEEN ? 16 * (q % 2) + (lane & 15) : n, k = SIXTEEN ? 4 * (q / 2) + (lane >> 4) : 2 * q + g;
+            *(f4 *)(ob + r * 128 + 16 * (k ^ ((r >> 1) & 7))) = f4{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
+        }
         if (half_res && t + kAhead < TILES)
             fetch(t + kAhead);
         __builtin_amdgcn_sched_barrier(0);

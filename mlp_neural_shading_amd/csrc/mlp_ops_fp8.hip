@@ -1,0 +1,683 @@
+// mlp_ops_fp8.hip -- one affine layer with 8-bit operands, dense or over the rows routed to experts:
+//   z[r][o] = sum_b xs[r][b] ws[o / 128][b] (sum_{i in block b} x[r][i] w[o][i]) + bias[o],  b over blocks of 128 columns,
+// with the epilogue of the 16-bit products.  A block of columns is a stage: the matrix unit sums it from 0, and one fused
+// multiply-add per sum brings it to the FP32 total with xs ws, which in a tile of 16 rows of x is one number a lane (a lane
+// holds one row of x, the tile lies in one block of weight rows).
+#include <hip/hip_runtime.h>
+
+#include "mlp_ops_device.h"
+#include "mlp_ops_fp8_kernels.h"
+#include "mlp_ops_quant.h"
+
+namespace mlpk {
+
+namespace {
+
+typedef int i4 __attribute__((ext_vector_type(4)));
+typedef int i8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+
+// 8 E4M3 values in FP16.
+__device__ __forceinline__ h8 widen(int lo, int hi)
+{
+    const h2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const h2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false), d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+
+// The sums of a block: 16 weight rows x 16 rows over 128 columns, of which lane (g, n) holds 32 of row n for both operands
+// (which 32 does not matter, as long as it is the same ones) and weight rows 4 g .. 4 g + 3 of row n of the result.
+// The matrix unit adds the products of E4M3 operands 8 at a time (8 neighbouring bytes of a lane), each cut to a multiple
+// of 2^-13 of the largest one's power of two, and then in FP32: off by about 2^-16 of a result.  That is far below the
+// rounding of a 16-bit output.  For outputs that keep more (FULL: FP32 rows, and 8-bit rows, whose scales are FP32) the
+// operands are widened to FP16, which holds them exactly and whose products are added in FP32, at half the rate.
+template <bool FULL>
+__device__ __forceinline__ f4 block_sums(i8 a, i8 b)
+{
+    if constexpr (!FULL) {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, (f4)0.0f, 0, 0, 0, 0, 0, 0);  // 0: E4M3, no scales
+    } else {
+        f4 c = (f4)0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c = mfma16(widen(a[2 * i], a[2 * i + 1]), widen(b[2 * i], b[2 * i + 1]), c);
+        return c;
+    }
+}
+
+__device__ __forceinline__ i8 join(u4 lo, u4 hi)
+{
+    return __builtin_shufflevector(__builtin_bit_cast(i4, lo), __builtin_bit_cast(i4, hi), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// 16 bytes at any address.
+__device__ __forceinline__ u4 load16(const uint8_t *p)
+{
+    struct __attribute__((packed, aligned(1))) Bytes16 {
+        u4 v;
+    };
+    return ((const Bytes16 *)p)->v;
+}
+
+// The 16 columns from `col` of a row of `width`, zero past its end; reads no byte past it.
+__device__ __forceinline__ u4 load16_tail(const uint8_t *row, int col, int width)
+{
+    if (col + 16 <= width)
+        return load16(row + col);
+    u4 v = (u4)0u;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        if (col + j < width)
+            v[j / 4] |= (unsigned)row[col + j] << (8 * (j % 4));
+    return v;
+}
+
+// The row of w's scales behind row r of a tile (as weight_row).
+template <bool GATED>
+__device__ __forceinline__ int scale_row(int o0, int r, int out)
+{
+    int o = GATED ? o0 + (r >> 6) * 32 + (r & 31) : o0 + r;
+    o = (o < out ? o : out - 1) / kFp8Block;
+    return GATED && (r & 32) ? o + (out + kFp8Block - 1) / kFp8Block : o;
+}
+
+template <bool GROUPED, bool GATED>
+__device__ __forceinline__ const float *tile_bias(const Fp8ProductArgs &p, int expert)
+{
+    const float *b = (const float *)p.bias;
+    return GROUPED && b ? b + (int64_t)expert * p.out * (GATED ? 2 : 1) : b;
+}
+
+// The bias of weight rows r .. r + 3 of a tile, r a multiple of 4.
+template <bool GATED>
+__device__ __forceinline__ f4 bias_rows(const float *bias, int o0, int r, int out)
+{
+    f4 b = (f4)0.0f;
+    if (bias)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            b[i] = bias[weight_row<GATED>(o0, r + i, out)];
+    return b;
+}
+
+// The epilogue of a wave's MT x NT tiles of 32 x 32.
+template <class T, bool GATED, int MT, int NT>
+__device__ __forceinline__ void finish(const ProductArgs &p, f4 (&acc)[2 * MT][2 * NT], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
+{
+    f16x t[MT][NT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                t[mt][nt][j] = acc[2 * mt + j / 8][2 * nt + j / 4 % 2][j % 4];
+    epilogue<T, GATED, true>(p, t, ob, o0, r0, row, row1);
+}
+
+// WM x WN waves, each MT x NT tiles of 32 weight rows x 32 rows, as four of 16 x 16.  A stage is 128 columns, 128 bytes
+// of every row, and the scales of the tile's rows for that block, a dword per thread; NS stages go from memory straight
+// into LDS.  Chunk c (16 bytes) of row r sits at slot c ^ ((r / 2) % 8), as in the 16-bit products.  A tile's multiply-adds
+// follow the matrix instructions of the next tiles, and the stage's last row of tiles is multiplied after the barrier that
+// frees it, while the next stage's first operands are read.
+template <class T, bool FULL, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int NS, int WPE>
+__global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void fp8_big(Fp8ProductArgs p)
+{
+    constexpr int BK = kFp8Block, TH = 64 * WM * WN, BM = 32 * WM * MT, BN = 32 * WN * NT;
+    constexpr int RPP = TH / 8, M = 2 * MT, N = 2 * NT, UN = M * N, LAG = N >= 4 ? 2 : 1;
+    constexpr int CA = BM / RPP, CB = BN / RPP;  // 16-byte loads per thread and stage
+    constexpr int A_ST = BM * BK, S_ST = (BM + BN) * BK, STAGE = S_ST + TH * 4;
+    static_assert(CA * RPP == BM && CB * RPP == BN && RPP % 16 == 0, "whole chunks per thread, one swizzle per thread");
+    static_assert(BM + BN <= TH && BM % 64 == 0, "a scale per thread");
+    static_assert(!GATED || MT % 2 == 0, "gate and partner tiles in one wave");
+    static_assert(WM * WN * 4096 <= STAGE, "the epilogue's rows fit a stage");
+    static_assert(NS == 2 || NS == 3, "");
+    // A variable each: the compiler then knows that a load into one does not touch another.
+    __shared__ __attribute__((aligned(16))) uint8_t l0[STAGE], l1[STAGE], l2[NS == 3 ? STAGE : 16];
+
+    Tile<uint8_t> tile;
+    if (!take_tile<uint8_t, GROUPED, GATED, (GATED ? BM / 2 : BM), BN>(p, tile))
+        return;  // whole workgroup, before any barrier
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int g = lane >> 4, n = lane & 15;
+    const int r_in = tid / 8;
+    const int c = (tid & 7) ^ ((r_in >> 1) & 7);  // the chunk that this thread's slot holds
+    const uint8_t *src[CA + CB];
+#pragma unroll
+    for (int i = 0; i < CA; ++i)
+        src[i] = tile.w + (int64_t)weight_row<GATED>(tile.o0, r_in + i * RPP, p.out) * p.ldw + 16 * c;
+#pragma unroll
+    for (int i = 0; i < CB; ++i)
+        src[CA + i] = (const uint8_t *)p.x + input_row<GROUPED>(p, tile.row0 + r_in + i * RPP, tile.row1) * p.ldx + 16 * c;
+    const float *const scale = tid < BM ? p.ws + tile.expert * p.ws_stride + scale_row<GATED>(tile.o0, tid, p.out) * p.ldws
+                                        : p.xs + input_row<GROUPED>(p, tile.row0 + (tid - BM < BN ? tid - BM : BN - 1), tile.row1) * p.ldxs;
+
+    const int full = p.in / BK, rest = p.in - full * BK, blocks = full + (rest != 0);
+    // After the whole stages come the row's last 128 columns, some of them a second time; past them they are requested
+    // again, unused, and so is the last whole stage where `rest` is 0, or no multiple of 4 (the loads' alignment).
+    const int last_step = rest % 4 ? 0 : rest;
+    int issued = 0;  // stages requested
+    auto request = [&](uint8_t *dst) {
+        const int step = issued + 1 < full ? BK : issued + 1 == full ? last_step : 0;
+#pragma unroll
+        for (int i = 0; i < CA + CB; ++i) {
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src[i],
+                                             (__attribute__((address_space(3))) void *)(dst + wave * 1024 + i * (TH * 16)), 16, 0, 0);
+            src[i] += step;
+        }
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(scale + (issued < blocks ? issued : blocks - 1)),
+                                         (__attribute__((address_space(3))) void *)(dst + S_ST + wave * 256), 4, 0, 0);
+        ++issued;
+    };
+    constexpr int LOADS = CA + CB + 1;
+
+    i8 fa[2], fb[N];
+    float sw[MT], sx[N], s[N];
+    f4 acc[M][N], part[4];
+    const int swz = (n >> 1) & 7, ch0 = 16 * (g ^ swz), ch1 = 16 * ((g + 4) ^ swz);
+    const int a_rd = (wm * MT * 32 + n) * BK, b_rd = A_ST + (wn * NT * 32 + n) * BK;
+    auto fragment = [&](const uint8_t *row) { return join(*(const u4 *)(row + ch0), *(const u4 *)(row + ch1)); };
+    auto read_a = [&](const uint8_t *d, int m) { fa[m & 1] = fragment(d + a_rd + m * 16 * BK); };
+    auto read_b = [&](const uint8_t *d, int k) { fb[k] = fragment(d + b_rd + k * 16 * BK); };
+    auto read_scales = [&](const uint8_t *d) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            sw[mt] = *(const float *)(d + S_ST + (wm * MT + mt) * 128);
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            sx[k] = *(const float *)(d + S_ST + (BM + wn * NT * 32 + k * 16 + n) * 4);
+    };
+    auto add = [&](int u) {  // tile u's block to its total
+        f4 &t = acc[u / N][u % N];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t[i] = fmaf(part[u & 3][i], s[u % N], t[i]);
+    };
+    // The block of tile u, and the total of the tile LAG before it.
+    auto unit = [&](int u) {
+        part[u & 3] = block_sums<FULL>(fa[u / N & 1], fb[u % N]);
+        add((u + UN - LAG) % UN);
+    };
+    auto mix = [&]() {
+        __builtin_amdgcn_sched_group_barrier(0x008, FULL ? 4 : 1, 0);  // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);             // LDS reads
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr int AHEAD = (NS - 2) * LOADS;  // loads still in flight when the next stage has to be there
+    auto turn = [&](auto ahead) {
+        constexpr int V = decltype(ahead)::value;
+        __builtin_amdgcn_s_waitcnt(0x0070 | (V & 15) | (V >> 4) << 14);  // vmcnt(V) lgkmcnt(0)
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    // One stage, whose first operands and scales have been read: cur is its buffer, nxt the next stage's.
+    auto stage = [&](uint8_t *__restrict cur, const uint8_t *__restrict nxt) {
+        float f[N];
+#pragma unroll
+        for (int m = 0; m < M - 1; ++m) {
+            read_a(cur, m + 1);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                unit(m * N + k);
+                s[k] = sw[m / 2] * sx[k];
+                mix();
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            f[k] = sw[MT - 1] * sx[k];
+        turn(Number<AHEAD>{});
+        request(cur);
+        read_a(nxt, 0);
+        read_scales(nxt);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            unit((M - 1) * N + k);
+            s[k] = f[k];
+            read_b(nxt, k);
+            mix();
+        }
+    };
+    if (full) {
+        request(l0);
+        request(l1);
+        if constexpr (NS == 3)
+            request(l2);
+    }
+    const float *const bias = tile_bias<GROUPED, GATED>(p, tile.expert);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const f4 b = bias_rows<GATED>(bias, tile.o0, (wm * M + m) * 16 + 4 * g, p.out);
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            acc[m][k] = b;
+    }
+    if (full) {
+        turn(Number<(NS - 1) * LOADS>{});
+        read_a(l0, 0);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            read_b(l0, k);
+            s[k] = 0.0f;
+        }
+        read_scales(l0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            part[i] = (f4)0.0f;
+        // The turns of the buffers, and what is left of one: a loop that ends in one place only, or the sums change
+        // registers on the way.
+        int left = full;
+        for (; left >= NS; left -= NS) {
+            stage(l0, l1);
+            stage(l1, NS == 3 ? l2 : l0);
+            if constexpr (NS == 3)
+                stage(l2, l0);
+        }
+        if (left > 0) {
+            stage(l0, l1);
+            if (NS == 3 && left > 1)
+                stage(l1, l2);
+        }
+#pragma unroll
+        for (int u = UN - LAG; u < UN; ++u)
+            add(u);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070);  // the requests past the end
+    __syncthreads();
+    if (rest) {
+        const uint8_t *d = NS == 2 ? (full % 2 ? l1 : l0) : full % 3 == 0 ? l0 : full % 3 == 1 ? l1 : l2;
+        int skip = BK - rest;  // columns of the last 128 that the whole stages have had
+        if (!full || !last_step) {  // the rest and zeros, through registers
+#pragma unroll
+            for (int i = 0; i < CA + CB; ++i) {
+                const uint8_t *row = src[i] - 16 * c - (full ? (full - 1) * BK : 0);
+                *(u4 *)(l0 + tid * 16 + i * (TH * 16)) = load16_tail(row, full * BK + 16 * c, p.in);
+            }
+            *(float *)(l0 + S_ST + tid * 4) = scale[full];
+            __syncthreads();
+            d = l0;
+            skip = 0;
+        }
+        auto keep = [&](const uint8_t *row) {
+            i8 v = fragment(row);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = 16 * (g + 4 * (i / 4)) + 4 * (i % 4) >= skip ? v[i] : 0;
+            return v;
+        };
+        read_scales(d);
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            fb[k] = keep(d + b_rd + k * 16 * BK);
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const i8 a = keep(d + a_rd + m * 16 * BK);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const f4 v = block_sums<FULL>(a, fb[k]);
+                const float by = sw[m / 2] * sx[k];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[m][k][i] = fmaf(v[i], by, acc[m][k][i]);
+            }
+        }
+        __syncthreads();
+    }
+    finish<T, GATED, MT, NT>(p, acc, l0 + wave * 4096, tile.o0, wm * MT * 32, tile.row0 + wn * NT * 32, tile.row1);
+}
+
+// The same through registers, for rows at any address: each thread loads its chunks of stage s + 1 while stage s is
+// multiplied.
+template <class T, bool FULL, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int WPE>
+__global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void fp8_tile(Fp8ProductArgs p)
+{
+    constexpr int BK = kFp8Block, TH = 64 * WM * WN, BM = 32 * WM * MT, BN = 32 * WN * NT;
+    constexpr int RPP = TH / 8;
+    constexpr int CA = BM / RPP, CB = BN / RPP;
+    constexpr int A_ST = BM * BK, S_ST = (BM + BN) * BK, STAGE = S_ST + TH * 4;
+    static_assert(CA * RPP == BM && CB * RPP == BN && RPP % 16 == 0, "whole chunks per thread, one swizzle per thread");
+    static_assert(BM + BN <= TH && BM % 64 == 0, "a scale per thread");
+    static_assert(!GATED || MT % 2 == 0, "gate and partner tiles in one wave");
+    static_assert(WM * WN * 4096 <= 2 * STAGE, "the epilogue's rows fit the stages");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
+
+    Tile<uint8_t> tile;
+    if (!take_tile<uint8_t, GROUPED, GATED, (GATED ? BM / 2 : BM), BN>(p, tile))
+        return;  // whole workgroup, before any barrier
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int g = lane >> 4, n = lane & 15;
+    const int c = tid % 8, r_in = tid / 8;
+    const uint8_t *wp[CA], *xp[CB];
+#pragma unroll
+    for (int i = 0; i < CA; ++i)
+        wp[i] = tile.w + (int64_t)weight_row<GATED>(tile.o0, r_in + i * RPP, p.out) * p.ldw;
+#pragma unroll
+    for (int i = 0; i < CB; ++i)
+        xp[i] = (const uint8_t *)p.x + input_row<GROUPED>(p, tile.row0 + r_in + i * RPP, tile.row1) * p.ldx;
+    const float *const scale = tid < BM ? p.ws + tile.expert * p.ws_stride + scale_row<GATED>(tile.o0, tid, p.out) * p.ldws
+                                        : p.xs + input_row<GROUPED>(p, tile.row0 + (tid - BM < BN ? tid - BM : BN - 1), tile.row1) * p.ldxs;
+    const int st = r_in * BK + 16 * (c ^ ((r_in >> 1) & 7));
+
+    constexpr int M = 2 * MT, N = 2 * NT;
+    f4 acc[M][N];
+    const float *const bias = tile_bias<GROUPED, GATED>(p, tile.expert);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const f4 b = bias_rows<GATED>(bias, tile.o0, (wm * M + m) * 16 + 4 * g, p.out);
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            acc[m][k] = b;
+    }
+
+    u4 ra[CA], rb[CB];
+    float rs;
+    const int steps = (p.in + BK - 1) / BK;
+    auto load = [&](int s) {
+        const int col = s * BK + 16 * c;
+#pragma unroll
+        for (int i = 0; i < CA; ++i)
+            ra[i] = load16_tail(wp[i], col, p.in);
+#pragma unroll
+        for (int i = 0; i < CB; ++i)
+            rb[i] = load16_tail(xp[i], col, p.in);
+        rs = scale[s];
+    };
+    auto store = [&](int s) {
+        uint8_t *d = lds + (s & 1) * STAGE;
+#pragma unroll
+        for (int i = 0; i < CA; ++i)
+            *(u4 *)(d + st + i * RPP * BK) = ra[i];
+#pragma unroll
+        for (int i = 0; i < CB; ++i)
+            *(u4 *)(d + A_ST + st + i * RPP * BK) = rb[i];
+        *(float *)(d + S_ST + tid * 4) = rs;
+    };
+    const int swz = (n >> 1) & 7, ch0 = 16 * (g ^ swz), ch1 = 16 * ((g + 4) ^ swz);
+    const int a_rd = (wm * MT * 32 + n) * BK, b_rd = A_ST + (wn * NT * 32 + n) * BK;
+    auto fragment = [&](const uint8_t *row) { return join(*(const u4 *)(row + ch0), *(const u4 *)(row + ch1)); };
+    auto multiply = [&](int s) {
+        const uint8_t *d = lds + (s & 1) * STAGE;
+        i8 b[N];
+        float sx[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            b[k] = fragment(d + b_rd + k * 16 * BK);
+            sx[k] = *(const float *)(d + S_ST + (BM + wn * NT * 32 + k * 16 + n) * 4);
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const i8 a = fragment(d + a_rd + m * 16 * BK);
+            const float sw = *(const float *)(d + S_ST + (wm * MT + m / 2) * 128);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const f4 v = block_sums<FULL>(a, b[k]);
+                const float by = sw * sx[k];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[m][k][i] = fmaf(v[i], by, acc[m][k][i]);
+            }
+        }
+    };
+    load(0);
+    store(0);
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+        if (s + 1 < steps)
+            load(s + 1);
+        multiply(s);
+        if (s + 1 < steps)
+            store(s + 1);
+        __syncthreads();
+    }
+    finish<T, GATED, MT, NT>(p, acc, lds + wave * 4096, tile.o0, wm * MT * 32, tile.row0 + wn * NT * 32, tile.row1);
+}
+
+// Few rows: a workgroup of up to 16 waves takes 16 * MA weight rows and up to 16 rows of x, and its waves share the
+// blocks of K: each multiplies a run of them straight from memory (16 x 16 x 128 MFMA: one block), kDepth requested at
+// once, and the waves' sums meet in LDS.
+template <class T, bool FULL, bool GROUPED, bool GATED, int MA>
+__global__ __launch_bounds__(1024) void fp8_few(Fp8ProductArgs p)
+{
+    static_assert(!GATED || MA == 2, "16 gates and the 16 they gate");
+    constexpr int BO = GATED ? 16 : 16 * MA, BN = 16, kDepth = 2;
+    constexpr int SUMS = 16 * MA * BN;  // per wave
+    extern __shared__ float sums[];      // [NW][MA][16 rows of x][16 weight rows]
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int nw = blockDim.x >> 6, g = lane >> 4, n = lane & 15;
+    const int n_out = (p.out + BO - 1) / BO;
+    const int o0 = (int)(blockIdx.x % n_out) * BO;
+    int64_t row0 = (int64_t)(blockIdx.x / n_out) * BN, row1 = row0 + BN < p.rows ? row0 + BN : p.rows;
+    const uint8_t *w = (const uint8_t *)p.w;
+    const float *ws = p.ws;
+    int expert = 0;
+    if constexpr (GROUPED) {
+        RowTile rt;
+        if (!find_tile(p.offsets, p.experts, (int)p.rows, BN, (int)(blockIdx.x / n_out), rt))
+            return;  // whole workgroup
+        row0 = rt.row0;
+        row1 = rt.row1;
+        expert = rt.expert;
+        w += expert * p.w_stride;
+        ws += expert * p.ws_stride;
+    }
+    const float *const bias = tile_bias<GROUPED, GATED>(p, expert);
+    const uint8_t *wp[MA];
+    const float *sp[MA];
+#pragma unroll
+    for (int i = 0; i < MA; ++i) {
+        const int first = o0 + (GATED ? 0 : 16 * i);  // 16 rows lie in one block
+        const int o = (first + n < p.out ? first + n : p.out - 1) + (GATED && i ? p.out : 0);
+        wp[i] = w + (int64_t)o * p.ldw + 32 * g;
+        const int b = (first < p.out ? first : p.out - 1) / kFp8Block + (GATED && i ? (p.out + kFp8Block - 1) / kFp8Block : 0);
+        sp[i] = ws + b * p.ldws;
+    }
+    const int64_t x_row = input_row<GROUPED>(p, row0 + n, row1);
+    const uint8_t *xp = (const uint8_t *)p.x + x_row * p.ldx + 32 * g;
+    const float *xs = p.xs + x_row * p.ldxs;
+
+    f4 acc[MA];
+#pragma unroll
+    for (int j = 0; j < MA; ++j)
+        acc[j] = (f4)0.0f;
+    const int full = p.in / kFp8Block, blocks = (p.in + kFp8Block - 1) / kFp8Block;
+    const int share = (blocks + nw - 1) / nw;
+    const int begin = wave * share, end = min(begin + share, blocks);
+    int k = begin;
+    i8 a[kDepth][MA], b[kDepth];
+    float s[kDepth][MA];
+    auto scales = [&](int d) {
+        const float sx = xs[k + d];
+#pragma unroll
+        for (int j = 0; j < MA; ++j)
+            s[d][j] = sx * sp[j][k + d];
+    };
+    auto multiply = [&](int d) {
+#pragma unroll
+        for (int j = 0; j < MA; ++j) {
+            const f4 v = block_sums<FULL>(a[d][j], b[d]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[j][i] = fmaf(v[i], s[d][j], acc[j][i]);
+        }
+    };
+    auto whole = [&](int d) {
+        const int64_t at = (int64_t)(k + d) * kFp8Block;
+#pragma unroll
+        for (int j = 0; j < MA; ++j)
+            a[d][j] = join(load16(wp[j] + at), load16(wp[j] + at + 16));
+        b[d] = join(load16(xp + at), load16(xp + at + 16));
+        scales(d);
+    };
+    for (; k + kDepth <= end && k + kDepth <= full; k += kDepth) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d)
+            whole(d);
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d)
+            multiply(d);
+    }
+    for (; k < end; ++k) {
+        if (k < full) {
+            whole(0);
+        } else {  // the last block's columns and zeros
+            const int col = k * kFp8Block + 32 * g;
+#pragma unroll
+            for (int j = 0; j < MA; ++j)
+                a[0][j] = join(load16_tail(wp[j] - 32 * g, col, p.in), load16_tail(wp[j] - 32 * g, col + 16, p.in));
+            b[0] = join(load16_tail(xp - 32 * g, col, p.in), load16_tail(xp - 32 * g, col + 16, p.in));
+            scales(0);
+        }
+        multiply(0);
+    }
+    // Lane (g, n) of an MFMA tile holds weight rows 4 g .. 4 g + 3 of row n.
+#pragma unroll
+    for (int j = 0; j < MA; ++j)
+        *(f4 *)(sums + wave * SUMS + (j * 16 + n) * 16 + 4 * g) = acc[j];
+    __syncthreads();
+    for (int i = tid; i < BO * BN; i += blockDim.x) {
+        // 16 outputs of a row together
+        const int ol = i % 16, oj = GATED ? 0 : i / 16 % MA, rl = i / BO;
+        const int at = (oj * 16 + rl) * 16 + ol;
+        const int o = o0 + 16 * oj + ol;
+        const int64_t row = row0 + rl;
+        if (o >= p.out || row >= row1)
+            continue;
+        float z = bias ? bias[o] : 0.0f, u = GATED && bias ? bias[o + p.out] : 0.0f;
+        for (int v = 0; v < nw; ++v) {
+            z += sums[v * SUMS + at];
+            if constexpr (GATED)
+                u += sums[v * SUMS + at + 256];
+        }
+        with_activation(p.act, [&](auto act) { z = act(z); });
+        if constexpr (GATED)
+            z *= u;
+        if (p.residual)
+            z += p.y_fp32 ? ((const float *)p.residual)[row * p.ldr + o] : (float)((const T *)p.residual)[row * p.ldr + o];
+        if (p.y_fp32)
+            ((float *)p.y)[row * p.ldy + o] = z;
+        else
+            ((T *)p.y)[row * p.ldy + o] = (T)z;
+    }
+}
+
+// ---- which kernel ---------------------------------------------------------------------------------
+
+// kBig 256 weight rows x 256 rows, kMid 128 x 128, kSmall 128 x 64 (all three straight into LDS), kTile 64 x 128 through
+// registers, kFew 16 x 16, kFewWide 32 x 16.
+enum Form { kBig, kMid, kSmall, kTile, kFew, kFewWide };
+struct Shape {
+    int bm, bn, threads;
+};
+constexpr Shape kShapes[] = {{256, 256, 512}, {128, 128, 256}, {128, 64, 256}, {64, 128, 256}, {16, 16, 1024}, {32, 16, 1024}};
+
+// Row tiles of bn rows there can be at most.
+int64_t row_tiles(const ProductArgs &p, bool grouped, int bn)
+{
+    return grouped ? p.rows / bn + (p.rows < p.experts ? p.rows : p.experts) : (p.rows + bn - 1) / bn;
+}
+
+int64_t tiles_most(const ProductArgs &p, bool gated, bool grouped, Form f)
+{
+    const Shape s = kShapes[f];
+    const int64_t bo = gated ? (f == kFew || f == kFewWide ? 16 : s.bm / 2) : s.bm;
+    const int64_t tiles = (p.out + bo - 1) / bo * row_tiles(p, grouped, s.bn);
+    return f == kFew || f == kFewWide ? tiles : (tiles + 7) / 8 * 8;  // the XCDs' runs are equally long
+}
+
+// Rounds of tiles over the chip, `at_once` of them per round; where a CU runs two, a last round that is at most half
+// full takes 0.6 of one.
+float rounds(int64_t tiles, int at_once, bool two_per_cu)
+{
+    const float whole = (float)(tiles / at_once), rest = (float)(tiles % at_once) / at_once;
+    return whole + (rest == 0.0f ? 0.0f : two_per_cu && rest <= 0.5f ? 0.6f : 1.0f);
+}
+
+Form choose_form(const Fp8ProductArgs &p, bool gated, bool grouped)
+{
+    const bool even = p.ldx % 4 == 0 && p.ldw % 4 == 0 && p.w_stride % 4 == 0 && (((uintptr_t)p.x | (uintptr_t)p.w) & 3) == 0;
+    const int64_t wide = (int64_t)p.out * (gated ? 2 : 1);
+    const int64_t few = row_tiles(p, grouped, 16) * ((wide + 15) / 16);
+    if (few < 1024)
+        return gated || few >= 512 ? kFewWide : kFew;
+    if (!even || wide <= 64)
+        return kTile;
+    const int64_t used = !grouped ? 0 : p.rows < p.experts ? p.rows : p.experts;
+    auto tiles = [&](Form f) {
+        const int64_t bm = kShapes[f].bm, bn = kShapes[f].bn;
+        return (grouped ? p.rows / bn + (used + 1) / 2 : (p.rows + bn - 1) / bn) * ((wide + bm - 1) / bm);
+    };
+    const float k = (float)p.in / 2048.0f;
+    const float big = rounds(tiles(kBig), 256, false) * (26.5f * k + 9.5f);
+    const float mid = rounds(tiles(kMid), 512, true) * (15.5f * k + 8.5f);
+    const float small = rounds(tiles(kSmall), 512, true) * (10.4f * k + 5.5f);
+    const int64_t each = used ? p.rows / used : INT64_MAX;  // rows per expert
+    if (each >= 192 && big <= mid && big <= small)
+        return kBig;
+    return each >= 96 && mid <= small ? kMid : kSmall;
+}
+
+template <class T, bool FULL, bool GROUPED, bool GATED>
+hipError_t launch(const Fp8ProductArgs &p, hipStream_t stream)
+{
+    const Form form = choose_form(p, GATED, GROUPED);
+    const dim3 grid((unsigned)tiles_most(p, GATED, GROUPED, form)), block(kShapes[form].threads);
+    switch (form) {
+    case kBig:
+        hipLaunchKernelGGL((fp8_big<T, FULL, GROUPED, GATED, 2, 4, 4, 2, 2, 2>), grid, block, 0, stream, p);
+        break;
+    case kMid:
+        hipLaunchKernelGGL((fp8_big<T, FULL, GROUPED, GATED, 2, 2, 2, 2, 2, 2>), grid, block, 0, stream, p);
+        break;
+    case kSmall:
+        hipLaunchKernelGGL((fp8_big<T, FULL, GROUPED, GATED, 2, 2, 2, 1, 3, 2>), grid, block, 0, stream, p);
+        break;
+    case kTile:
+        hipLaunchKernelGGL((fp8_tile<T, FULL, GROUPED, GATED, 1, 4, 2, 1, 2>), grid, block, 0, stream, p);
+        break;
+    default:
+        // a block for each of up to 16 waves
+        const int blocks = (p.in + kFp8Block - 1) / kFp8Block, waves = blocks < 16 ? blocks : 16;
+        const size_t lds = (size_t)waves * kShapes[form].bm * 16 * 4;
+        if (GATED || form == kFewWide)
+            hipLaunchKernelGGL((fp8_few<T, FULL, GROUPED, GATED, 2>), grid, dim3(64 * waves), lds, stream, p);
+        else
+            hipLaunchKernelGGL((fp8_few<T, FULL, GROUPED, GATED, GATED ? 2 : 1>), grid, dim3(64 * waves), lds, stream, p);
+    }
+    return hipGetLastError();
+}
+
+template <class T, bool FULL>
+hipError_t launch(const Fp8ProductArgs &p, bool gated, bool grouped, hipStream_t stream)
+{
+    if (grouped)
+        return gated ? launch<T, FULL, true, true>(p, stream) : launch<T, FULL, true, false>(p, stream);
+    return gated ? launch<T, FULL, false, true>(p, stream) : launch<T, FULL, false, false>(p, stream);
+}
+
+}  // namespace
+
+bool fp8_product_fits(const Fp8ProductArgs &p, bool gated, bool grouped)
+{
+    const Form form = choose_form(p, gated, grouped);
+    return tiles_most(p, gated, grouped, form) * kShapes[form].threads <= UINT32_MAX;  // a grid counts its threads in 32 bits
+}
+
+const char *fp8_product_kernel(const Fp8ProductArgs &p, bool gated, bool grouped)
+{
+    static const char *const names[] = {"big", "mid", "small", "tile", "few", "few wide"};
+    return names[choose_form(p, gated, grouped)];
+}
+
+hipError_t launch_fp8_product(const Fp8ProductArgs &p, int type, bool gated, bool grouped, hipStream_t stream)
+{
+    return type == kFp16 ? launch<_Float16, false>(p, gated, grouped, stream)
+           : type == kBf16 ? launch<__bf16, false>(p, gated, grouped, stream)
+                           : launch<_Float16, true>(p, gated, grouped, stream);
+}
+
+}  // namespace mlpk

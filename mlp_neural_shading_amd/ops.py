@@ -34,8 +34,10 @@ MLP_OPS_MAX_TOPK = 32
 
 EXPORTED = ("mlp_linear", "mlp_route", "mlp_dispatch_workspace", "mlp_dispatch", "mlp_expert_linear_workspace",
             "mlp_expert_linear")
+EXPORTED_FP8 = ("mlp_rms_norm", "mlp_quantize", "mlp_fp8_linear_workspace", "mlp_fp8_linear",
+                "mlp_fp8_expert_linear_workspace", "mlp_fp8_expert_linear")  # include/mlp_ops_fp8.h, for ops_fp8
 
-_p, _i32, _i64, _u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
+_p, _i32, _i64, _u64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
 
 
 class LinearArgs(ctypes.Structure):
@@ -46,7 +48,7 @@ class LinearArgs(ctypes.Structure):
 
 class RouteArgs(ctypes.Structure):
     _fields_ = [("tokens", _i64), ("experts", _i32), ("k", _i32), ("dtype", _i32), ("score", _i32), ("groups", _i32),
-                ("topk_groups", _i32), ("group_top", _i32), ("renormalise", _i32), ("scale", ctypes.c_float),
+                ("topk_groups", _i32), ("group_top", _i32), ("renormalise", _i32), ("scale", _f32),
                 ("logits", _p), ("ld", _i64), ("bias", _p), ("index", _p), ("weight", _p)]
 
 
@@ -63,7 +65,7 @@ class ExpertLinearArgs(ctypes.Structure):
                 ("ldr", _i64), ("y", _p), ("ldy", _i64), ("workspace", _p), ("workspace_bytes", _u64)]
 
 
-_FORMAT = {_p: "P", _i32: "i", _i64: "q", _u64: "Q", ctypes.c_float: "f"}
+_FORMAT = {_p: "P", _i32: "i", _i64: "q", _u64: "Q", _f32: "f"}
 
 
 def _packer(cls):
@@ -105,7 +107,7 @@ def lib() -> ctypes.CDLL:
     global _lib
     if _lib is None:
         L = B.lib()
-        for name in EXPORTED:
+        for name in EXPORTED + EXPORTED_FP8:
             f = getattr(L, name)
             f.argtypes = [_p, _p]
             f.restype = ctypes.c_int
