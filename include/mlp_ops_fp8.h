@@ -106,7 +106,8 @@ typedef struct mlp_fp8_linear_args {
     uint64_t workspace_bytes;
 } mlp_fp8_linear_args;
 
-/* Bytes of workspace mlp_fp8_linear needs for these sizes and strides. */
+/* Bytes of workspace mlp_fp8_linear needs for these sizes, strides and (by their alignment) pointers of x and w: FP32 rows
+ * where 8-bit outputs are rounded by a kernel of its own, else 0. */
 int mlp_fp8_linear_workspace(const mlp_fp8_linear_args *args, uint64_t *bytes);
 int mlp_fp8_linear(const mlp_fp8_linear_args *args, void *stream);
 
@@ -145,6 +146,7 @@ typedef struct mlp_fp8_expert_linear_args {
     uint64_t workspace_bytes;
 } mlp_fp8_expert_linear_args;
 
+/* Bytes of workspace mlp_fp8_expert_linear needs, as above; also the FP32 outputs by slot where it combines. */
 int mlp_fp8_expert_linear_workspace(const mlp_fp8_expert_linear_args *args, uint64_t *bytes);
 int mlp_fp8_expert_linear(const mlp_fp8_expert_linear_args *args, void *stream);
 

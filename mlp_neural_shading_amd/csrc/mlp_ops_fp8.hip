@@ -60,6 +60,14 @@ __device__ __forceinline__ u4 load16(const uint8_t *p)
     return ((const Bytes16 *)p)->v;
 }
 
+__device__ __forceinline__ void store16(uint8_t *p, u4 v)
+{
+    struct __attribute__((packed, aligned(1))) Bytes16 {
+        u4 v;
+    };
+    ((Bytes16 *)p)->v = v;
+}
+
 // The 16 columns from `col` of a row of `width`, zero past its end; reads no byte past it.
 __device__ __forceinline__ u4 load16_tail(const uint8_t *row, int col, int width)
 {
@@ -114,6 +122,90 @@ __device__ __forceinline__ void finish(const ProductArgs &p, f4 (&acc)[2 * MT][2
             for (int j = 0; j < 16; ++j)
                 t[mt][nt][j] = acc[2 * mt + j / 8][2 * nt + j / 4 % 2][j % 4];
     epilogue<T, GATED, true>(p, t, ob, o0, r0, row, row1);
+}
+
+// The epilogue into 8 bits, for a workgroup whose BO outputs are whole blocks of 128: a block's outputs lie in several waves,
+// which exchange each row's largest through LDS, and then the rows' bytes, so that they leave 16 at a time.
+template <bool GATED, int WM, int WN, int MT, int NT>
+__device__ __forceinline__ void finish8(const Fp8ProductArgs &p, f4 (&acc)[2 * MT][2 * NT], uint8_t *lds, int o0, int wm, int wn, int64_t row0,
+                                        int64_t row1)
+{
+    constexpr int MO = GATED ? MT / 2 : MT, BO = 32 * WM * MO, BN = 32 * WN * NT, LD = BO + 16, PER = kFp8Block / (32 * MO);  // waves a block
+    static_assert(BO % kFp8Block == 0 && WM % PER == 0, "whole blocks");
+    float *const part = (float *)(lds + BN * LD);  // [WM][BN]
+    const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+    f16x z[MO][NT];
+#pragma unroll
+    for (int mo = 0; mo < MO; ++mo)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int mt = GATED ? 2 * mo : mo;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                z[mo][nt][j] = acc[2 * mt + j / 8][2 * nt + j / 4 % 2][j % 4];
+            with_activation(p.act, [&](auto act) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    z[mo][nt][j] = act(z[mo][nt][j]);
+            });
+            if constexpr (GATED)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    z[mo][nt][j] *= acc[2 * mt + 2 + j / 8][2 * nt + j / 4 % 2][j % 4];
+        }
+    // Outputs past the last repeat it, in its block.
+#pragma unroll
+    for (int k = 0; k < 2 * NT; ++k) {
+        float m = 0.0f;
+#pragma unroll
+        for (int mo = 0; mo < MO; ++mo)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (j / 4 % 2 == k % 2)
+                    m = fmaxf(m, finite_abs(z[mo][k / 2][j]));
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        if (g == 0)
+            part[wm * BN + wn * NT * 32 + k * 16 + n] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2 * NT; ++k) {
+        const int r = wn * NT * 32 + k * 16 + n;
+        float m = part[(wm / PER * PER) * BN + r];
+#pragma unroll
+        for (int i = 1; i < PER; ++i)
+            m = fmaxf(m, part[(wm / PER * PER + i) * BN + r]);
+        const float scale = scale_of(m), inv = 1.0f / scale;
+        const int o = o0 + wm / PER * kFp8Block;
+        if (wm % PER == 0 && g == 0 && row0 + r < row1 && o < p.out)
+            p.ys[(row0 + r) * p.ldys + o / kFp8Block] = scale;
+#pragma unroll
+        for (int mo = 0; mo < MO; ++mo)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = 8 * h + 4 * (k % 2);
+                const f16x &v = z[mo][k / 2];
+                *(unsigned *)(lds + r * LD + wm * MO * 32 + mo * 32 + 16 * h + 4 * g) = to_e4m3x4(v[j], v[j + 1], v[j + 2], v[j + 3], inv);
+            }
+    }
+    __syncthreads();
+    constexpr int CHUNKS = BO / 16;
+    for (int i = threadIdx.x; i < BN * CHUNKS; i += 64 * WM * WN) {
+        const int r = i / CHUNKS, c = i % CHUNKS * 16, left = p.out - o0 - c;
+        if (row0 + r >= row1 || left <= 0)
+            continue;
+        const u4 v = *(const u4 *)(lds + r * LD + c);
+        uint8_t *const y = p.values + (row0 + r) * p.ldv + o0 + c;
+        if (left >= 16) {
+            store16(y, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 15; ++j)
+                if (j < left)
+                    y[j] = (uint8_t)(v[j / 4] >> (8 * (j % 4)));
+        }
+    }
 }
 
 // WM x WN waves, each MT x NT tiles of 32 weight rows x 32 rows, as four of 16 x 16.  A stage is 128 columns, 128 bytes
@@ -201,8 +293,11 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
         add((u + UN - LAG) % UN);
     };
     auto mix = [&]() {
-        __builtin_amdgcn_sched_group_barrier(0x008, FULL ? 4 : 1, 0);  // MFMA
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);             // LDS reads
+        if constexpr (!FULL) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+            __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);  // the multiply-adds
+        }
         __builtin_amdgcn_sched_barrier(0);
     };
     constexpr int AHEAD = (NS - 2) * LOADS;  // loads still in flight when the next stage has to be there
@@ -325,6 +420,13 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
             }
         }
         __syncthreads();
+    }
+    if constexpr (FULL && (GATED ? BM / 2 : BM) % kFp8Block == 0) {
+        static_assert(BN * ((GATED ? BM / 2 : BM) + 16 + 4 * WM) <= STAGE, "the 8-bit rows fit a stage");
+        if (p.values) {
+            finish8<GATED, WM, WN, MT, NT>(p, acc, l0, tile.o0, wm, wn, tile.row0, tile.row1);
+            return;
+        }
     }
     finish<T, GATED, MT, NT>(p, acc, l0 + wave * 4096, tile.o0, wm * MT * 32, tile.row0 + wn * NT * 32, tile.row1);
 }
@@ -567,13 +669,17 @@ __global__ __launch_bounds__(1024) void fp8_few(Fp8ProductArgs p)
 
 // ---- which kernel ---------------------------------------------------------------------------------
 
-// kBig 256 weight rows x 256 rows, kMid 128 x 128, kSmall 128 x 64 (all three straight into LDS), kTile 64 x 128 through
-// registers, kFew 16 x 16, kFewWide 32 x 16.
+// kBig 256 weight rows x 256 rows (FULL: 256 x 128), kMid 128 x 128, kSmall 128 x 64 (all three straight into LDS), kTile
+// 64 x 128 through registers, kFew 16 x 16, kFewWide 32 x 16.
 enum Form { kBig, kMid, kSmall, kTile, kFew, kFewWide };
 struct Shape {
     int bm, bn, threads;
 };
-constexpr Shape kShapes[] = {{256, 256, 512}, {128, 128, 256}, {128, 64, 256}, {64, 128, 256}, {16, 16, 1024}, {32, 16, 1024}};
+Shape shape(Form f, bool full)
+{
+    static constexpr Shape shapes[] = {{256, 256, 512}, {128, 128, 256}, {128, 64, 256}, {64, 128, 256}, {16, 16, 1024}, {32, 16, 1024}};
+    return f == kBig && full ? Shape{256, 128, 512} : shapes[f];
+}
 
 // Row tiles of bn rows there can be at most.
 int64_t row_tiles(const ProductArgs &p, bool grouped, int bn)
@@ -581,9 +687,9 @@ int64_t row_tiles(const ProductArgs &p, bool grouped, int bn)
     return grouped ? p.rows / bn + (p.rows < p.experts ? p.rows : p.experts) : (p.rows + bn - 1) / bn;
 }
 
-int64_t tiles_most(const ProductArgs &p, bool gated, bool grouped, Form f)
+int64_t tiles_most(const ProductArgs &p, bool full, bool gated, bool grouped, Form f)
 {
-    const Shape s = kShapes[f];
+    const Shape s = shape(f, full);
     const int64_t bo = gated ? (f == kFew || f == kFewWide ? 16 : s.bm / 2) : s.bm;
     const int64_t tiles = (p.out + bo - 1) / bo * row_tiles(p, grouped, s.bn);
     return f == kFew || f == kFewWide ? tiles : (tiles + 7) / 8 * 8;  // the XCDs' runs are equally long
@@ -597,7 +703,7 @@ float rounds(int64_t tiles, int at_once, bool two_per_cu)
     return whole + (rest == 0.0f ? 0.0f : two_per_cu && rest <= 0.5f ? 0.6f : 1.0f);
 }
 
-Form choose_form(const Fp8ProductArgs &p, bool gated, bool grouped)
+Form choose_form(const Fp8ProductArgs &p, bool full, bool gated, bool grouped)
 {
     const bool even = p.ldx % 4 == 0 && p.ldw % 4 == 0 && p.w_stride % 4 == 0 && (((uintptr_t)p.x | (uintptr_t)p.w) & 3) == 0;
     const int64_t wide = (int64_t)p.out * (gated ? 2 : 1);
@@ -608,7 +714,7 @@ Form choose_form(const Fp8ProductArgs &p, bool gated, bool grouped)
         return kTile;
     const int64_t used = !grouped ? 0 : p.rows < p.experts ? p.rows : p.experts;
     auto tiles = [&](Form f) {
-        const int64_t bm = kShapes[f].bm, bn = kShapes[f].bn;
+        const int64_t bm = shape(f, full).bm, bn = shape(f, full).bn;
         return (grouped ? p.rows / bn + (used + 1) / 2 : (p.rows + bn - 1) / bn) * ((wide + bm - 1) / bm);
     };
     const float k = (float)p.in / 2048.0f;
@@ -624,11 +730,15 @@ Form choose_form(const Fp8ProductArgs &p, bool gated, bool grouped)
 template <class T, bool FULL, bool GROUPED, bool GATED>
 hipError_t launch(const Fp8ProductArgs &p, hipStream_t stream)
 {
-    const Form form = choose_form(p, GATED, GROUPED);
-    const dim3 grid((unsigned)tiles_most(p, GATED, GROUPED, form)), block(kShapes[form].threads);
+    const Form form = choose_form(p, FULL, GATED, GROUPED);
+    const Shape s = shape(form, FULL);
+    const dim3 grid((unsigned)tiles_most(p, FULL, GATED, GROUPED, form)), block(s.threads);
     switch (form) {
     case kBig:
-        hipLaunchKernelGGL((fp8_big<T, FULL, GROUPED, GATED, 2, 4, 4, 2, 2, 2>), grid, block, 0, stream, p);
+        if constexpr (FULL)
+            hipLaunchKernelGGL((fp8_big<T, FULL, GROUPED, GATED, 4, 2, 2, 2, 2, 2>), grid, block, 0, stream, p);
+        else
+            hipLaunchKernelGGL((fp8_big<T, FULL, GROUPED, GATED, 2, 4, 4, 2, 2, 2>), grid, block, 0, stream, p);
         break;
     case kMid:
         hipLaunchKernelGGL((fp8_big<T, FULL, GROUPED, GATED, 2, 2, 2, 2, 2, 2>), grid, block, 0, stream, p);
@@ -642,7 +752,7 @@ hipError_t launch(const Fp8ProductArgs &p, hipStream_t stream)
     default:
         // a block for each of up to 16 waves
         const int blocks = (p.in + kFp8Block - 1) / kFp8Block, waves = blocks < 16 ? blocks : 16;
-        const size_t lds = (size_t)waves * kShapes[form].bm * 16 * 4;
+        const size_t lds = (size_t)waves * s.bm * 16 * 4;
         if (GATED || form == kFewWide)
             hipLaunchKernelGGL((fp8_few<T, FULL, GROUPED, GATED, 2>), grid, dim3(64 * waves), lds, stream, p);
         else
@@ -661,16 +771,22 @@ hipError_t launch(const Fp8ProductArgs &p, bool gated, bool grouped, hipStream_t
 
 }  // namespace
 
-bool fp8_product_fits(const Fp8ProductArgs &p, bool gated, bool grouped)
+bool fp8_product_fits(const Fp8ProductArgs &p, int type, bool gated, bool grouped)
 {
-    const Form form = choose_form(p, gated, grouped);
-    return tiles_most(p, gated, grouped, form) * kShapes[form].threads <= UINT32_MAX;  // a grid counts its threads in 32 bits
+    const Form form = choose_form(p, type == kFp32, gated, grouped);
+    return tiles_most(p, type == kFp32, gated, grouped, form) * shape(form, type == kFp32).threads <= UINT32_MAX;  // a grid counts its threads in 32 bits
 }
 
-const char *fp8_product_kernel(const Fp8ProductArgs &p, bool gated, bool grouped)
+bool fp8_product_rounds(const Fp8ProductArgs &p, bool gated, bool grouped)
+{
+    const Form form = choose_form(p, true, gated, grouped);
+    return (form == kBig || form == kMid || form == kSmall) && shape(form, true).bm / (gated ? 2 : 1) % kFp8Block == 0;
+}
+
+const char *fp8_product_kernel(const Fp8ProductArgs &p, int type, bool gated, bool grouped)
 {
     static const char *const names[] = {"big", "mid", "small", "tile", "few", "few wide"};
-    return names[choose_form(p, gated, grouped)];
+    return names[choose_form(p, type == kFp32, gated, grouped)];
 }
 
 hipError_t launch_fp8_product(const Fp8ProductArgs &p, int type, bool gated, bool grouped, hipStream_t stream)

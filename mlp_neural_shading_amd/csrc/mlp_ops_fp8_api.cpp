@@ -151,16 +151,51 @@ int check_expert_linear(const mlp_fp8_expert_linear_args *a)
 // Row stride (floats) of FP32 rows in a workspace.
 int64_t part_stride(int out_width) { return round_up(out_width, 4); }
 
-// FP32 rows: of 8-bit outputs before their rounding, and of combined slots.
-uint64_t linear_need(const mlp_fp8_linear_args *a)
+// What the choice of kernel depends on: sizes, strides and the operands' alignment.
+Fp8ProductArgs sizes(const mlp_fp8_linear_args *a)
 {
-    return a->out_dtype == MLP_DTYPE_FP8 ? (uint64_t)a->rows * part_stride(a->out_width) * 4 : 0;
+    Fp8ProductArgs p{};
+    p.rows = a->rows;
+    p.in = a->in_width;
+    p.out = a->out_width;
+    p.x = a->x;
+    p.ldx = a->ldx;
+    p.w = a->w;
+    p.ldw = a->ldw;
+    return p;
 }
 
-uint64_t expert_linear_need(const mlp_fp8_expert_linear_args *a)
+Fp8ProductArgs sizes(const mlp_fp8_expert_linear_args *a)
 {
-    return a->combine || a->out_dtype == MLP_DTYPE_FP8 ? (uint64_t)a->tokens * a->k * part_stride(a->out_width) * 4 : 0;
+    Fp8ProductArgs p{};
+    p.rows = a->tokens * a->k;
+    p.in = a->in_width;
+    p.out = a->out_width;
+    p.x = a->x;
+    p.ldx = a->ldx;
+    p.w = a->w;
+    p.ldw = a->ldw;
+    p.experts = a->experts;
+    p.k = a->k;
+    p.w_stride = a->experts > 1 ? a->w_stride : 0;  // of one expert it may be anything
+    return p;
 }
+
+// The workspace holds FP32 rows: combined slots, or outputs that another kernel rounds to 8 bits.
+template <class A>
+uint64_t rows_need(const A *a, bool combine, bool grouped)
+{
+    const Fp8ProductArgs p = sizes(a);
+    if (p.rows == 0 || !(combine || (a->out_dtype == MLP_DTYPE_FP8 && !fp8_product_rounds(p, a->gated, grouped))))
+        return 0;
+    return (uint64_t)p.rows * part_stride(a->out_width) * 4;
+}
+
+uint64_t linear_need(const mlp_fp8_linear_args *a) { return rows_need(a, false, false); }
+uint64_t expert_linear_need(const mlp_fp8_expert_linear_args *a) { return rows_need(a, a->combine, true); }
+
+// 8-bit outputs have FP32 scales.
+int result_type(int out_dtype) { return out_dtype == MLP_DTYPE_FP8 ? kFp32 : out_dtype; }
 
 int activation(int act, int out_dtype)
 {
@@ -216,35 +251,32 @@ int check_outputs(const A *a, int64_t y_rows, uint64_t need, const Span (&in)[N]
     return MLP_OK;
 }
 
+// Where the product's results go.
 template <class A>
-void fill(const A *a, Fp8ProductArgs &p)
+void outputs(const A *a, uint64_t need, Fp8ProductArgs &p)
 {
-    p.x = a->x;
-    p.ldx = a->ldx;
     p.xs = a->x_scale;
     p.ldxs = a->ldxs;
-    p.w = a->w;
-    p.ldw = a->ldw;
     p.ws = a->w_scale;
     p.ldws = a->ldws;
     p.bias = a->bias;
-    p.in = a->in_width;
-    p.out = a->out_width;
     p.act = activation(a->act, a->out_dtype);
-    p.y_fp32 = a->out_dtype == MLP_DTYPE_FP32;
-    p.y = a->y;
-    p.ldy = a->ldy;
-    p.residual = a->residual;
-    p.ldr = a->ldr;
-}
-
-// FP32 rows, for another kernel to finish.
-void to_workspace(void *workspace, Fp8ProductArgs &p)
-{
-    p.y = workspace;
-    p.ldy = part_stride(p.out);
-    p.y_fp32 = 1;
-    p.residual = nullptr;
+    if (need) {  // FP32 rows, for another kernel to finish
+        p.y = a->workspace;
+        p.ldy = part_stride(p.out);
+        p.y_fp32 = 1;
+    } else if (a->out_dtype == MLP_DTYPE_FP8) {
+        p.values = (uint8_t *)a->y;
+        p.ldv = a->ldy;
+        p.ys = a->y_scale;
+        p.ldys = a->ldys;
+    } else {
+        p.y = a->y;
+        p.ldy = a->ldy;
+        p.y_fp32 = a->out_dtype == MLP_DTYPE_FP32;
+        p.residual = a->residual;
+        p.ldr = a->ldr;
+    }
 }
 
 // The checked call as its product; rows are left 0 where there is nothing to do.
@@ -259,12 +291,11 @@ int prepare_linear(const mlp_fp8_linear_args *a, Fp8ProductArgs &p)
     const Span in[] = {span(a->x, a->rows, a->in_width, a->ldx, 1), span(a->x_scale, a->rows, blocks, a->ldxs, 4),
                        span(a->w, wide, a->in_width, a->ldw, 1), span(a->w_scale, down, blocks, a->ldws, 4),
                        span(a->bias, 1, wide, wide, 4)};
-    MLP_TRY(check_outputs(a, a->rows, linear_need(a), in));
-    fill(a, p);
-    p.rows = a->rows;
-    if (a->out_dtype == MLP_DTYPE_FP8)
-        to_workspace(a->workspace, p);
-    if (!fp8_product_fits(p, a->gated, false))
+    const uint64_t need = linear_need(a);
+    MLP_TRY(check_outputs(a, a->rows, need, in));
+    p = sizes(a);
+    outputs(a, need, p);
+    if (!fp8_product_fits(p, result_type(a->out_dtype), a->gated, false))
         return fail(MLP_ERR_UNSUPPORTED, "%lld rows of %d outputs are more tiles than one launch holds", (long long)a->rows,
                     a->out_width);
     return MLP_OK;
@@ -295,18 +326,14 @@ int prepare_expert_linear(const mlp_fp8_expert_linear_args *a, Fp8ProductArgs &p
                        many(a->w_scale, a->experts, a->ws_stride, down, blocks, a->ldws, 4), span(a->bias, 1, all, all, 4),
                        span(a->offsets, 1, a->experts + 1, a->experts + 1, 4), span(a->slots, 1, n, n, 4),
                        span(a->places, 1, n, n, 4), span(a->weight, 1, n, n, 4)};
-    MLP_TRY(check_outputs(a, y_rows, expert_linear_need(a), in));
-    fill(a, p);
-    p.rows = n;
-    p.w_stride = a->experts > 1 ? a->w_stride : 0;  // of one expert they may be anything
+    const uint64_t need = expert_linear_need(a);
+    MLP_TRY(check_outputs(a, y_rows, need, in));
+    p = sizes(a);
+    outputs(a, need, p);
     p.ws_stride = a->experts > 1 ? a->ws_stride : 0;
     p.offsets = a->offsets;
     p.slots = a->x_slots ? nullptr : a->slots;
-    p.experts = a->experts;
-    p.k = a->k;
-    if (a->combine || a->out_dtype == MLP_DTYPE_FP8)
-        to_workspace(a->workspace, p);
-    if (!fp8_product_fits(p, a->gated, true))
+    if (!fp8_product_fits(p, result_type(a->out_dtype), a->gated, true))
         return fail(MLP_ERR_UNSUPPORTED, "%lld slots of %d outputs are more tiles than one launch holds", (long long)n,
                     a->out_width);
     return MLP_OK;
@@ -329,9 +356,6 @@ QuantizeArgs rounding(const A *a, int64_t rows, const int32_t *used)
     q.used = used;
     return q;
 }
-
-// 8-bit outputs have FP32 scales.
-int result_type(int out_dtype) { return out_dtype == MLP_DTYPE_FP8 ? kFp32 : out_dtype; }
 
 int put_name(const char *text, char *name, size_t cap)
 {
@@ -417,7 +441,7 @@ int mlp_fp8_linear(const mlp_fp8_linear_args *a, void *stream)
     hipError_t err = launch_fp8_product(p, result_type(a->out_dtype), a->gated, false, (hipStream_t)stream);
     if (err != hipSuccess)
         return hip_fail(err, "launching the layer");
-    if (a->out_dtype == MLP_DTYPE_FP8) {
+    if (a->out_dtype == MLP_DTYPE_FP8 && !p.values) {
         err = launch_quantize(rounding(a, a->rows, nullptr), kFp32, 1, (hipStream_t)stream);
         if (err != hipSuccess)
             return hip_fail(err, "launching the rounding to 8 bits");
@@ -459,7 +483,7 @@ int mlp_fp8_expert_linear(const mlp_fp8_expert_linear_args *a, void *stream)
         err = launch_combine(c, a->out_dtype, (hipStream_t)stream);
         if (err != hipSuccess)
             return hip_fail(err, "launching the combination");
-    } else if (a->out_dtype == MLP_DTYPE_FP8) {
+    } else if (a->out_dtype == MLP_DTYPE_FP8 && !p.values) {
         err = launch_quantize(rounding(a, p.rows, a->offsets + a->experts), kFp32, 1, (hipStream_t)stream);
         if (err != hipSuccess)
             return hip_fail(err, "launching the rounding to 8 bits");
@@ -478,14 +502,14 @@ int mlp_testing_fp8_linear_kernel(const mlp_fp8_linear_args *a, char *name, size
 {
     Fp8ProductArgs p{};
     MLP_TRY(prepare_linear(a, p));
-    return put_name(p.rows ? fp8_product_kernel(p, a->gated, false) : "none", name, cap);
+    return put_name(p.rows ? fp8_product_kernel(p, result_type(a->out_dtype), a->gated, false) : "none", name, cap);
 }
 
 int mlp_testing_fp8_expert_linear_kernel(const mlp_fp8_expert_linear_args *a, char *name, size_t cap)
 {
     Fp8ProductArgs p{};
     MLP_TRY(prepare_expert_linear(a, p));
-    return put_name(p.rows ? fp8_product_kernel(p, a->gated, true) : "none", name, cap);
+    return put_name(p.rows ? fp8_product_kernel(p, result_type(a->out_dtype), a->gated, true) : "none", name, cap);
 }
 
 }  // extern "C"

@@ -56,7 +56,9 @@ struct Fp8ProductArgs : ProductArgs {
 };
 // type: what becomes of the results, kFp16 or kBf16 (at once, or from FP32 rows in a workspace), or kFp32 for FP32's accuracy.
 hipError_t launch_fp8_product(const Fp8ProductArgs &p, int type, bool gated, bool grouped, hipStream_t stream);
-bool fp8_product_fits(const Fp8ProductArgs &p, bool gated, bool grouped);
-const char *fp8_product_kernel(const Fp8ProductArgs &p, bool gated, bool grouped);
+bool fp8_product_fits(const Fp8ProductArgs &p, int type, bool gated, bool grouped);
+// Whether the product's kernel (type kFp32) rounds to 8 bits itself: `values` and `ys` may be set, y is not used then.
+bool fp8_product_rounds(const Fp8ProductArgs &p, bool gated, bool grouped);
+const char *fp8_product_kernel(const Fp8ProductArgs &p, int type, bool gated, bool grouped);
 
 }  // namespace mlpk

@@ -247,7 +247,7 @@ def linear(x: Quantized, w: Quantized, bias=None, *, residual=None, act="none", 
     a = (rows, k, n, _OUT[out_dtype], _choice("act", act, ACTIVATIONS), 1 if gated else 0, *operand, *weights, b,
          0 if residual is None else residual.data_ptr(), ldr, y.data_ptr(), ldy, ys, ldys)
     packed = _linear_args(*a, 0, 0)
-    ws = _workspace("mlp_fp8_linear_workspace", packed, device)
+    ws = _workspace("mlp_fp8_linear_workspace", packed, device) if ys else None
     _call("mlp_fp8_linear", packed if ws is None else _linear_args(*a, ws.data_ptr(), ws.numel()), device)
     return _done(out, given)
 
@@ -281,6 +281,6 @@ def expert_linear(x: Quantized, w: Quantized, plan: Dispatch, bias=None, *, k, a
          0 if weight is None else _vector("weight", weight, torch.float32, device, total),
          0 if residual is None else residual.data_ptr(), ldr, y.data_ptr(), ldy, ys, ldys)
     packed = _expert_linear_args(*a, 0, 0)
-    ws = _workspace("mlp_fp8_expert_linear_workspace", packed, device)
+    ws = _workspace("mlp_fp8_expert_linear_workspace", packed, device) if ys or combine else None
     _call("mlp_fp8_expert_linear", packed if ws is None else _expert_linear_args(*a, ws.data_ptr(), ws.numel()), device)
     return _done(out, given)
