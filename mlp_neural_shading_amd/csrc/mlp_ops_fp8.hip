@@ -111,7 +111,7 @@ __device__ __forceinline__ f4 bias_rows(const float *bias, int o0, int r, int ou
 
 // The epilogue of a wave's MT x NT tiles of 32 x 32.
 template <class T, bool GATED, int MT, int NT>
-__device__ __forceinline__ void finish(const ProductArgs &p, f4 (&acc)[2 * MT][2 * NT], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
+__device__ __forceinline__ void finish(const ProductArgs &p, float (&acc)[2 * MT][2 * NT][4], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
 {
     f16x t[MT][NT];
 #pragma unroll
@@ -127,7 +127,7 @@ __device__ __forceinline__ void finish(const ProductArgs &p, f4 (&acc)[2 * MT][2
 // The epilogue into 8 bits, for a workgroup whose BO outputs are whole blocks of 128: a block's outputs lie in several waves,
 // which exchange each row's largest through LDS, and then the rows' bytes, so that they leave 16 at a time.
 template <bool GATED, int WM, int WN, int MT, int NT>
-__device__ __forceinline__ void finish8(const Fp8ProductArgs &p, f4 (&acc)[2 * MT][2 * NT], uint8_t *lds, int o0, int wm, int wn, int64_t row0,
+__device__ __forceinline__ void finish8(const Fp8ProductArgs &p, float (&acc)[2 * MT][2 * NT][4], uint8_t *lds, int o0, int wm, int wn, int64_t row0,
                                         int64_t row1)
 {
     constexpr int MO = GATED ? MT / 2 : MT, BO = 32 * WM * MO, BN = 32 * WN * NT, LD = BO + 16, PER = kFp8Block / (32 * MO);  // waves a block
@@ -209,8 +209,7 @@ __device__ __forceinline__ void finish8(const Fp8ProductArgs &p, f4 (&acc)[2 * M
 }
 
 // WM x WN waves, each MT x NT tiles of 32 weight rows x 32 rows, as four of 16 x 16.  A stage is 128 columns, 128 bytes
-// of every row, and the scales of the tile's rows for that block, a dword per thread; NS stages go from memory straight
-// into LDS.  Chunk c (16 bytes) of row r sits at slot c ^ ((r / 2) % 8), as in the 16-bit products.  A tile's multiply-adds
+// of every row; NS stages go from memory straight into LDS, and so do the rows' scales, for four blocks at a time.  Chunk c (16 bytes) of row r sits at slot c ^ ((r / 2) % 8), as in the 16-bit products.  A tile's multiply-adds
 // follow the matrix instructions of the next tiles, and the stage's last row of tiles is multiplied after the barrier that
 // frees it, while the next stage's first operands are read.
 template <class T, bool FULL, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int NS, int WPE>
@@ -219,14 +218,15 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
     constexpr int BK = kFp8Block, TH = 64 * WM * WN, BM = 32 * WM * MT, BN = 32 * WN * NT;
     constexpr int RPP = TH / 8, M = 2 * MT, N = 2 * NT, UN = M * N, LAG = N >= 4 ? 2 : 1;
     constexpr int CA = BM / RPP, CB = BN / RPP;  // 16-byte loads per thread and stage
-    constexpr int A_ST = BM * BK, S_ST = (BM + BN) * BK, STAGE = S_ST + TH * 4;
+    constexpr int A_ST = BM * BK, STAGE = (BM + BN) * BK, SCALES = (BM + BN) * 16;
     static_assert(CA * RPP == BM && CB * RPP == BN && RPP % 16 == 0, "whole chunks per thread, one swizzle per thread");
-    static_assert(BM + BN <= TH && BM % 64 == 0, "a scale per thread");
+    static_assert(BM + BN <= TH && BM % 64 == 0 && BN % 64 == 0, "a row's scales per thread, whole waves");
     static_assert(!GATED || MT % 2 == 0, "gate and partner tiles in one wave");
     static_assert(WM * WN * 4096 <= STAGE, "the epilogue's rows fit a stage");
     static_assert(NS == 2 || NS == 3, "");
     // A variable each: the compiler then knows that a load into one does not touch another.
     __shared__ __attribute__((aligned(16))) uint8_t l0[STAGE], l1[STAGE], l2[NS == 3 ? STAGE : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t ls[2][SCALES];  // 4 blocks' scales of each row
 
     Tile<uint8_t> tile;
     if (!take_tile<uint8_t, GROUPED, GATED, (GATED ? BM / 2 : BM), BN>(p, tile))
@@ -251,6 +251,9 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
     // again, unused, and so is the last whole stage where `rest` is 0, or no multiple of 4 (the loads' alignment).
     const int last_step = rest % 4 ? 0 : rest;
     int issued = 0;  // stages requested
+    // The scales come four blocks at a time (a lane per row touches a cache line per row: 16 bytes cost what 4 do), the last
+    // four of a row ending with it; of rows with fewer, through registers below.
+    auto first_scale = [&](int st) { return st / 4 * 4 < blocks - 4 ? st / 4 * 4 : blocks - 4; };
     auto request = [&](uint8_t *dst) {
         const int step = issued + 1 < full ? BK : issued + 1 == full ? last_step : 0;
 #pragma unroll
@@ -259,30 +262,33 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
                                              (__attribute__((address_space(3))) void *)(dst + wave * 1024 + i * (TH * 16)), 16, 0, 0);
             src[i] += step;
         }
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(scale + (issued < blocks ? issued : blocks - 1)),
-                                         (__attribute__((address_space(3))) void *)(dst + S_ST + wave * 256), 4, 0, 0);
+        if (issued % 4 == 0 && issued < blocks && blocks >= 4 && tid < BM + BN)  // whole waves
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(scale + first_scale(issued)),
+                                             (__attribute__((address_space(3))) void *)(ls[issued / 4 & 1] + wave * 1024), 16, 0, 0);
         ++issued;
     };
-    constexpr int LOADS = CA + CB + 1;
+    constexpr int LOADS = CA + CB;  // and one where scales are requested
 
     i8 fa[2], fb[N];
     float sw[MT], sx[N], s[N];
-    f4 acc[M][N], part[4];
+    float acc[M][N][4];
+    f4 part[4];
     const int swz = (n >> 1) & 7, ch0 = 16 * (g ^ swz), ch1 = 16 * ((g + 4) ^ swz);
     const int a_rd = (wm * MT * 32 + n) * BK, b_rd = A_ST + (wn * NT * 32 + n) * BK;
     auto fragment = [&](const uint8_t *row) { return join(*(const u4 *)(row + ch0), *(const u4 *)(row + ch1)); };
     auto read_a = [&](const uint8_t *d, int m) { fa[m & 1] = fragment(d + a_rd + m * 16 * BK); };
     auto read_b = [&](const uint8_t *d, int k) { fb[k] = fragment(d + b_rd + k * 16 * BK); };
-    auto read_scales = [&](const uint8_t *d) {
+    auto read_scales = [&](int st) {
+        const uint8_t *d = ls[st / 4 & 1] + 4 * (blocks >= 4 ? st - first_scale(st) : st);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-            sw[mt] = *(const float *)(d + S_ST + (wm * MT + mt) * 128);
+            sw[mt] = *(const float *)(d + (wm * MT + mt) * 512);
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            sx[k] = *(const float *)(d + S_ST + (BM + wn * NT * 32 + k * 16 + n) * 4);
+            sx[k] = *(const float *)(d + (BM + wn * NT * 32 + k * 16 + n) * 16);
     };
     auto add = [&](int u) {  // tile u's block to its total
-        f4 &t = acc[u / N][u % N];
+        float (&t)[4] = acc[u / N][u % N];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             t[i] = fmaf(part[u & 3][i], s[u % N], t[i]);
@@ -308,7 +314,16 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
+    // Keeps the multiply-adds before the branches that follow them: moved behind one, they would hold on to their blocks' sums.
+    auto settle = [&]() {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                asm volatile("" : "+v"(acc[m][k][0]), "+v"(acc[m][k][1]), "+v"(acc[m][k][2]), "+v"(acc[m][k][3]));
+    };
     // One stage, whose first operands and scales have been read: cur is its buffer, nxt the next stage's.
+    int at = 0;  // the stage
     auto stage = [&](uint8_t *__restrict cur, const uint8_t *__restrict nxt) {
         float f[N];
 #pragma unroll
@@ -324,10 +339,12 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 #pragma unroll
         for (int k = 0; k < N; ++k)
             f[k] = sw[MT - 1] * sx[k];
+        settle();
         turn(Number<AHEAD>{});
         request(cur);
         read_a(nxt, 0);
-        read_scales(nxt);
+        at = at + 1 < blocks ? at + 1 : at;
+        read_scales(at);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             unit((M - 1) * N + k);
@@ -342,13 +359,17 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
         if constexpr (NS == 3)
             request(l2);
     }
+    if (blocks < 4 && tid < BM + BN)
+        *(f4 *)(ls[0] + tid * 16) = f4{scale[0], blocks > 1 ? scale[1] : 0.0f, blocks > 2 ? scale[2] : 0.0f, 0.0f};
     const float *const bias = tile_bias<GROUPED, GATED>(p, tile.expert);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         const f4 b = bias_rows<GATED>(bias, tile.o0, (wm * M + m) * 16 + 4 * g, p.out);
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            acc[m][k] = b;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[m][k][i] = b[i];
     }
     if (full) {
         turn(Number<(NS - 1) * LOADS>{});
@@ -358,7 +379,7 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
             read_b(l0, k);
             s[k] = 0.0f;
         }
-        read_scales(l0);
+        read_scales(0);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             part[i] = (f4)0.0f;
@@ -391,7 +412,6 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
                 const uint8_t *row = src[i] - 16 * c - (full ? (full - 1) * BK : 0);
                 *(u4 *)(l0 + tid * 16 + i * (TH * 16)) = load16_tail(row, full * BK + 16 * c, p.in);
             }
-            *(float *)(l0 + S_ST + tid * 4) = scale[full];
             __syncthreads();
             d = l0;
             skip = 0;
@@ -403,7 +423,7 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
                 v[i] = 16 * (g + 4 * (i / 4)) + 4 * (i % 4) >= skip ? v[i] : 0;
             return v;
         };
-        read_scales(d);
+        read_scales(full);
 #pragma unroll
         for (int k = 0; k < N; ++k)
             fb[k] = keep(d + b_rd + k * 16 * BK);
@@ -465,14 +485,16 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
     const int st = r_in * BK + 16 * (c ^ ((r_in >> 1) & 7));
 
     constexpr int M = 2 * MT, N = 2 * NT;
-    f4 acc[M][N];
+    float acc[M][N][4];
     const float *const bias = tile_bias<GROUPED, GATED>(p, tile.expert);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         const f4 b = bias_rows<GATED>(bias, tile.o0, (wm * M + m) * 16 + 4 * g, p.out);
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            acc[m][k] = b;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[m][k][i] = b[i];
     }
 
     u4 ra[CA], rb[CB];
