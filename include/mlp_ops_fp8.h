@@ -113,7 +113,8 @@ int mlp_fp8_linear(const mlp_fp8_linear_args *args, void *stream);
 
 /* mlp_expert_linear with operands in the format above, each expert's layer as in mlp_fp8_linear.  offsets, slots and
  * places are mlp_dispatch's, with the same clamping; x_scale has a row for each row of x, y_scale for each of y (rows
- * behind offsets[experts] are left as they were).  MLP_DTYPE_FP8 goes without combine. */
+ * behind offsets[experts] are left as they were).  MLP_DTYPE_FP8 goes without combine.  Combined into 16 bits, a term may be
+ * off by 0.51 * 2^-15 of the largest of its 32 neighbouring outputs of the slot; the sum is FP32 and is rounded once. */
 typedef struct mlp_fp8_expert_linear_args {
     int64_t tokens; /* tokens * k: 0 .. INT32_MAX */
     int32_t k;
@@ -146,7 +147,7 @@ typedef struct mlp_fp8_expert_linear_args {
     uint64_t workspace_bytes;
 } mlp_fp8_expert_linear_args;
 
-/* Bytes of workspace mlp_fp8_expert_linear needs, as above; also the FP32 outputs by slot where it combines. */
+/* Bytes of workspace mlp_fp8_expert_linear needs, as above; also the outputs by slot where it combines. */
 int mlp_fp8_expert_linear_workspace(const mlp_fp8_expert_linear_args *args, uint64_t *bytes);
 int mlp_fp8_expert_linear(const mlp_fp8_expert_linear_args *args, void *stream);
 

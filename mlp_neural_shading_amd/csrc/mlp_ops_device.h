@@ -304,6 +304,61 @@ struct __attribute__((packed, aligned(2))) Float8 {
     float v[8];
 };
 
+// Terms of a sum on their way to it, where it is rounded to 16 bits: 32 neighbouring outputs of a row as whole numbers up to
+// 32,766 and their FP32 scale, of which four neighbouring lanes hold 8 each.  Off by at most 0.51 * 2^-15 of the largest of
+// the 32: a 16-bit float's own rounding of the term alone is up to 64 times that (FP16: 8), and FP32 rows are twice the
+// bytes.  Larger numbers stand for infinities and NaN.
+__device__ __forceinline__ u4 to_terms(f8 v, float &scale)
+{
+    typedef short s2 __attribute__((ext_vector_type(2)));
+    float m = 0.0f, odd = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a = fabsf(v[j]);
+        m = fmaxf(m, a < __builtin_inff() ? a : 0.0f);
+        odd = fmaf(v[j], 0.0f, odd);  // 0, or NaN
+    }
+    auto other = [](float w, auto perm) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, w), decltype(perm)::value, 0xf, 0xf, true));
+    };
+    m = fmaxf(m, other(m, Number<0xb1>{}));  // quad_perm 1 0 3 2
+    m = fmaxf(m, other(m, Number<0x4e>{}));  // quad_perm 2 3 0 1
+    scale = fmaxf(m * (1.0f / 32766.0f), 0x1p-126f);
+    const float inv = 1.0f / scale * (1.0f / 32767.0f);
+    u4 q;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        q[j] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_pknorm_i16(v[2 * j] * inv, v[2 * j + 1] * inv));  // times 32,767, nearest
+    if (odd != 0.0f)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (!(fabsf(v[j]) < __builtin_inff())) {
+                s2 t = __builtin_bit_cast(s2, q[j / 2]);
+                t[j % 2] = v[j] > 0.0f ? 32767 : v[j] < 0.0f ? -32767 : -32768;
+                q[j / 2] = __builtin_bit_cast(unsigned, t);
+            }
+    return q;
+}
+
+__device__ __forceinline__ f8 from_terms(u4 q, float scale)
+{
+    typedef short s8 __attribute__((ext_vector_type(8)));
+    const s8 t = __builtin_bit_cast(s8, q);
+    f8 v;
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        v[j] = (float)t[j] * scale;
+        odd |= t[j] == 32767 || t[j] < -32766;
+    }
+    if (odd)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (t[j] == 32767 || t[j] < -32766)
+                v[j] = t[j] == -32768 ? __builtin_nanf("") : t[j] < 0 ? -__builtin_inff() : __builtin_inff();
+    return v;
+}
+
 // The epilogue of one wave: MT x NT MFMA tiles whose first weight row is tile row r0 and first row `row` (the same
 // in all lanes).  One 32 x 32 tile of outputs at a time: the activation and the gate on the sums as they lie, then
 // through 4 KB of LDS of the wave's own (no barrier: one wave writes and reads it) into rows, from which a lane takes
@@ -313,8 +368,8 @@ struct __attribute__((packed, aligned(2))) Float8 {
 // once per tile.  Addresses are a base per tile plus 32 bits per lane (262,144 rows 64 -> 64: 20.4 -> 18.7 us with both).
 // SIXTEEN: a tile is four of 16 x 16, of which lane (g, n) holds outputs 4 g .. 4 g + 3 of row n: element 4 e + i is that
 // of outputs 16 (e / 2) .. and rows 16 (e % 2) ..
-template <class T, bool GATED, bool SIXTEEN = false, int MT, int NT>
-__device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][NT], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
+template <class T, bool GATED, bool SIXTEEN = false, class ARGS, int MT, int NT>
+__device__ __forceinline__ void epilogue(const ARGS &p, f16x (&acc)[MT][NT], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
 {
     typedef typename Vec8<T>::type V8;
     typedef T V4 __attribute__((ext_vector_type(4)));
@@ -363,6 +418,29 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f16x (&acc)[MT][N
             z *= acc[mt + 1][nt];
         const int left = outs - 32 * (t % MO) - oc;  // outputs from this lane's first on
         const int64_t y_tile = (int64_t)(32 * nt) * ldy + 32 * (t % MO), r_tile = (int64_t)(32 * nt) * ldr + 32 * (t % MO);
+        if constexpr (SIXTEEN)
+            if (p.terms) {  // 16-bit whole numbers and a scale for the 32 of a row
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int r = 16 * (q % 2) + (lane & 15);
+                    *(f4 *)(ob + r * 128 + 16 * ((4 * (q / 2) + (lane >> 4)) ^ ((r >> 1) & 7))) = f4{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int rt = 16 * i + rl, sw = (rt >> 1) & 7;
+                    const f4 lo = *(const f4 *)(ob + rt * 128 + 16 * ((oc / 4) ^ sw)), hi = *(const f4 *)(ob + rt * 128 + 16 * ((oc / 4 + 1) ^ sw));
+                    const f8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                    float scale;
+                    const u4 term = to_terms(v, scale);
+                    if (32 * nt + rt >= rows)
+                        continue;
+                    *(u4 *)((int16_t *)p.y + row * p.ldy + first + y_tile + y_at[i]) = term;
+                    if (oc == 0)
+                        p.terms[(row + 32 * nt + rt) * (p.ldy / 32) + first / 32 + t % MO] = scale;
+                }
+                continue;
+            }
         if (!p.residual && !p.y_fp32) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {

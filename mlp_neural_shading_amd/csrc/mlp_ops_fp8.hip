@@ -111,7 +111,7 @@ __device__ __forceinline__ f4 bias_rows(const float *bias, int o0, int r, int ou
 
 // The epilogue of a wave's MT x NT tiles of 32 x 32.
 template <class T, bool GATED, int MT, int NT>
-__device__ __forceinline__ void finish(const ProductArgs &p, float (&acc)[2 * MT][2 * NT][4], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
+__device__ __forceinline__ void finish(const Fp8ProductArgs &p, float (&acc)[2 * MT][2 * NT][4], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
 {
     f16x t[MT][NT];
 #pragma unroll
@@ -243,13 +243,15 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 #pragma unroll
     for (int i = 0; i < CB; ++i)
         src[CA + i] = (const uint8_t *)p.x + input_row<GROUPED>(p, tile.row0 + r_in + i * RPP, tile.row1) * p.ldx + 16 * c;
+    const int x_at = tid - BM < BN ? tid - BM : BN - 1;  // the row of x that this thread serves besides, if it has none of w
     const float *const scale = tid < BM ? p.ws + tile.expert * p.ws_stride + scale_row<GATED>(tile.o0, tid, p.out) * p.ldws
-                                        : p.xs + input_row<GROUPED>(p, tile.row0 + (tid - BM < BN ? tid - BM : BN - 1), tile.row1) * p.ldxs;
+                                        : p.xs + input_row<GROUPED>(p, tile.row0 + x_at, tile.row1) * p.ldxs;
 
     const int full = p.in / BK, rest = p.in - full * BK, blocks = full + (rest != 0);
-    // After the whole stages come the row's last 128 columns, some of them a second time; past them they are requested
-    // again, unused, and so is the last whole stage where `rest` is 0, or no multiple of 4 (the loads' alignment).
-    const int last_step = rest % 4 ? 0 : rest;
+    // After the whole stages come the row's last 128 columns, or those before its last 1 to 3 (the loads are 4-byte aligned),
+    // some of them a second time; past them they are requested again, unused, and so is the last whole stage where `rest`
+    // is less than 4.
+    const int last_step = rest / 4 * 4;
     int issued = 0;  // stages requested
     // The scales come four blocks at a time (a lane per row touches a cache line per row: 16 bytes cost what 4 do), the last
     // four of a row ending with it; of rows with fewer, through registers below.
@@ -401,26 +403,37 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
         for (int u = UN - LAG; u < UN; ++u)
             add(u);
     }
+    unsigned last_word = 0;  // the columns behind the requested ones
+    const bool odd = full && rest % 4;
+    if (odd && tid < BM + BN) {
+        const uint8_t *row = tid < BM ? tile.w + (int64_t)weight_row<GATED>(tile.o0, tid, p.out) * p.ldw
+                                      : (const uint8_t *)p.x + input_row<GROUPED>(p, tile.row0 + x_at, tile.row1) * p.ldx;
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if (j < rest % 4)
+                last_word |= (unsigned)row[p.in - rest % 4 + j] << (8 * j);
+    }
     __builtin_amdgcn_s_waitcnt(0x0070);  // the requests past the end
     __syncthreads();
     if (rest) {
-        const uint8_t *d = NS == 2 ? (full % 2 ? l1 : l0) : full % 3 == 0 ? l0 : full % 3 == 1 ? l1 : l2;
-        int skip = BK - rest;  // columns of the last 128 that the whole stages have had
-        if (!full || !last_step) {  // the rest and zeros, through registers
+        uint8_t *d = !full ? l0 : NS == 2 ? (full % 2 ? l1 : l0) : full % 3 == 0 ? l0 : full % 3 == 1 ? l1 : l2;
+        int skip = BK - last_step;  // columns of the last 128 that the whole stages have had
+        if (!full) {  // the rest and zeros, through registers
 #pragma unroll
-            for (int i = 0; i < CA + CB; ++i) {
-                const uint8_t *row = src[i] - 16 * c - (full ? (full - 1) * BK : 0);
-                *(u4 *)(l0 + tid * 16 + i * (TH * 16)) = load16_tail(row, full * BK + 16 * c, p.in);
-            }
-            __syncthreads();
-            d = l0;
+            for (int i = 0; i < CA + CB; ++i)
+                *(u4 *)(l0 + tid * 16 + i * (TH * 16)) = load16_tail(src[i] - 16 * c, 16 * c, p.in);
             skip = 0;
+        } else if (odd && tid < BM + BN) {  // in place of the row's first word, of columns that the whole stages have had
+            *(unsigned *)(d + tid * BK + 16 * ((tid >> 1) & 7)) = last_word;
         }
+        __syncthreads();
         auto keep = [&](const uint8_t *row) {
             i8 v = fragment(row);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = 16 * (g + 4 * (i / 4)) + 4 * (i % 4) >= skip ? v[i] : 0;
+            for (int i = 0; i < 8; ++i) {
+                const int at = 16 * (g + 4 * (i / 4)) + 4 * (i % 4);
+                v[i] = at >= skip || (at == 0 && odd) ? v[i] : 0;
+            }
             return v;
         };
         read_scales(full);
@@ -689,6 +702,61 @@ __global__ __launch_bounds__(1024) void fp8_few(Fp8ProductArgs p)
     }
 }
 
+// One token's row of a combined product from 16-bit terms, in the order of j and in FP32; 8 outputs per thread.  Bound by the
+// terms' bytes (8,192 tokens x 4 x 2,048: 143 MB).
+template <class T, class INDEX>
+__global__ __launch_bounds__(256) void sum_terms(TermsArgs c)
+{
+    typedef typename Vec8<T>::type V8;
+    struct __attribute__((packed, aligned(2))) Half8 {
+        V8 v;
+    };
+    const INDEX chunks = (c.out + 7) / 8, all = (INDEX)c.tokens * chunks;
+    const int64_t n = c.tokens * c.k;
+    for (INDEX i = (INDEX)blockIdx.x * 256 + threadIdx.x; i < all; i += (INDEX)gridDim.x * 256) {
+        const INDEX t = i / chunks;
+        const int o = (int)(i - t * chunks) * 8;
+        const int32_t *places = c.places + (int64_t)t * c.k;
+        const float *weights = c.weight + (int64_t)t * c.k;
+        f8 v = (f8)0.0f;
+        for (int j0 = 0; j0 < c.k; j0 += 4) {
+            u4 term[4];
+            float scale[4], weight[4];
+            bool on[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int place = j0 + j < c.k ? places[j0 + j] : -1;
+                on[j] = place >= 0 && place < n;  // else dropped
+                weight[j] = on[j] && c.weight ? weights[j0 + j] : 1.0f;
+                if (on[j]) {
+                    term[j] = *(const u4 *)(c.terms + (int64_t)place * c.ld + o);
+                    scale[j] = c.scales[(int64_t)place * (c.ld / 32) + o / 32];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (on[j]) {
+                    const f8 part = from_terms(term[j], scale[j]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = fmaf(weight[j], part[e], v[e]);
+                }
+        }
+        T *y = (T *)c.y + (int64_t)t * c.ldy + o;
+        const T *res = c.residual ? (const T *)c.residual + (int64_t)t * c.ldr + o : nullptr;
+        if (o + 8 <= c.out) {
+            if (res)
+                v += __builtin_convertvector(((const Half8 *)res)->v, f8);
+            ((Half8 *)y)->v = __builtin_convertvector(v, V8);  // nearest even
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (o + e < c.out)
+                    y[e] = (T)(v[e] + (res ? (float)res[e] : 0.0f));
+        }
+    }
+}
+
 // ---- which kernel ---------------------------------------------------------------------------------
 
 // kBig 256 weight rows x 256 rows (FULL: 256 x 128), kMid 128 x 128, kSmall 128 x 64 (all three straight into LDS), kTile
@@ -803,6 +871,29 @@ bool fp8_product_rounds(const Fp8ProductArgs &p, bool gated, bool grouped)
 {
     const Form form = choose_form(p, true, gated, grouped);
     return (form == kBig || form == kMid || form == kSmall) && shape(form, true).bm / (gated ? 2 : 1) % kFp8Block == 0;
+}
+
+bool fp8_product_terms(const Fp8ProductArgs &p, int type, bool gated, bool grouped)
+{
+    const Form form = choose_form(p, type == kFp32, gated, grouped);
+    return type != kFp32 && form != kFew && form != kFewWide;
+}
+
+template <class T>
+hipError_t launch_terms_typed(const TermsArgs &c, hipStream_t stream)
+{
+    const int64_t work = c.tokens * ((c.out + 7) / 8), most = 256 * 32, blocks = (work + 255) / 256;
+    const dim3 grid((unsigned)(blocks < most ? blocks : most));
+    if (work < (int64_t)1 << 31)  // and so is the last step past it
+        hipLaunchKernelGGL((sum_terms<T, unsigned>), grid, dim3(256), 0, stream, c);
+    else
+        hipLaunchKernelGGL((sum_terms<T, int64_t>), grid, dim3(256), 0, stream, c);
+    return hipGetLastError();
+}
+
+hipError_t launch_terms(const TermsArgs &c, int out_dtype, hipStream_t stream)
+{
+    return out_dtype == kFp16 ? launch_terms_typed<_Float16>(c, stream) : launch_terms_typed<__bf16>(c, stream);
 }
 
 const char *fp8_product_kernel(const Fp8ProductArgs &p, int type, bool gated, bool grouped)

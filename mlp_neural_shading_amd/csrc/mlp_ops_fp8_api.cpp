@@ -181,21 +181,34 @@ Fp8ProductArgs sizes(const mlp_fp8_expert_linear_args *a)
     return p;
 }
 
-// The workspace holds FP32 rows: combined slots, or outputs that another kernel rounds to 8 bits.
+// 8-bit outputs have FP32 scales.
+int result_type(int out_dtype) { return out_dtype == MLP_DTYPE_FP8 ? kFp32 : out_dtype; }
+
+// What the workspace holds: rows for another kernel to combine or to round to 8 bits, in FP32, or as 16-bit terms (32's
+// multiple of them a row) and behind them their scales.
+enum Rows { kNoRows, kFp32Rows, kTermRows };
+
+Rows rows_of(const Fp8ProductArgs &p, int out_dtype, bool combine, bool gated, bool grouped)
+{
+    if (combine)
+        return fp8_product_terms(p, result_type(out_dtype), gated, grouped) ? kTermRows : kFp32Rows;
+    return out_dtype == MLP_DTYPE_FP8 && !fp8_product_rounds(p, gated, grouped) ? kFp32Rows : kNoRows;
+}
+
+int64_t term_stride(int out_width) { return round_up(out_width, 32); }
+
 template <class A>
 uint64_t rows_need(const A *a, bool combine, bool grouped)
 {
     const Fp8ProductArgs p = sizes(a);
-    if (p.rows == 0 || !(combine || (a->out_dtype == MLP_DTYPE_FP8 && !fp8_product_rounds(p, a->gated, grouped))))
+    if (p.rows == 0)
         return 0;
-    return (uint64_t)p.rows * part_stride(a->out_width) * 4;
+    const Rows r = rows_of(p, a->out_dtype, combine, a->gated, grouped);
+    return r == kNoRows ? 0 : (uint64_t)p.rows * (r == kTermRows ? term_stride(p.out) * 2 + term_stride(p.out) / 32 * 4 : part_stride(p.out) * 4);
 }
 
 uint64_t linear_need(const mlp_fp8_linear_args *a) { return rows_need(a, false, false); }
 uint64_t expert_linear_need(const mlp_fp8_expert_linear_args *a) { return rows_need(a, a->combine, true); }
-
-// 8-bit outputs have FP32 scales.
-int result_type(int out_dtype) { return out_dtype == MLP_DTYPE_FP8 ? kFp32 : out_dtype; }
 
 int activation(int act, int out_dtype)
 {
@@ -253,7 +266,7 @@ int check_outputs(const A *a, int64_t y_rows, uint64_t need, const Span (&in)[N]
 
 // Where the product's results go.
 template <class A>
-void outputs(const A *a, uint64_t need, Fp8ProductArgs &p)
+void outputs(const A *a, bool combine, bool grouped, Fp8ProductArgs &p)
 {
     p.xs = a->x_scale;
     p.ldxs = a->ldxs;
@@ -261,7 +274,12 @@ void outputs(const A *a, uint64_t need, Fp8ProductArgs &p)
     p.ldws = a->ldws;
     p.bias = a->bias;
     p.act = activation(a->act, a->out_dtype);
-    if (need) {  // FP32 rows, for another kernel to finish
+    const Rows rows = rows_of(p, a->out_dtype, combine, a->gated, grouped);
+    if (rows == kTermRows) {
+        p.y = a->workspace;
+        p.ldy = term_stride(p.out);
+        p.terms = (float *)((int16_t *)a->workspace + p.rows * p.ldy);
+    } else if (rows == kFp32Rows) {
         p.y = a->workspace;
         p.ldy = part_stride(p.out);
         p.y_fp32 = 1;
@@ -291,10 +309,9 @@ int prepare_linear(const mlp_fp8_linear_args *a, Fp8ProductArgs &p)
     const Span in[] = {span(a->x, a->rows, a->in_width, a->ldx, 1), span(a->x_scale, a->rows, blocks, a->ldxs, 4),
                        span(a->w, wide, a->in_width, a->ldw, 1), span(a->w_scale, down, blocks, a->ldws, 4),
                        span(a->bias, 1, wide, wide, 4)};
-    const uint64_t need = linear_need(a);
-    MLP_TRY(check_outputs(a, a->rows, need, in));
+    MLP_TRY(check_outputs(a, a->rows, linear_need(a), in));
     p = sizes(a);
-    outputs(a, need, p);
+    outputs(a, false, false, p);
     if (!fp8_product_fits(p, result_type(a->out_dtype), a->gated, false))
         return fail(MLP_ERR_UNSUPPORTED, "%lld rows of %d outputs are more tiles than one launch holds", (long long)a->rows,
                     a->out_width);
@@ -326,10 +343,9 @@ int prepare_expert_linear(const mlp_fp8_expert_linear_args *a, Fp8ProductArgs &p
                        many(a->w_scale, a->experts, a->ws_stride, down, blocks, a->ldws, 4), span(a->bias, 1, all, all, 4),
                        span(a->offsets, 1, a->experts + 1, a->experts + 1, 4), span(a->slots, 1, n, n, 4),
                        span(a->places, 1, n, n, 4), span(a->weight, 1, n, n, 4)};
-    const uint64_t need = expert_linear_need(a);
-    MLP_TRY(check_outputs(a, y_rows, need, in));
+    MLP_TRY(check_outputs(a, y_rows, expert_linear_need(a), in));
     p = sizes(a);
-    outputs(a, need, p);
+    outputs(a, a->combine, true, p);
     p.ws_stride = a->experts > 1 ? a->ws_stride : 0;
     p.offsets = a->offsets;
     p.slots = a->x_slots ? nullptr : a->slots;
@@ -467,7 +483,24 @@ int mlp_fp8_expert_linear(const mlp_fp8_expert_linear_args *a, void *stream)
     hipError_t err = launch_fp8_product(p, result_type(a->out_dtype), a->gated, true, (hipStream_t)stream);
     if (err != hipSuccess)
         return hip_fail(err, "launching the experts' layer");
-    if (a->combine) {
+    if (a->combine && p.terms) {
+        TermsArgs c{};
+        c.terms = (const int16_t *)p.y;
+        c.scales = p.terms;
+        c.ld = p.ldy;
+        c.places = a->places;
+        c.weight = a->weight;
+        c.residual = a->residual;
+        c.ldr = a->ldr;
+        c.y = a->y;
+        c.ldy = a->ldy;
+        c.tokens = a->tokens;
+        c.k = a->k;
+        c.out = a->out_width;
+        err = launch_terms(c, a->out_dtype, (hipStream_t)stream);
+        if (err != hipSuccess)
+            return hip_fail(err, "launching the combination");
+    } else if (a->combine) {
         CombineArgs c{};
         c.part = (const float *)a->workspace;
         c.ldp = part_stride(a->out_width);
