@@ -793,28 +793,44 @@ float rounds(int64_t tiles, int at_once, bool two_per_cu)
     return whole + (rest == 0.0f ? 0.0f : two_per_cu && rest <= 0.5f ? 0.6f : 1.0f);
 }
 
+bool rounds_itself(Form f, bool gated) { return f <= kSmall && shape(f, true).bm / (gated ? 2 : 1) % kFp8Block == 0; }
+
+// The kernel, for 256 CUs (MI355X); times in us of every kernel forced on the size:
+//   - few tiles of 16 x 16 in all: kFew, whose waves share K, from 512 on 32 weight rows at a time.  1 x 4,096 -> 4,096 7.5
+//     (kSmall 15), 16 rows 7.5 (kFewWide 8.7), 33 rows kFewWide 13.7 (kFew 14.7, kSmall 15.5).  Behind the border: 64 rows kSmall
+//     15.6 (kFewWide 15.5), 128 rows 15.5 (29); widened, 64 rows kFewWide 16.5 (25.7), 128 rows kSmall 25.7 (31.5);
+//   - at most 64 weight rows, or rows that are not 4-byte aligned: kTile, which takes them;
+//   - else the one of kBig, kMid and kSmall that takes the least time by its rounds, each of so much per 1,024 columns and so
+//     much for its start and epilogue, fitted to 65,536 x 1,024 -> 1,024 (86, 109 and 135; widened 183, 172 and 205) and
+//     8,192^3 (457, 562 and 714; 925, 917 and 1,124), and where 8-bit outputs need another kernel, that kernel's launch and the
+//     bytes of the FP32 rows.  It gives kSmall for 512 x 4,096 -> 4,096 (16.5; 23, 50), kMid for 1,024 rows (26; kSmall 27, kBig
+//     51) and kBig for 4,096 (64; 77, 96).
+//     The experts' last tiles count as half full, and from 64 (kMid) and 128 rows (kBig) per expert on.  32 experts, 2,048 ->
+//     2,048, by rows per expert: 32 kSmall 25 (kMid 29, kBig 41), 64 kMid 30 (39; 42), 128 kBig 46 (kMid 54, kSmall 52).
 Form choose_form(const Fp8ProductArgs &p, bool full, bool gated, bool grouped)
 {
     const bool even = p.ldx % 4 == 0 && p.ldw % 4 == 0 && p.w_stride % 4 == 0 && (((uintptr_t)p.x | (uintptr_t)p.w) & 3) == 0;
     const int64_t wide = (int64_t)p.out * (gated ? 2 : 1);
     const int64_t few = row_tiles(p, grouped, 16) * ((wide + 15) / 16);
-    if (few < 1024)
+    if (few < (full ? 1536 : 1024))
         return gated || few >= 512 ? kFewWide : kFew;
     if (!even || wide <= 64)
         return kTile;
     const int64_t used = !grouped ? 0 : p.rows < p.experts ? p.rows : p.experts;
-    auto tiles = [&](Form f) {
+    const float k = (float)p.in / 1024.0f;
+    auto time = [&](Form f, float per_k, float start, int at_once) {
         const int64_t bm = shape(f, full).bm, bn = shape(f, full).bn;
-        return (grouped ? p.rows / bn + (used + 1) / 2 : (p.rows + bn - 1) / bn) * ((wide + bm - 1) / bm);
+        const int64_t tiles = (grouped ? p.rows / bn + (used + 1) / 2 : (p.rows + bn - 1) / bn) * ((wide + bm - 1) / bm);
+        const float more = p.eight && !rounds_itself(f, gated) ? 3.0f + (float)p.rows * p.out * 1.8e-6f : 0.0f;
+        return rounds(tiles, at_once, at_once == 512) * (per_k * k + start) + more;
     };
-    const float k = (float)p.in / 2048.0f;
-    const float big = rounds(tiles(kBig), 256, false) * (26.5f * k + 9.5f);
-    const float mid = rounds(tiles(kMid), 512, true) * (15.5f * k + 8.5f);
-    const float small = rounds(tiles(kSmall), 512, true) * (10.4f * k + 5.5f);
+    const float big = full ? time(kBig, 13.8f, 8.7f, 256) : time(kBig, 13.2f, 8.3f, 256);
+    const float mid = full ? time(kMid, 14.2f, 7.1f, 512) : time(kMid, 8.1f, 5.5f, 512);
+    const float small = full ? time(kSmall, 8.8f, 3.8f, 512) : time(kSmall, 5.2f, 3.3f, 512);
     const int64_t each = used ? p.rows / used : INT64_MAX;  // rows per expert
-    if (each >= 192 && big <= mid && big <= small)
+    if (each >= shape(kBig, full).bn / 2 && big <= mid && big <= small)
         return kBig;
-    return each >= 96 && mid <= small ? kMid : kSmall;
+    return each >= 64 && mid <= small ? kMid : kSmall;
 }
 
 template <class T, bool FULL, bool GROUPED, bool GATED>
@@ -869,8 +885,7 @@ bool fp8_product_fits(const Fp8ProductArgs &p, int type, bool gated, bool groupe
 
 bool fp8_product_rounds(const Fp8ProductArgs &p, bool gated, bool grouped)
 {
-    const Form form = choose_form(p, true, gated, grouped);
-    return (form == kBig || form == kMid || form == kSmall) && shape(form, true).bm / (gated ? 2 : 1) % kFp8Block == 0;
+    return rounds_itself(choose_form(p, true, gated, grouped), gated);
 }
 
 bool fp8_product_terms(const Fp8ProductArgs &p, int type, bool gated, bool grouped)

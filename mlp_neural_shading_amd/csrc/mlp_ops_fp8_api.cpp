@@ -158,6 +158,7 @@ Fp8ProductArgs sizes(const mlp_fp8_linear_args *a)
     p.rows = a->rows;
     p.in = a->in_width;
     p.out = a->out_width;
+    p.eight = a->out_dtype == MLP_DTYPE_FP8;
     p.x = a->x;
     p.ldx = a->ldx;
     p.w = a->w;
@@ -171,6 +172,7 @@ Fp8ProductArgs sizes(const mlp_fp8_expert_linear_args *a)
     p.rows = a->tokens * a->k;
     p.in = a->in_width;
     p.out = a->out_width;
+    p.eight = a->out_dtype == MLP_DTYPE_FP8;
     p.x = a->x;
     p.ldx = a->ldx;
     p.w = a->w;

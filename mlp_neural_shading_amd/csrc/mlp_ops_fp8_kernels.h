@@ -49,6 +49,7 @@ struct Fp8ProductArgs : ProductArgs {
     int64_t ldxs;
     const float *ws;
     int64_t ldws, ws_stride;
+    bool eight;       // 8-bit outputs, here or by another kernel from FP32 rows
     uint8_t *values;  // 8-bit outputs, or NULL: then y
     int64_t ldv;
     float *ys;
