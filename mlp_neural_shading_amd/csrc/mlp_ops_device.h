@@ -367,8 +367,10 @@ __device__ __forceinline__ f8 from_terms(u4 q, float scale)
 // n * 128 + 16 (k ^ ((n / 2) % 8))).  The residual is requested kAhead tiles ahead: its latency would otherwise stand
 // once per tile.  Addresses are a base per tile plus 32 bits per lane (262,144 rows 64 -> 64: 20.4 -> 18.7 us with both).
 // SIXTEEN: a tile is four of 16 x 16, of which lane (g, n) holds outputs 4 g .. 4 g + 3 of row n: element 4 e + i is that
-// of outputs 16 (e / 2) .. and rows 16 (e % 2) ..
-template <class T, bool GATED, bool SIXTEEN = false, class ARGS, int MT, int NT>
+// of outputs 16 (e / 2) .. and rows 16 (e % 2) ..  OUT: what is written, where the kernel is for one kind (the branches of
+// the others cost 10 us of 96 in 65,536 x 1,024 -> 1,024 with 8-bit operands).
+enum { kAnyRows = -1, kHalfRows, kWholeRows, kTermRows };  // 16 bits or FP32 by p.y_fp32, 16 bits, FP32, terms
+template <class T, bool GATED, bool SIXTEEN = false, int OUT = kAnyRows, class ARGS, int MT, int NT>
 __device__ __forceinline__ void epilogue(const ARGS &p, f16x (&acc)[MT][NT], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
 {
     typedef typename Vec8<T>::type V8;
@@ -377,12 +379,13 @@ __device__ __forceinline__ void epilogue(const ARGS &p, f16x (&acc)[MT][NT], uin
         V8 v;
     };
     const int lane = threadIdx.x & 63, g = lane >> 5, n = lane & 31;
-    constexpr int MO = GATED ? MT / 2 : MT, TILES = MO * NT, kAhead = TILES < 4 ? TILES : 4;
+    constexpr int MO = GATED ? MT / 2 : MT, TILES = MO * NT, AHEAD = SIXTEEN ? 2 : 4, kAhead = TILES < AHEAD ? TILES : AHEAD;
+    const bool y_fp32 = OUT == kAnyRows ? p.y_fp32 : OUT == kWholeRows;
     const int first = o0 + (GATED ? r0 / 2 : r0);            // output
     const int rows = (int)(row1 - row < 32 * NT ? row1 - row : 32 * NT);  // may be 0 or less
     const int outs = p.out - first;
     const int oc = 8 * (lane & 3), rl = lane >> 2;  // this lane's outputs and (of 16 at a time) row
-    const bool half_res = p.residual && !p.y_fp32;
+    const bool half_res = p.residual && !y_fp32;
     T *const y16 = (T *)p.y + row * p.ldy + first;
     float *const y32 = (float *)p.y + row * p.ldy + first;
     const T *const r16 = (const T *)p.residual + row * p.ldr + first;
@@ -406,6 +409,9 @@ __device__ __forceinline__ void epilogue(const ARGS &p, f16x (&acc)[MT][NT], uin
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
         const int mt = (t % MO) * (GATED ? 2 : 1), nt = t / MO;
+        if constexpr (SIXTEEN)  // also where this tile is left out
+            if (half_res && t + kAhead < TILES)
+                fetch(t + kAhead);
         if (32 * nt >= rows || 32 * (t % MO) >= outs)
             continue;
         f16x z = acc[mt][nt];
@@ -418,30 +424,29 @@ __device__ __forceinline__ void epilogue(const ARGS &p, f16x (&acc)[MT][NT], uin
             z *= acc[mt + 1][nt];
         const int left = outs - 32 * (t % MO) - oc;  // outputs from this lane's first on
         const int64_t y_tile = (int64_t)(32 * nt) * ldy + 32 * (t % MO), r_tile = (int64_t)(32 * nt) * ldr + 32 * (t % MO);
-        if constexpr (SIXTEEN)
-            if (p.terms) {  // 16-bit whole numbers and a scale for the 32 of a row
+        if constexpr (OUT == kTermRows) {  // 16-bit whole numbers and a scale for the 32 of a row
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int r = 16 * (q % 2) + (lane & 15);
-                    *(f4 *)(ob + r * 128 + 16 * ((4 * (q / 2) + (lane >> 4)) ^ ((r >> 1) & 7))) = f4{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
-                }
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int rt = 16 * i + rl, sw = (rt >> 1) & 7;
-                    const f4 lo = *(const f4 *)(ob + rt * 128 + 16 * ((oc / 4) ^ sw)), hi = *(const f4 *)(ob + rt * 128 + 16 * ((oc / 4 + 1) ^ sw));
-                    const f8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                    float scale;
-                    const u4 term = to_terms(v, scale);
-                    if (32 * nt + rt >= rows)
-                        continue;
-                    *(u4 *)((int16_t *)p.y + row * p.ldy + first + y_tile + y_at[i]) = term;
-                    if (oc == 0)
-                        p.terms[(row + 32 * nt + rt) * (p.ldy / 32) + first / 32 + t % MO] = scale;
-                }
-                continue;
+            for (int q = 0; q < 4; ++q) {
+                const int r = 16 * (q % 2) + (lane & 15);
+                *(f4 *)(ob + r * 128 + 16 * ((4 * (q / 2) + (lane >> 4)) ^ ((r >> 1) & 7))) = f4{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
             }
-        if (!p.residual && !p.y_fp32) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int rt = 16 * i + rl, sw = (rt >> 1) & 7;
+                const f4 lo = *(const f4 *)(ob + rt * 128 + 16 * ((oc / 4) ^ sw)), hi = *(const f4 *)(ob + rt * 128 + 16 * ((oc / 4 + 1) ^ sw));
+                const f8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                float scale;
+                const u4 term = to_terms(v, scale);
+                if (32 * nt + rt >= rows)
+                    continue;
+                *(u4 *)((int16_t *)p.y + row * p.ldy + first + y_tile + y_at[i]) = term;
+                if (oc == 0)
+                    p.terms[(row + 32 * nt + rt) * (p.ldy / 32) + first / 32 + t % MO] = scale;
+            }
+            continue;
+        }
+        if (!p.residual && !y_fp32) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const f4 v = {z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
@@ -472,8 +477,9 @@ __device__ __forceinline__ void epilogue(const ARGS &p, f16x (&acc)[MT][NT], uin
             const int r = SIXTEEN ? 16 * (q % 2) + (lane & 15) : n, k = SIXTEEN ? 4 * (q / 2) + (lane >> 4) : 2 * q + g;
             *(f4 *)(ob + r * 128 + 16 * (k ^ ((r >> 1) & 7))) = f4{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
         }
-        if (half_res && t + kAhead < TILES)
-            fetch(t + kAhead);
+        if constexpr (!SIXTEEN)  // kAhead is a multiple of MO: a tile that is left out has its successor left out too
+            if (half_res && t + kAhead < TILES)
+                fetch(t + kAhead);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -485,7 +491,7 @@ __device__ __forceinline__ void epilogue(const ARGS &p, f16x (&acc)[MT][NT], uin
             if (left >= 8) {
                 const f4 lo = *(const f4 *)(lr + 16 * ((oc / 4) ^ sw)), hi = *(const f4 *)(lr + 16 * ((oc / 4 + 1) ^ sw));
                 f8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                if (p.y_fp32) {
+                if (y_fp32) {
                     if (p.residual) {
                         const Float8 r = *(const Float8 *)(r32 + r_tile + r_at[i]);
 #pragma unroll
@@ -507,8 +513,8 @@ __device__ __forceinline__ void epilogue(const ARGS &p, f16x (&acc)[MT][NT], uin
                 for (int j = 0; j < left; ++j) {
                     float v = *(const float *)(lr + 16 * ((oc / 4 + j / 4) ^ sw) + 4 * (j % 4));
                     if (p.residual)
-                        v += p.y_fp32 ? r32[r_tile + r_at[i] + j] : (float)r16[r_tile + r_at[i] + j];
-                    if (p.y_fp32)
+                        v += y_fp32 ? r32[r_tile + r_at[i] + j] : (float)r16[r_tile + r_at[i] + j];
+                    if (y_fp32)
                         y32[y_tile + y_at[i] + j] = v;
                     else
                         y16[y_tile + y_at[i] + j] = (T)v;

@@ -9,6 +9,8 @@
 #include "mlp_ops_fp8_kernels.h"
 #include "mlp_ops_quant.h"
 
+#include <type_traits>
+
 namespace mlpk {
 
 namespace {
@@ -121,7 +123,12 @@ __device__ __forceinline__ void finish(const Fp8ProductArgs &p, float (&acc)[2 *
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 t[mt][nt][j] = acc[2 * mt + j / 8][2 * nt + j / 4 % 2][j % 4];
-    epilogue<T, GATED, true>(p, t, ob, o0, r0, row, row1);
+    if constexpr (std::is_same<T, float>::value)
+        epilogue<_Float16, GATED, true, kWholeRows>(p, t, ob, o0, r0, row, row1);
+    else if constexpr (std::is_same<T, int16_t>::value)
+        epilogue<_Float16, GATED, true, kTermRows>(p, t, ob, o0, r0, row, row1);
+    else
+        epilogue<T, GATED, true, kHalfRows>(p, t, ob, o0, r0, row, row1);
 }
 
 // The epilogue into 8 bits, for a workgroup whose BO outputs are whole blocks of 128: a block's outputs lie in several waves,
@@ -208,13 +215,16 @@ __device__ __forceinline__ void finish8(const Fp8ProductArgs &p, float (&acc)[2 
     }
 }
 
+// T is what a kernel writes: _Float16 or __bf16 rows, float (FULL: FP32 or 8-bit rows) or int16_t (terms).
+//
 // WM x WN waves, each MT x NT tiles of 32 weight rows x 32 rows, as four of 16 x 16.  A stage is 128 columns, 128 bytes
 // of every row; NS stages go from memory straight into LDS, and so do the rows' scales, for four blocks at a time.  Chunk c (16 bytes) of row r sits at slot c ^ ((r / 2) % 8), as in the 16-bit products.  A tile's multiply-adds
 // follow the matrix instructions of the next tiles, and the stage's last row of tiles is multiplied after the barrier that
 // frees it, while the next stage's first operands are read.
-template <class T, bool FULL, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int NS, int WPE>
+template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int NS, int WPE>
 __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void fp8_big(Fp8ProductArgs p)
 {
+    constexpr bool FULL = std::is_same<T, float>::value;
     constexpr int BK = kFp8Block, TH = 64 * WM * WN, BM = 32 * WM * MT, BN = 32 * WN * NT;
     constexpr int RPP = TH / 8, M = 2 * MT, N = 2 * NT, UN = M * N, LAG = N >= 4 ? 2 : 1;
     constexpr int CA = BM / RPP, CB = BN / RPP;  // 16-byte loads per thread and stage
@@ -466,9 +476,10 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 
 // The same through registers, for rows at any address: each thread loads its chunks of stage s + 1 while stage s is
 // multiplied.
-template <class T, bool FULL, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int WPE>
+template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int WPE>
 __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void fp8_tile(Fp8ProductArgs p)
 {
+    constexpr bool FULL = std::is_same<T, float>::value;
     constexpr int BK = kFp8Block, TH = 64 * WM * WN, BM = 32 * WM * MT, BN = 32 * WN * NT;
     constexpr int RPP = TH / 8;
     constexpr int CA = BM / RPP, CB = BN / RPP;
@@ -833,46 +844,51 @@ Form choose_form(const Fp8ProductArgs &p, bool full, bool gated, bool grouped)
     return each >= 64 && mid <= small ? kMid : kSmall;
 }
 
-template <class T, bool FULL, bool GROUPED, bool GATED>
+template <class T, bool GROUPED, bool GATED>
 hipError_t launch(const Fp8ProductArgs &p, hipStream_t stream)
 {
+    constexpr bool FULL = std::is_same<T, float>::value;
+    typedef typename std::conditional<std::is_same<T, __bf16>::value, __bf16, _Float16>::type Half;  // where a kernel asks p.y_fp32
     const Form form = choose_form(p, FULL, GATED, GROUPED);
     const Shape s = shape(form, FULL);
     const dim3 grid((unsigned)tiles_most(p, FULL, GATED, GROUPED, form)), block(s.threads);
     switch (form) {
     case kBig:
         if constexpr (FULL)
-            hipLaunchKernelGGL((fp8_big<T, FULL, GROUPED, GATED, 4, 2, 2, 2, 2, 2>), grid, block, 0, stream, p);
+            hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 4, 2, 2, 2, 2, 2>), grid, block, 0, stream, p);
         else
-            hipLaunchKernelGGL((fp8_big<T, FULL, GROUPED, GATED, 2, 4, 4, 2, 2, 2>), grid, block, 0, stream, p);
+            hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 2, 4, 4, 2, 2, 2>), grid, block, 0, stream, p);
         break;
     case kMid:
-        hipLaunchKernelGGL((fp8_big<T, FULL, GROUPED, GATED, 2, 2, 2, 2, 2, 2>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 2, 2, 2, 2, 2, 2>), grid, block, 0, stream, p);
         break;
     case kSmall:
-        hipLaunchKernelGGL((fp8_big<T, FULL, GROUPED, GATED, 2, 2, 2, 1, 3, 2>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 2, 2, 2, 1, 3, 2>), grid, block, 0, stream, p);
         break;
     case kTile:
-        hipLaunchKernelGGL((fp8_tile<T, FULL, GROUPED, GATED, 1, 4, 2, 1, 2>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((fp8_tile<T, GROUPED, GATED, 1, 4, 2, 1, 2>), grid, block, 0, stream, p);
         break;
     default:
         // a block for each of up to 16 waves
         const int blocks = (p.in + kFp8Block - 1) / kFp8Block, waves = blocks < 16 ? blocks : 16;
         const size_t lds = (size_t)waves * s.bm * 16 * 4;
         if (GATED || form == kFewWide)
-            hipLaunchKernelGGL((fp8_few<T, FULL, GROUPED, GATED, 2>), grid, dim3(64 * waves), lds, stream, p);
+            hipLaunchKernelGGL((fp8_few<Half, FULL, GROUPED, GATED, 2>), grid, dim3(64 * waves), lds, stream, p);
         else
-            hipLaunchKernelGGL((fp8_few<T, FULL, GROUPED, GATED, GATED ? 2 : 1>), grid, dim3(64 * waves), lds, stream, p);
+            hipLaunchKernelGGL((fp8_few<Half, FULL, GROUPED, GATED, GATED ? 2 : 1>), grid, dim3(64 * waves), lds, stream, p);
     }
     return hipGetLastError();
 }
 
-template <class T, bool FULL>
+template <class T>
 hipError_t launch(const Fp8ProductArgs &p, bool gated, bool grouped, hipStream_t stream)
 {
     if (grouped)
-        return gated ? launch<T, FULL, true, true>(p, stream) : launch<T, FULL, true, false>(p, stream);
-    return gated ? launch<T, FULL, false, true>(p, stream) : launch<T, FULL, false, false>(p, stream);
+        return gated ? launch<T, true, true>(p, stream) : launch<T, true, false>(p, stream);
+    if constexpr (std::is_same<T, int16_t>::value)  // terms are of slots
+        return hipErrorInvalidValue;
+    else
+        return gated ? launch<T, false, true>(p, stream) : launch<T, false, false>(p, stream);
 }
 
 }  // namespace
@@ -919,9 +935,11 @@ const char *fp8_product_kernel(const Fp8ProductArgs &p, int type, bool gated, bo
 
 hipError_t launch_fp8_product(const Fp8ProductArgs &p, int type, bool gated, bool grouped, hipStream_t stream)
 {
-    return type == kFp16 ? launch<_Float16, false>(p, gated, grouped, stream)
-           : type == kBf16 ? launch<__bf16, false>(p, gated, grouped, stream)
-                           : launch<_Float16, true>(p, gated, grouped, stream);
+    if (p.terms)
+        return launch<int16_t>(p, gated, grouped, stream);
+    return type == kFp16 ? launch<_Float16>(p, gated, grouped, stream)
+           : type == kBf16 ? launch<__bf16>(p, gated, grouped, stream)
+                           : launch<float>(p, gated, grouped, stream);
 }
 
 }  // namespace mlpk
