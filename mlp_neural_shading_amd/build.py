@@ -32,6 +32,9 @@ SOURCES = ["mlp_kernels.hip", "mlp_kernels_fp8.hip", "mlp_layered.hip", "mlp_pac
 CEILING_SOURCE = "mlp_ceiling.hip"
 CEILING_LIB = PKG / "libmlp_ceiling.so"
 
+TORCH_SOURCE = "mlp_torch_fp8.cpp"  # the torch form's usual call as a Python extension
+TORCH_LIB = PKG / "_torch_fp8.so"
+
 
 INCLUDE = PKG.parent / "include"
 
@@ -44,17 +47,48 @@ def _compile(src: Path, obj: Path, extra) -> None:
         raise RuntimeError("hipcc failed for %s:\n%s\n%s" % (src.name, " ".join(cmd), r.stderr[-8000:]))
 
 
+def _compile_torch(obj: Path) -> None:
+    import torch
+    from sysconfig import get_paths
+
+    at = Path(torch.__file__).parent / "include"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", str(INCLUDE), "-isystem", str(at), "-isystem",
+           str(at / "torch" / "csrc" / "api" / "include"), "-isystem", "/opt/rocm/include", "-isystem", get_paths()["include"], "-c",
+           str(CSRC / TORCH_SOURCE), "-o", str(obj)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (TORCH_SOURCE, " ".join(cmd), r.stderr[-8000:]))
+
+
+def _link_torch(obj: Path) -> None:
+    import torch
+
+    libs = Path(torch.__file__).parent / "lib"
+    tmp = TORCH_LIB.with_name(TORCH_LIB.name + ".tmp%d" % os.getpid())
+    cmd = ["g++", "-shared", "-fPIC", str(obj), "-o", str(tmp), "-L", str(libs), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_hip",
+           "-lc10", "-lc10_hip", "-L", str(PKG), "-l:" + LIB.name, "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr[-8000:]))
+    os.replace(tmp, TORCH_LIB)
+
+
 def build(verbose: bool = False, extra=()) -> Path:
     BUILD_DIR.mkdir(exist_ok=True)
     objs = [BUILD_DIR / (Path(s).stem + ".o") for s in SOURCES]
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    torch_obj = BUILD_DIR / "mlp_torch_fp8.o"
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_torch, torch_obj)
         list(ex.map(lambda so: _compile(CSRC / so[0], so[1], list(extra)), zip(SOURCES, objs)))
+        binding.result()
     tmp = LIB.with_name(LIB.name + ".tmp%d" % os.getpid())
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", *map(str, objs), "-o", str(tmp)]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr[-8000:]))
     os.replace(tmp, LIB)
+    _link_torch(torch_obj)
     # the benchmark's MFMA-ceiling probe, a separate small library
     cobj = BUILD_DIR / "mlp_ceiling.o"
     _compile(CSRC / CEILING_SOURCE, cobj, list(extra))
@@ -65,7 +99,7 @@ def build(verbose: bool = False, extra=()) -> Path:
         raise RuntimeError("link failed for the ceiling probe:\n%s" % r.stderr[-8000:])
     os.replace(tmp, CEILING_LIB)
     if verbose:
-        print("built", LIB, "and", CEILING_LIB)
+        print("built %s, %s and %s" % (LIB, TORCH_LIB, CEILING_LIB))
     return LIB
 
 

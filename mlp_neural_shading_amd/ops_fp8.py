@@ -4,8 +4,9 @@ the experts' layers on routed rows (``expert_linear``).
 
 ``Quantized`` pairs E4M3 values with an FP32 scale for each block of 128 columns, of one row (activations) or of 128
 rows (weights).  As in ``ops``: tensors are checked, outputs and scratch memory come from torch's allocator on the
-current stream, nothing here computes or waits, and inputs that require gradients are refused.  A layer of experts
-with its weights rounded once::
+current stream, nothing here computes or waits, and inputs that require gradients are refused.  The usual call of each
+(new outputs, the current device) goes through an extension in C++, ``_torch_fp8``, which leaves any other to the
+functions here.  A layer of experts with its weights rounded once::
 
     w1, w2 = ops_fp8.quantize(w1, block_rows=128, gated=True), ops_fp8.quantize(w2, block_rows=128)
 
@@ -21,7 +22,12 @@ import ctypes
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
+try:
+    from . import _torch_fp8 as _usual
+except ImportError as e:
+    raise RuntimeError("the extension _torch_fp8 is not built; run `python -m mlp_neural_shading_amd.build`: %s" % e) from e
 from .ops import (ACTIVATIONS, DTYPES, Dispatch, _call, _choice, _count, _f32, _FLOATS, _i32, _i64, _matrix, _out_dtype,
                   _p, _packer, _tensor, _u64, _vector, _workspace, _written)
 
@@ -104,6 +110,11 @@ def rms_norm(x, weight=None, *, residual=None, total=None, eps=1e-6, out="same",
     ``out``: "same" gives ``y`` in x's type (or ``out_dtype`` float32), "fp8" the normed rows ``quantized``, "both" both."""
     if out not in ("same", "fp8", "both"):
         raise ValueError("out must be same, fp8 or both, got %r" % (out,))
+    if total is None and forward_ad._current_level < 0 and (out_dtype is None or out_dtype is torch.float32):
+        r = _usual.rms_norm(x, weight, residual, eps, out != "fp8", out != "same", out_dtype is not None)
+        if r is not None:
+            y, values, scales, total = r
+            return Normed(y, None if values is None else Quantized(values, scales), total)
     ldx = _matrix("x", x, _FLOATS)
     rows, width = x.shape
     device, dtype = x.device, x.dtype
@@ -142,6 +153,10 @@ def quantize(x, *, block_rows=1, gated=False) -> Quantized:
 
     ``block_rows`` 1: a scale for each row and 128 columns (activations); 128: for 128 rows and 128 columns (weights).
     ``gated``: the weights of a gated layer, whose two halves of the rows are matrices of their own."""
+    if not gated and forward_ad._current_level < 0:
+        r = _usual.quantize(x, block_rows)
+        if r is not None:
+            return Quantized(*r)
     block_rows = _count("block_rows", block_rows)
     if block_rows not in (1, BLOCK):
         raise ValueError("block_rows must be 1 or %d, got %d" % (BLOCK, block_rows))
@@ -240,6 +255,10 @@ def linear(x: Quantized, w: Quantized, bias=None, *, residual=None, act="none", 
     ``act`` one of ``ops.ACTIVATIONS``.  ``gated``: w and bias have 2 * out rows, the gates first, with blocks of their
     own (``quantize(gated=True)``).  ``out_dtype`` float16, bfloat16, float32 (a residual's too, which may be ``out``
     itself), or float8_e4m3fn, which gives ``Quantized`` rows and takes no residual."""
+    if out is None and forward_ad._current_level < 0:
+        r = _usual.linear(x, w, bias, residual, ACTIVATIONS.get(act), gated, _OUT.get(out_dtype))
+        if r is not None:
+            return Quantized(*r) if out_dtype is FP8 else r
     device, rows, k, n, _, operand, weights, b = _layer(x, w, bias, gated, False)
     given = out is not None
     out, y, ldy, ys, ldys = _outputs(out, out_dtype, rows, n, device)
@@ -261,6 +280,11 @@ def expert_linear(x: Quantized, w: Quantized, plan: Dispatch, bias=None, *, k, a
     rows for the next layer."""
     if rows not in ("tokens", "slots"):
         raise ValueError("rows must be tokens or slots, got %r" % (rows,))
+    if out is None and forward_ad._current_level < 0 and isinstance(plan, Dispatch):
+        r = _usual.expert_linear(x, w, *plan, bias, k, ACTIVATIONS.get(act), gated, rows == "slots", combine, weight, residual,
+                                 _OUT.get(out_dtype))
+        if r is not None:
+            return Quantized(*r) if out_dtype is FP8 else r
     k = _count("k", k)
     device, x_rows, k_in, n, experts, operand, weights, b = _layer(x, w, bias, gated, True)
     if not isinstance(plan.places, torch.Tensor) or k < 1 or plan.places.numel() % k:

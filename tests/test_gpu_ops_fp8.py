@@ -9,6 +9,7 @@ import torch
 import ops_fp8_reference as F
 import ops_reference as R
 from gpu_util import device, log
+from mlp_neural_shading_amd import binding as B
 from mlp_neural_shading_amd import ops
 from mlp_neural_shading_amd import ops_fp8 as E
 
@@ -527,6 +528,88 @@ def test_same_call_same_bits():
     x = gpu(rnd(gen(1), 777, 200, dtype=t))
     first = layer_of_experts(x, x, *weights, 3)[0]
     assert all(torch.equal(first, layer_of_experts(x, x, *weights, 3)[0]) for _ in range(5))
+
+
+class Never:
+    """Stands for the extension: leaves every call to the functions in Python."""
+
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+def flat(r):
+    return [t for x in r for t in (flat(x) if isinstance(x, tuple) else [x])] if isinstance(r, tuple) else [r]
+
+
+@pytest.mark.parametrize("rows,k,n", [(1, 128, 40), (5, 1001, 130), (300, 264, 300)])
+def test_both_ways_to_the_library_are_one(rows, k, n, monkeypatch):
+    """The usual call through the extension, and the same through the checks in Python: bits, types, shapes and strides."""
+    g = gen(k)
+    (x, w), (_, wg) = operands(g, rows, k, n), operands(g, rows, k, n, True)
+    X, W, WG = on_gpu(x), on_gpu(w), on_gpu(wg)
+    f, r, weight = gpu(rnd(g, rows, k)), gpu(rnd(g, rows, k)), gpu(rnd(g, k))
+    b, res = gpu(rnd(g, n)), gpu(rnd(g, rows, n))
+    index = torch.randint(-1, 3, (rows, 2), generator=g, dtype=torch.int32).to(device())
+    plan = ops.dispatch(index, 3)
+    w3 = on_gpu(expert_weights(g, 3, n, k, False))
+    calls = [lambda: E.rms_norm(f), lambda: E.rms_norm(f.half(), weight.half(), residual=r.half(), out="both", eps=1e-3),
+             lambda: E.rms_norm(f.bfloat16(), weight.bfloat16(), out="fp8"), lambda: E.rms_norm(f.half(), out_dtype=torch.float32),
+             lambda: E.quantize(f), lambda: E.quantize(f.half(), block_rows=128), lambda: E.linear(X, W),
+             lambda: E.linear(X, W, b, residual=res.half(), act="gelu", out_dtype=torch.float16),
+             lambda: E.linear(X, WG, act="silu", gated=True, out_dtype=FP8), lambda: E.linear(X, W, out_dtype=torch.float32),
+             lambda: E.expert_linear(X, w3, plan, k=2, combine=True, weight=torch.ones(rows, 2, device=device()), residual=res.bfloat16()),
+             lambda: E.expert_linear(X, w3, plan, k=2, combine=True, out_dtype=torch.float32)]
+    usual = E._usual
+    seen = []
+
+    class Spy:
+        def __getattr__(self, name):
+            def call(*a):
+                seen.append(getattr(usual, name)(*a) is not None)
+                return getattr(usual, name)(*a)
+            return call
+    for call in calls:
+        monkeypatch.setattr(E, "_usual", Spy())
+        a = flat(call())
+        monkeypatch.setattr(E, "_usual", Never())
+        for p, q in zip(a, flat(call())):
+            assert (p is None) == (q is None)
+            if p is not None:
+                assert p.dtype == q.dtype and p.shape == q.shape and p.stride() == q.stride()
+                assert torch.equal(bits(p), bits(q))
+    assert len(seen) == len(calls) and all(seen)
+
+
+def test_unusual_calls_are_left_to_the_checks():
+    """Each is refused with Python's own words, whatever the extension sees of it."""
+    d = device()
+    x, w = E.quantize(torch.ones(4, 130, device=d)), E.quantize(torch.ones(8, 130, device=d), block_rows=128)
+    f = torch.ones(4, 130, device=d)
+    plan = ops.dispatch(torch.zeros(4, 2, dtype=torch.int32, device=d), 1)
+    w3 = E.Quantized(w.values[None], w.scales[None])
+    for call, says in ((lambda: E.linear(x, E.Quantized(w.values[:, :129], w.scales)), "w must be"),
+                       (lambda: E.linear(x, E.Quantized(w.values, w.scales[:, :1])), "w.scales must be"),
+                       (lambda: E.linear(E.Quantized(x.values, x.scales[:3]), w), "x.scales must be"),
+                       (lambda: E.linear(x, w, torch.ones(7, device=d)), "bias"), (lambda: E.linear(x, w, torch.ones(8, device=d).half()), "bias"),
+                       (lambda: E.linear(x, w, act="tanh"), "act"), (lambda: E.linear(x, w, out_dtype=torch.float64), "out_dtype"),
+                       (lambda: E.linear(x, w, residual=torch.ones(4, 8, device=d)), "residual"),
+                       (lambda: E.linear(x, E.Quantized(w.values[:7], w.scales), gated=True), "even"),
+                       (lambda: E.linear(x, w, residual=f[:, :8].bfloat16().requires_grad_()), "gradient"),
+                       (lambda: E.rms_norm(f, f[0, :7]), "weight"), (lambda: E.rms_norm(f, residual=f[:3]), "residual must be"),
+                       (lambda: E.rms_norm(f, residual=f.half()), "of type"), (lambda: E.rms_norm(f.t()), "contiguous"),
+                       (lambda: E.rms_norm(f.clone().requires_grad_()), "gradient"), (lambda: E.rms_norm(f, out_dtype=torch.float16), "out_dtype"),
+                       (lambda: E.rms_norm(f, total=f), "total"), (lambda: E.quantize(f.t()), "contiguous"),
+                       (lambda: E.quantize(f, block_rows=2), "block_rows"), (lambda: E.quantize(f[:3], block_rows=128, gated=True), "even"),
+                       (lambda: E.expert_linear(x, w3, plan, k=3), "places"), (lambda: E.expert_linear(x, w3, plan, k=1), "rows, the plan"),
+                       (lambda: E.expert_linear(x, w, plan, k=2), "3-D"), (lambda: E.expert_linear(x, w3, plan, k=2.0), "whole"),
+                       (lambda: E.expert_linear(x, w3, plan._replace(offsets=plan.offsets[:1]), k=2), "offsets"),
+                       (lambda: E.expert_linear(x, w3, plan, k=2, combine=True, weight=torch.ones(4, device=d)), "weight")):
+        with pytest.raises(ValueError, match=says):
+            call()
+    for call, says in ((lambda: E.rms_norm(f, eps=0.0), "eps"), (lambda: E.linear(x, w, residual=torch.ones(4, 8, dtype=torch.uint8, device=d).view(FP8), out_dtype=FP8), "residual"),
+                       (lambda: E.expert_linear(x, w3, plan, k=2, combine=True, out_dtype=FP8), "combine")):
+        with pytest.raises(B.MlpError, match=says):
+            call()
 
 
 def test_no_rows():
