@@ -770,16 +770,17 @@ __global__ __launch_bounds__(256) void sum_terms(TermsArgs c)
 
 // ---- which kernel ---------------------------------------------------------------------------------
 
-// kBig 256 weight rows x 256 rows (FULL: 256 x 128), kMid 128 x 128, kSmall 128 x 64 (all three straight into LDS), kTile
-// 64 x 128 through registers, kFew 16 x 16, kFewWide 32 x 16.
+// kBig 256 weight rows x 256 rows (FULL: 256 x 128), kMid 128 x 128 (of 8 waves; FULL: of 4), kSmall 128 x 64 (all three
+// straight into LDS), kTile 64 x 128 through registers, kFew 16 x 16, kFewWide 32 x 16.  kMid of 8 waves against 4: 5,003 x 1,008 -> 777
+// 15.7 against 16.9, 65,536 x 1,024 -> 1,024 107 against 109; widened 207 against 171.
 enum Form { kBig, kMid, kSmall, kTile, kFew, kFewWide };
 struct Shape {
     int bm, bn, threads;
 };
 Shape shape(Form f, bool full)
 {
-    static constexpr Shape shapes[] = {{256, 256, 512}, {128, 128, 256}, {128, 64, 256}, {64, 128, 256}, {16, 16, 1024}, {32, 16, 1024}};
-    return f == kBig && full ? Shape{256, 128, 512} : shapes[f];
+    static constexpr Shape shapes[] = {{256, 256, 512}, {128, 128, 512}, {128, 64, 256}, {64, 128, 256}, {16, 16, 1024}, {32, 16, 1024}};
+    return !full ? shapes[f] : f == kBig ? Shape{256, 128, 512} : f == kMid ? Shape{128, 128, 256} : shapes[f];
 }
 
 // Row tiles of bn rows there can be at most.
@@ -812,8 +813,8 @@ bool rounds_itself(Form f, bool gated) { return f <= kSmall && shape(f, true).bm
 //     15.6 (kFewWide 15.5), 128 rows 15.5 (29); widened, 64 rows kFewWide 16.5 (25.7), 128 rows kSmall 25.7 (31.5);
 //   - at most 64 weight rows, or rows that are not 4-byte aligned: kTile, which takes them;
 //   - else the one of kBig, kMid and kSmall that takes the least time by its rounds, each of so much per 1,024 columns and so
-//     much for its start and epilogue, fitted to 65,536 x 1,024 -> 1,024 (86, 109 and 135; widened 183, 172 and 205) and
-//     8,192^3 (457, 562 and 714; 925, 917 and 1,124), and where 8-bit outputs need another kernel, that kernel's launch and the
+//     much for its start and epilogue, fitted to 65,536 x 1,024 -> 1,024 (86, 107 and 135; widened 183, 172 and 205) and
+//     8,192^3 (457, 555 and 714; 925, 917 and 1,124), and where 8-bit outputs need another kernel, that kernel's launch and the
 //     bytes of the FP32 rows.  It gives kSmall for 512 x 4,096 -> 4,096 (16.5; 23, 50), kMid for 1,024 rows (26; kSmall 27, kBig
 //     51) and kBig for 4,096 (64; 77, 96).
 //     The experts' last tiles count as half full, and from 64 (kMid) and 128 rows (kBig) per expert on.  32 experts, 2,048 ->
@@ -860,7 +861,10 @@ hipError_t launch(const Fp8ProductArgs &p, hipStream_t stream)
             hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 2, 4, 4, 2, 2, 2>), grid, block, 0, stream, p);
         break;
     case kMid:
-        hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 2, 2, 2, 2, 2, 2>), grid, block, 0, stream, p);
+        if constexpr (FULL)
+            hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 2, 2, 2, 2, 2, 2>), grid, block, 0, stream, p);
+        else
+            hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 2, 4, 2, 1, 2, 4>), grid, block, 0, stream, p);
         break;
     case kSmall:
         hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 2, 2, 2, 1, 3, 2>), grid, block, 0, stream, p);
