@@ -798,11 +798,11 @@ int64_t tiles_most(const ProductArgs &p, bool full, bool gated, bool grouped, Fo
 }
 
 // Rounds of tiles over the chip, `at_once` of them per round; where a CU runs two, a last round that is at most half
-// full takes 0.6 of one.
-float rounds(int64_t tiles, int at_once, bool two_per_cu)
+// full takes `half` of one.
+float rounds(int64_t tiles, int at_once, float half)
 {
     const float whole = (float)(tiles / at_once), rest = (float)(tiles % at_once) / at_once;
-    return whole + (rest == 0.0f ? 0.0f : two_per_cu && rest <= 0.5f ? 0.6f : 1.0f);
+    return whole + (rest == 0.0f ? 0.0f : rest <= 0.5f ? half : 1.0f);
 }
 
 bool rounds_itself(Form f, bool gated) { return f <= kSmall && shape(f, true).bm / (gated ? 2 : 1) % kFp8Block == 0; }
@@ -815,10 +815,10 @@ bool rounds_itself(Form f, bool gated) { return f <= kSmall && shape(f, true).bm
 //   - else the one of kBig, kMid and kSmall that takes the least time by its rounds, each of so much per 1,024 columns and so
 //     much for its start and epilogue, fitted to 65,536 x 1,024 -> 1,024 (86, 107 and 135; widened 183, 172 and 205) and
 //     8,192^3 (457, 555 and 714; 925, 917 and 1,124), and where 8-bit outputs need another kernel, that kernel's launch and the
-//     bytes of the FP32 rows.  It gives kSmall for 512 x 4,096 -> 4,096 (16.5; 23, 50), kMid for 1,024 rows (26; kSmall 27, kBig
-//     51) and kBig for 4,096 (64; 77, 96).
+//     bytes of the FP32 rows.  It gives kSmall for 512 x 4,096 -> 4,096 (16.4; 23, 48), kMid for 1,024 rows (25; kSmall 27, kBig
+//     49) and for 5,003 x 1,001 -> 777 (16.5; 19.3, 27.5) and kBig for 4,096 rows (63; 76, 97).
 //     The experts' last tiles count as half full, and from 64 (kMid) and 128 rows (kBig) per expert on.  32 experts, 2,048 ->
-//     2,048, by rows per expert: 32 kSmall 25 (kMid 29, kBig 41), 64 kMid 30 (39; 42), 128 kBig 46 (kMid 54, kSmall 52).
+//     2,048, by rows per expert: 32 kSmall 24 (kMid 27, kBig 38), 64 kMid 29 (39; 40), 128 kBig 42 (kMid 52, kSmall 49).
 Form choose_form(const Fp8ProductArgs &p, bool full, bool gated, bool grouped)
 {
     const bool even = p.ldx % 4 == 0 && p.ldw % 4 == 0 && p.w_stride % 4 == 0 && (((uintptr_t)p.x | (uintptr_t)p.w) & 3) == 0;
@@ -834,7 +834,7 @@ Form choose_form(const Fp8ProductArgs &p, bool full, bool gated, bool grouped)
         const int64_t bm = shape(f, full).bm, bn = shape(f, full).bn;
         const int64_t tiles = (grouped ? p.rows / bn + (used + 1) / 2 : (p.rows + bn - 1) / bn) * ((wide + bm - 1) / bm);
         const float more = p.eight && !rounds_itself(f, gated) ? 3.0f + (float)p.rows * p.out * 1.8e-6f : 0.0f;
-        return rounds(tiles, at_once, at_once == 512) * (per_k * k + start) + more;
+        return rounds(tiles, at_once, at_once == 256 ? 1.0f : full ? 0.6f : 0.63f) * (per_k * k + start) + more;
     };
     const float big = full ? time(kBig, 13.8f, 8.7f, 256) : time(kBig, 13.2f, 8.3f, 256);
     const float mid = full ? time(kMid, 14.2f, 7.1f, 512) : time(kMid, 8.1f, 5.5f, 512);
