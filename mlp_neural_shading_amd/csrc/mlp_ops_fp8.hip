@@ -807,6 +807,9 @@ float rounds(int64_t tiles, int at_once, float half)
 
 bool rounds_itself(Form f, bool gated) { return f <= kSmall && shape(f, true).bm / (gated ? 2 : 1) % kFp8Block == 0; }
 
+// Widened, kMid is at least as fast; only kBig has whole blocks of a gated layer's 8-bit outputs in a tile.
+bool big_fits(bool full, bool gated_eight) { return !full || gated_eight; }
+
 // The kernel, for 256 CUs (MI355X); times in us of every kernel forced on the size:
 //   - few tiles of 16 x 16 in all: kFew, whose waves share K, from 512 on 32 weight rows at a time.  1 x 4,096 -> 4,096 7.5
 //     (kSmall 15), 16 rows 7.5 (kFewWide 8.7), 33 rows kFewWide 13.7 (kFew 14.7, kSmall 15.5).  Behind the border: 64 rows kSmall
@@ -836,11 +839,11 @@ Form choose_form(const Fp8ProductArgs &p, bool full, bool gated, bool grouped)
         const float more = p.eight && !rounds_itself(f, gated) ? 3.0f + (float)p.rows * p.out * 1.8e-6f : 0.0f;
         return rounds(tiles, at_once, at_once == 256 ? 1.0f : full ? 0.6f : 0.63f) * (per_k * k + start) + more;
     };
-    const float big = full ? time(kBig, 13.8f, 8.7f, 256) : time(kBig, 13.2f, 8.3f, 256);
-    const float mid = full ? time(kMid, 14.2f, 7.1f, 512) : time(kMid, 8.1f, 5.5f, 512);
-    const float small = full ? time(kSmall, 8.8f, 3.8f, 512) : time(kSmall, 5.2f, 3.3f, 512);
+    const float big = full ? time(kBig, 13.3f, 9.6f, 256) : time(kBig, 13.2f, 8.3f, 256);
+    const float mid = full ? time(kMid, 13.3f, 8.2f, 512) : time(kMid, 8.1f, 5.5f, 512);
+    const float small = full ? time(kSmall, 8.2f, 4.6f, 512) : time(kSmall, 5.2f, 3.3f, 512);
     const int64_t each = used ? p.rows / used : INT64_MAX;  // rows per expert
-    if (each >= shape(kBig, full).bn / 2 && big <= mid && big <= small)
+    if (big_fits(full, gated && p.eight) && each >= shape(kBig, full).bn / 2 && big <= mid && big <= small)
         return kBig;
     return each >= 64 && mid <= small ? kMid : kSmall;
 }
@@ -855,9 +858,9 @@ hipError_t launch(const Fp8ProductArgs &p, hipStream_t stream)
     const dim3 grid((unsigned)tiles_most(p, FULL, GATED, GROUPED, form)), block(s.threads);
     switch (form) {
     case kBig:
-        if constexpr (FULL)
+        if constexpr (FULL && GATED)
             hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 4, 2, 2, 2, 2, 2>), grid, block, 0, stream, p);
-        else
+        else if constexpr (!FULL)
             hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 2, 4, 4, 2, 2, 2>), grid, block, 0, stream, p);
         break;
     case kMid:

@@ -46,12 +46,15 @@ def norm_kernel(rows, width, dtype=1):
         total=None, ldt=0, y=2 * FAR, ldy=width, values=None, ldv=0, scales=None, lds=0))
 
 
+# The kernel that writes 16 bits, by size; FP32 and 8-bit outputs take others of them.
 LINEAR = {"few": (70, 100, 60, False), "few wide": (300, 72, 700, False), "small": (601, 136, 699, False),
-          "mid": (1501, 200, 1303, False), "big": (5001, 200, 1801, False), "tile": (9001, 72, 63, False)}
-GATED = {"few wide": (100, 72, 40, True), "small": (600, 136, 351, True), "mid": (1301, 200, 1099, True),
+          "mid": (2601, 200, 2501, False), "big": (5001, 200, 1801, False), "tile": (9001, 72, 63, False)}
+GATED = {"few wide": (100, 72, 40, True), "small": (600, 136, 351, True), "mid": (2601, 200, 1251, True),
          "big": (2601, 264, 1700, True), "tile": (8200, 72, 32, True)}
 EXPERTS = {"few": (37, 3, 5, 200, 130, False), "small": (900, 2, 5, 136, 700, False), "mid": (3000, 2, 4, 72, 1201, False),
-           "big": (3000, 2, 4, 72, 1200, True), "tile": (700, 2, 6, 33, 300, False), "few wide": (200, 2, 6, 64, 200, True)}
+           "big": (4000, 2, 4, 72, 1200, False), "tile": (700, 2, 6, 33, 300, False), "few wide": (300, 2, 3, 72, 300, False)}
+EXPERTS_GATED = {"few wide": (200, 2, 6, 64, 200, True), "small": (900, 2, 5, 136, 351, True), "mid": (2600, 2, 4, 136, 611, True),
+                 "big": (3000, 2, 4, 72, 1200, True), "tile": (1500, 2, 6, 33, 150, True)}
 NORMS = [(1, 1, "16x1"), (1 << 20, 128, "16x1"), (1, 129, "256x1"), (1023, 2048, "256x1"), (1024, 129, "64x1"), (1024, 512, "64x1"),
          (1024, 513, "64x2"), (1024, 1024, "64x2"), (1024, 1025, "64x4"), (1024, 2048, "64x4"), (1, 2049, "256x2"), (9999, 4096, "256x2"),
          (2, 4097, "256x4"), (2, 8192, "256x4"), (2, 8193, "1024x4"), (2, 32768, "1024x4"), (2, 32769, "1024x4 twice")]

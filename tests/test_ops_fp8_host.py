@@ -201,12 +201,14 @@ def test_torch_refusals():
 # ---- which kernel ----------------------------------------------------------------------------------
 
 def test_kernels_by_size():
-    for name, size in K.LINEAR.items():
-        assert K.linear_kernel(*size) == name, size
-    for name, size in K.GATED.items():
-        assert K.linear_kernel(*size) == name, size
-    for name, size in K.EXPERTS.items():
-        assert K.expert_kernel(*size) == name, size
+    """The sizes take every kernel for 16 bits, for FP32 and for 8-bit outputs (`big` there for gated layers only)."""
+    for sizes, kernel in ((K.LINEAR, K.linear_kernel), (K.GATED, K.linear_kernel), (K.EXPERTS, K.expert_kernel),
+                          (K.EXPERTS_GATED, K.expert_kernel)):
+        for name, size in sizes.items():
+            assert kernel(*size) == name, size
+        gated = size[-1]
+        assert {kernel(*s, out_dtype=2) for s in sizes.values()} == set(sizes) - {"big"}
+        assert {kernel(*s, out_dtype=3) for s in sizes.values()} >= set(sizes) - ({"mid"} if gated else {"big"})
     assert K.linear_kernel(0, 8, 8) == "none" and K.expert_kernel(0, 2, 4, 8, 8) == "none"
 
 
