@@ -78,8 +78,9 @@ int mlp_quantize(const mlp_quantize_args *args, void *stream);
  *   y[r][o] = round(act(z[r][o]) + residual[r][o]),  or gated, round(act(z[r][o]) z[r][out_width + o] + residual[r][o]),
  * in FP32, rounded once.  16-bit outputs are sums of the matrix unit's 8-bit products: it adds 8 neighbouring columns'
  * products after cutting each to 2^-13 of the largest one's power of two, which leaves a result off by some 2^-16 of
- * itself.  FP32 and 8-bit outputs get sums whose products are not cut, at half that unit's rate.  The halves of a gated layer's w are matrices of their own: the blocks of the second begin at its row
- * out_width, and its scales' rows follow the ceil(out_width / 128) of the first. */
+ * itself.  FP32 and 8-bit outputs get sums whose products are not cut, at half that unit's rate.  The halves of a gated
+ * layer's w are matrices of their own: the blocks of the second begin at its row out_width, and its scales' rows follow
+ * the ceil(out_width / 128) of the first. */
 typedef struct mlp_fp8_linear_args {
     int64_t rows;      /* 0 .. INT32_MAX                                                                */
     int32_t in_width;  /* 1 .. MLP_OPS_MAX_WIDTH                                                         */
@@ -114,7 +115,8 @@ int mlp_fp8_linear(const mlp_fp8_linear_args *args, void *stream);
 /* mlp_expert_linear with operands in the format above, each expert's layer as in mlp_fp8_linear.  offsets, slots and
  * places are mlp_dispatch's, with the same clamping; x_scale has a row for each row of x, y_scale for each of y (rows
  * behind offsets[experts] are left as they were).  MLP_DTYPE_FP8 goes without combine.  Combined into 16 bits, a term may be
- * off by 0.51 * 2^-15 of the largest of its 32 neighbouring outputs of the slot; the sum is FP32 and is rounded once. */
+ * off by 0.51 * 2^-15 of the largest of its 32 neighbouring outputs of the slot (or of 2^-111, if that is more); the sum is
+ * FP32 and is rounded once. */
 typedef struct mlp_fp8_expert_linear_args {
     int64_t tokens; /* tokens * k: 0 .. INT32_MAX */
     int32_t k;

@@ -310,7 +310,6 @@ struct __attribute__((packed, aligned(2))) Float8 {
 // bytes.  Larger numbers stand for infinities and NaN.
 __device__ __forceinline__ u4 to_terms(f8 v, float &scale)
 {
-    typedef short s2 __attribute__((ext_vector_type(2)));
     float m = 0.0f, odd = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -333,9 +332,8 @@ __device__ __forceinline__ u4 to_terms(f8 v, float &scale)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (!(fabsf(v[j]) < __builtin_inff())) {
-                s2 t = __builtin_bit_cast(s2, q[j / 2]);
-                t[j % 2] = v[j] > 0.0f ? 32767 : v[j] < 0.0f ? -32767 : -32768;
-                q[j / 2] = __builtin_bit_cast(unsigned, t);
+                const unsigned code = v[j] > 0.0f ? 0x7fffu : v[j] < 0.0f ? 0x8001u : 0x8000u, both = q[j / 2];
+                q[j / 2] = j % 2 ? (both & 0xffffu) | code << 16 : (both & 0xffff0000u) | code;
             }
     return q;
 }

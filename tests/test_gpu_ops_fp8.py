@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import ops_fp8_kernels as K
 import ops_fp8_reference as F
 import ops_reference as R
 from gpu_util import device, log
@@ -355,6 +356,59 @@ def test_scales_are_taken_as_they_are():
     assert bool(got[7].isnan().all()) and int(got.isnan().sum()) == n
 
 
+@pytest.mark.parametrize("rows,k,n,gated", [*K.LINEAR.values(), *K.GATED.values()])
+def test_linear_by_kernel(rows, k, n, gated):
+    """A size of every kernel's, into each type that it writes."""
+    g = gen(rows + n)
+    wide = 2 * n if gated else n
+    x, w = operands(g, rows, k, n, gated, aligned=False)
+    X, W, b = on_gpu(x), on_gpu(w), rnd(g, wide)
+    for full in (False, True):
+        want = F.linear64(x, w, b, None, "silu", gated, full)
+        for t in (torch.float32, FP8) if full else (torch.float16, torch.bfloat16):
+            log("linear", rows, k, n, gated, t, K.linear_kernel(rows, k, n, gated, E._OUT[t]))
+            y = E.linear(X, W, gpu(b), act="silu", gated=gated, out_dtype=t)
+            F.check_quantized(y, *want) if t == FP8 else R.check(y, *want, t)
+
+
+ODD = ((3, math.inf), (40, math.nan), (41, -math.inf))  # outputs and their bias
+
+
+def without_odd(t, fill=0):
+    t = t.clone()
+    for o, _ in ODD:
+        t[:, o] = fill
+    return t
+
+
+def check_odd(y, sign=True):
+    for o, v in ODD:
+        assert bool(y[:, o].float().isnan().all() if math.isnan(v) or not sign else (y[:, o] == v).all()), o
+
+
+@pytest.mark.parametrize("rows,k,n,gated", [s for s in K.LINEAR.values()] + [K.GATED["big"], K.GATED["small"]])
+def test_infinities_and_nans_stay_by_themselves(rows, k, n, gated):
+    """Outputs that are not finite, from the bias, in blocks with others: NaN in 8 bits, and the others as without them."""
+    g = gen(rows + 5)
+    x, w = operands(g, rows, k, n, gated, aligned=False)
+    X, W = on_gpu(x), on_gpu(w)
+    b = without_odd(rnd(g, 1, 2 * n if gated else n))[0]
+    want, e = F.linear64(x, w, b, None, "none", gated)
+    full, ef = F.linear64(x, w, b, None, "none", gated, True)
+    for o, v in ODD:
+        b[o] = v
+        if gated:
+            b[n + o] = 1e9  # positive, so that the product's sign is the gate's
+    log("odd", rows, k, n, gated)
+    for t in (torch.bfloat16, torch.float32):
+        y = E.linear(X, W, gpu(b), gated=gated, out_dtype=t)
+        check_odd(y)
+        R.check(without_odd(y), without_odd(full if t == torch.float32 else want), without_odd(ef if t == torch.float32 else e), t)
+    q = E.linear(X, W, gpu(b), gated=gated, out_dtype=FP8)
+    check_odd(q.values, False)
+    F.check_quantized((without_odd(bits(q.values)).view(FP8), q.scales), without_odd(full), without_odd(ef))
+
+
 # ---- the experts' layers ---------------------------------------------------------------------------
 
 EXPERTS = [(1, 1, 1, 8, 8), (1, 2, 3, 40, 24), (3, 4, 9, 33, 17), (8, 4, 32, 128, 96), (64, 2, 4, 64, 64), (37, 3, 5, 200, 130),
@@ -402,6 +456,53 @@ def test_expert_linear(tokens, k, experts, k_in, n):
     y = E.expert_linear(X, W, P, k=k, rows="slots", gated=True, combine=True, out_dtype=torch.float32)
     want, bound, _ = F.experts64(x, w, plan, k, gated=True, rows="slots", combine=True, full=True)
     R.check(y, want, bound, torch.float32, "combined fp32, no weights")
+
+
+@pytest.mark.parametrize("tokens,k,experts,k_in,n,gated", [*K.EXPERTS.values(), *K.EXPERTS_GATED.values()])
+def test_expert_linear_by_kernel(tokens, k, experts, k_in, n, gated):
+    """A size of every kernel's, by slot into each type that it writes, and combined; and outputs that are not finite."""
+    g = gen(tokens + n)
+    index = torch.randint(0, experts, (tokens, k), generator=g, dtype=torch.int32)
+    plan = R.dispatch64(index, experts)
+    P = ops.Dispatch(*map(gpu, plan))
+    wide = 2 * n if gated else n
+    x, w, b = F.quantize(rnd(g, tokens, k_in)), F.quantize_weights(rnd(g, experts, wide, k_in, scale=k_in ** -0.5), gated), rnd(g, experts, wide)
+    X, W = put(x), put(w)
+    weight, r = 0.1 + torch.rand(tokens, k, generator=g), rnd(g, tokens, n, dtype=torch.float16)
+    for full in (False, True):
+        want, e, _ = F.experts64(x, w, plan, k, b, "silu", gated, full=full)
+        for t in (torch.float32, FP8) if full else (torch.float16, torch.bfloat16):
+            log("experts", tokens, k, experts, k_in, n, gated, t, K.expert_kernel(tokens, k, experts, k_in, n, gated, E._OUT[t]))
+            y = E.expert_linear(X, W, P, gpu(b), k=k, act="silu", gated=gated, out_dtype=t)
+            F.check_quantized(y, want, e) if t == FP8 else R.check(y, want, e, t)
+    for t in (torch.float16, torch.bfloat16, torch.float32):
+        y = E.expert_linear(X, W, P, gpu(b), k=k, gated=gated, combine=True, weight=gpu(weight), residual=gpu(r.to(t)), out_dtype=t)
+        want, e, _ = F.experts64(x, w, plan, k, b, "none", gated, combine=True, weight=weight, residual=r.to(t), full=t == torch.float32)
+        R.check(y, want, e, t, "combined")
+    b = torch.stack([without_odd(v[None])[0] for v in b])
+    want, e, _ = F.experts64(x, w, plan, k, b, "none", gated, combine=True, weight=weight)
+    for o, v in ODD:
+        b[:, o] = v
+        if gated:
+            b[:, n + o] = 1e9
+    y = E.expert_linear(X, W, P, gpu(b), k=k, gated=gated, combine=True, weight=gpu(weight))
+    check_odd(y)
+    R.check(without_odd(y), without_odd(want), without_odd(e), torch.bfloat16, "odd")
+    q = E.expert_linear(X, W, P, gpu(b), k=k, gated=gated, out_dtype=FP8)
+    check_odd(q.values, False)
+    want, e, _ = F.experts64(x, w, plan, k, torch.stack([without_odd(v[None])[0] for v in b]), "none", gated, full=True)
+    F.check_quantized((without_odd(bits(q.values)).view(FP8), q.scales), without_odd(want), without_odd(e), "odd fp8")
+
+
+def test_expert_linear_same_expert_twice():
+    """A token routed twice to one expert has two slots there, and both count."""
+    g = gen(5)
+    tokens, k, experts = 300, 4, 3
+    x, w = F.quantize(rnd(g, tokens, 200)), expert_weights(g, experts, 136, 200, False)
+    index = torch.randint(0, experts, (tokens, 1), generator=g, dtype=torch.int32).repeat(1, k)
+    plan, weight = R.dispatch64(index, experts), torch.rand(tokens, k, generator=g)
+    y = E.expert_linear(put(x), on_gpu(w), ops.dispatch(gpu(index), experts), k=k, combine=True, weight=gpu(weight))
+    R.check(y, *F.experts64(x, w, plan, k, combine=True, weight=weight)[:2], torch.bfloat16)
 
 
 def test_expert_linear_all_rows_to_one_expert_or_none():
@@ -647,3 +748,44 @@ def test_rows_and_experts_far_apart():
     wide.copy_(gpu(values))
     same(E.quantize(wide), F.quantize(values))
     assert torch.equal(E.rms_norm(wide).y, E.rms_norm(gpu(values)).y)
+
+
+def test_more_than_32_bits_of_elements():
+    """Outputs, 8-bit rows, terms and normed rows of more than 2^31 elements; the last rows against 64 bits."""
+    g = gen(80)
+    rows, k, n = (1 << 20) + 300, 16, 2056
+    x, w = F.quantize(rnd(g, 1000, k)), F.quantize_weights(rnd(g, n, k, scale=k ** -0.5))
+    many = [gpu(t).repeat(-(-rows // 1000), 1)[:rows] for t in (x[0].view(torch.uint8), x[1])]
+    X, W = E.Quantized(many[0].view(FP8), many[1]), put(w)
+    last = slice(rows - 700, rows)
+    tail = (X.values[last].cpu(), X.scales[last].cpu())
+    for t in (torch.bfloat16, FP8):
+        log("many rows", t)
+        y = E.linear(X, W, out_dtype=t)
+        if t == FP8:
+            F.check_quantized((bits(y.values[last]).view(FP8), y.scales[last]), *F.linear64(tail, w, full=True))
+        else:
+            R.check(y[last], *F.linear64(tail, w), t)
+        if t != FP8:
+            log("norm, 8 bits")
+            normed = E.rms_norm(y, residual=y, out="both")
+            h, e, total = F.norm64(y[last], residual=y[last])
+            R.check(normed.y[last], h, e, t)
+            assert torch.equal(normed.total[last].cpu(), total)
+            same(E.Quantized(normed.quantized.values[last], normed.quantized.scales[last]),
+                 tuple(q.cpu() for q in E.rms_norm(y[last], residual=y[last], out="fp8").quantized))
+            del normed
+            q = E.quantize(y)
+            same(E.Quantized(q.values[last], q.scales[last]), F.quantize(y[last].cpu()))
+            del q
+        del y
+    tokens, kk, experts = rows // 4, 4, 3
+    we = F.quantize_weights(rnd(g, experts, n, k, scale=k ** -0.5))
+    index = torch.randint(0, experts, (tokens, kk), generator=g, dtype=torch.int32)
+    weight = torch.rand(tokens, kk, generator=g)
+    log("many slots")
+    y = E.expert_linear(E.Quantized(X.values[:tokens], X.scales[:tokens]), put(we), ops.dispatch(gpu(index), experts), k=kk,
+                        combine=True, weight=gpu(weight))
+    at = slice(tokens - 500, tokens)
+    want, e, _ = F.experts64((X.values[at].cpu(), X.scales[at].cpu()), we, R.dispatch64(index[at], experts), kk, combine=True, weight=weight[at])
+    R.check(y[at], want, e, torch.bfloat16)
