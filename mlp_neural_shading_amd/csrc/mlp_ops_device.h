@@ -310,12 +310,18 @@ struct __attribute__((packed, aligned(2))) Float8 {
 // bytes.  Larger numbers stand for infinities and NaN.
 __device__ __forceinline__ u4 to_terms(f8 v, float &scale)
 {
-    float m = 0.0f, odd = 0.0f;
+    float m = 0.0f, sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float a = fabsf(v[j]);
-        m = fmaxf(m, a < __builtin_inff() ? a : 0.0f);
-        odd = fmaf(v[j], 0.0f, odd);  // 0, or NaN
+        m = fmaxf(m, fabsf(v[j]));
+        sum += v[j];
+    }
+    const bool odd = !(fabsf(sum) < __builtin_inff());  // wherever one of them is not finite, hardly ever else
+    if (odd) {
+        m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            m = fmaxf(m, fabsf(v[j]) < __builtin_inff() ? fabsf(v[j]) : 0.0f);
     }
     auto other = [](float w, auto perm) {
         return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, w), decltype(perm)::value, 0xf, 0xf, true));
@@ -328,7 +334,7 @@ __device__ __forceinline__ u4 to_terms(f8 v, float &scale)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         q[j] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_pknorm_i16(v[2 * j] * inv, v[2 * j + 1] * inv));  // times 32,767, nearest
-    if (odd != 0.0f)
+    if (odd)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (!(fabsf(v[j]) < __builtin_inff())) {
