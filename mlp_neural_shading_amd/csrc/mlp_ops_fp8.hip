@@ -163,13 +163,11 @@ __device__ __forceinline__ void finish8(const Fp8ProductArgs &p, float (&acc)[2 
     // Outputs past the last repeat it, in its block.
 #pragma unroll
     for (int k = 0; k < 2 * NT; ++k) {
-        float m = 0.0f;
+        float v[8 * MO];
 #pragma unroll
-        for (int mo = 0; mo < MO; ++mo)
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (j / 4 % 2 == k % 2)
-                    m = fmaxf(m, finite_abs(z[mo][k / 2][j]));
+        for (int i = 0; i < 8 * MO; ++i)
+            v[i] = z[i / 8][k / 2][i / 4 % 2 * 8 + k % 2 * 4 + i % 4];
+        float m = largest<8 * MO>(v);
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
         if (g == 0)
@@ -183,7 +181,7 @@ __device__ __forceinline__ void finish8(const Fp8ProductArgs &p, float (&acc)[2 
 #pragma unroll
         for (int i = 1; i < PER; ++i)
             m = fmaxf(m, part[(wm / PER * PER + i) * BN + r]);
-        const float scale = scale_of(m), inv = 1.0f / scale;
+        const float scale = scale_of(m), inv = inverse(scale);
         const int o = o0 + wm / PER * kFp8Block;
         if (wm % PER == 0 && g == 0 && row0 + r < row1 && o < p.out)
             p.ys[(row0 + r) * p.ldys + o / kFp8Block] = scale;

@@ -79,7 +79,7 @@ __device__ __forceinline__ void store_eight(uint8_t *row, float *scales, int col
     struct __attribute__((packed, aligned(1))) Bytes8 {
         unsigned v[2];
     };
-    const float s = scale_of(block), inv = 1.0f / s;
+    const float s = scale_of(block), inv = inverse(s);
     if (col >= width)
         return;
     const Bytes8 o = {{to_e4m3x4(v[0], v[1], v[2], v[3], inv), to_e4m3x4(v[4], v[5], v[6], v[7], inv)}};
@@ -93,15 +93,6 @@ __device__ __forceinline__ void store_eight(uint8_t *row, float *scales, int col
             if (col + j < width)
                 row[col + j] = (uint8_t)(o.v[j / 4] >> (8 * (j % 4)));
     }
-}
-
-__device__ __forceinline__ float largest(f8 v)
-{
-    float m = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        m = fmaxf(m, finite_abs(v[j]));
-    return m;
 }
 
 // Sum over LANES neighbouring lanes (16, 32 or 64), or over a workgroup of LANES threads.
@@ -196,7 +187,7 @@ __global__ __launch_bounds__(LANES <= 256 ? 256 : LANES) void rms_norm(NormArgs 
                         store_chunk((T *)p.y + row * p.ldy, col, p.width, y);
                 }
                 if (p.values)
-                    store_eight(p.values + row * p.ldv, p.scales + row * p.lds, col, p.width, y, max16(largest(y)), first);
+                    store_eight(p.values + row * p.ldv, p.scales + row * p.lds, col, p.width, y, max16(largest<8>(y)), first);
             }
         }
     }
@@ -230,7 +221,7 @@ __global__ __launch_bounds__(256) void quantize_rows(QuantizeArgs p)
             if (first + u * step >= all)  // the same for the 16 lanes
                 break;
             const f8 v = col[u] < p.width ? unpack(c[u]) : (f8)0.0f;
-            store_eight(values + (int64_t)row[u] * p.ldv, scales + (int64_t)row[u] * p.lds, col[u], p.width, v, max16(largest(v)), lane == 0);
+            store_eight(values + (int64_t)row[u] * p.ldv, scales + (int64_t)row[u] * p.lds, col[u], p.width, v, max16(largest<8>(v)), lane == 0);
         }
     }
 }
@@ -260,7 +251,7 @@ __global__ __launch_bounds__(256) void quantize_blocks(QuantizeArgs p)
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (row0 + 16 * u + r < p.rows && col < p.width)
-                m = fmaxf(m, largest(unpack(c[u])));
+                m = fmaxf(m, largest<8>(unpack(c[u])));
         m = max16(m);
         if (lane == 0)
             part[turn][r] = m;
