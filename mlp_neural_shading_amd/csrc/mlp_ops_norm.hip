@@ -267,29 +267,29 @@ __global__ __launch_bounds__(256) void quantize_blocks(QuantizeArgs p)
 
 // ---- which kernel ---------------------------------------------------------------------------------
 
-// Lanes and chunks for a row, by its width and how many rows there are.
+// Lanes and chunks for a row: one chunk a lane where that fills the lanes, and registers few enough that a CU holds several
+// workgroups, of which some wait for memory while others compute.  us, BF16 into 8 bits (and with a residual into both):
+//   65,536 x 1,024   64x2 49 (112)      256x1 82 (117): below 1,024 rows, where only latency counts, 256x1
+//   32,768 x 2,048   256x1 52 (107)     64x4 55 (120), 256x2 67 (109)
+//   32,768 x 4,096   256x2 99 (221)     512x1 107 (217), 256x4 180 (249)
+//   8,192 x 8,192    512x2 57 (110)     256x4 76 (125), 1024x1 76 (110)
+//   4,096 x 16,384   512x2 twice 59 (127)   1024x2 78 (124), 512x4 97 (144): the second reading comes from the caches
+//   4,096 x 32,768   512x2 twice 118 (260)  1024x2 twice 144 (254), 1024x4 211 (288, registers spilled)
+//   1,024 x 65,536   1024x4 twice 66 (145)  512x4 twice 68 (173)
 struct NormForm {
     int lanes, chunks;
     bool loop;
 };
-constexpr NormForm kNormForms[] = {{16, 1, false}, {64, 1, false}, {64, 2, false}, {64, 4, false},
-                                   {256, 1, false}, {256, 2, false}, {256, 4, false}, {1024, 4, false}, {1024, 4, true}};
+constexpr NormForm kNormForms[] = {{16, 1, false}, {64, 1, false}, {64, 2, false}, {256, 1, false},
+                                   {256, 2, false}, {512, 2, false}, {512, 2, true}, {1024, 4, true}};
 
 int choose_norm(const NormArgs &p)
 {
     if (p.width <= 128)
         return 0;
-    if (p.rows >= 1024) {
-        if (p.width <= 512)
-            return 1;
-        if (p.width <= 1024)
-            return 2;
-        if (p.width <= 2048)
-            return 3;
-    }
-    if (p.width <= 2048)
-        return 4;
-    return p.width <= 4096 ? 5 : p.width <= 8192 ? 6 : p.width <= 32768 ? 7 : 8;
+    if (p.rows >= 1024 && p.width <= 1024)
+        return p.width <= 512 ? 1 : 2;
+    return p.width <= 2048 ? 3 : p.width <= 4096 ? 4 : p.width <= 8192 ? 5 : p.width <= 32768 ? 6 : 7;
 }
 
 template <class T>
@@ -304,11 +304,10 @@ hipError_t launch_norm_typed(const NormArgs &p, hipStream_t stream)
     case 0: hipLaunchKernelGGL((rms_norm<T, 16, 1, false>), grid, block, 0, stream, p); break;
     case 1: hipLaunchKernelGGL((rms_norm<T, 64, 1, false>), grid, block, 0, stream, p); break;
     case 2: hipLaunchKernelGGL((rms_norm<T, 64, 2, false>), grid, block, 0, stream, p); break;
-    case 3: hipLaunchKernelGGL((rms_norm<T, 64, 4, false>), grid, block, 0, stream, p); break;
-    case 4: hipLaunchKernelGGL((rms_norm<T, 256, 1, false>), grid, block, 0, stream, p); break;
-    case 5: hipLaunchKernelGGL((rms_norm<T, 256, 2, false>), grid, block, 0, stream, p); break;
-    case 6: hipLaunchKernelGGL((rms_norm<T, 256, 4, false>), grid, block, 0, stream, p); break;
-    case 7: hipLaunchKernelGGL((rms_norm<T, 1024, 4, false>), grid, block, 0, stream, p); break;
+    case 3: hipLaunchKernelGGL((rms_norm<T, 256, 1, false>), grid, block, 0, stream, p); break;
+    case 4: hipLaunchKernelGGL((rms_norm<T, 256, 2, false>), grid, block, 0, stream, p); break;
+    case 5: hipLaunchKernelGGL((rms_norm<T, 512, 2, false>), grid, block, 0, stream, p); break;
+    case 6: hipLaunchKernelGGL((rms_norm<T, 512, 2, true>), grid, block, 0, stream, p); break;
     default: hipLaunchKernelGGL((rms_norm<T, 1024, 4, true>), grid, block, 0, stream, p); break;
     }
     return hipGetLastError();
@@ -336,7 +335,7 @@ hipError_t launch_quantize_typed(const QuantizeArgs &q, int block_rows, hipStrea
 
 const char *norm_kernel(const NormArgs &p, int)
 {
-    static const char *const names[] = {"16x1", "64x1", "64x2", "64x4", "256x1", "256x2", "256x4", "1024x4", "1024x4 twice"};
+    static const char *const names[] = {"16x1", "64x1", "64x2", "256x1", "256x2", "512x2", "512x2 twice", "1024x4 twice"};
     return names[choose_norm(p)];
 }
 

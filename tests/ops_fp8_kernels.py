@@ -56,5 +56,5 @@ EXPERTS = {"few": (37, 3, 5, 200, 130, False), "small": (900, 2, 5, 136, 700, Fa
 EXPERTS_GATED = {"few wide": (200, 2, 6, 64, 200, True), "small": (900, 2, 5, 136, 351, True), "mid": (2600, 2, 4, 136, 611, True),
                  "big": (3000, 2, 4, 72, 1200, True), "tile": (1500, 2, 6, 33, 150, True)}
 NORMS = [(1, 1, "16x1"), (1 << 20, 128, "16x1"), (1, 129, "256x1"), (1023, 2048, "256x1"), (1024, 129, "64x1"), (1024, 512, "64x1"),
-         (1024, 513, "64x2"), (1024, 1024, "64x2"), (1024, 1025, "64x4"), (1024, 2048, "64x4"), (1, 2049, "256x2"), (9999, 4096, "256x2"),
-         (2, 4097, "256x4"), (2, 8192, "256x4"), (2, 8193, "1024x4"), (2, 32768, "1024x4"), (2, 32769, "1024x4 twice")]
+         (1024, 513, "64x2"), (1024, 1024, "64x2"), (1024, 1025, "256x1"), (1, 2049, "256x2"), (9999, 4096, "256x2"),
+         (2, 4097, "512x2"), (2, 8192, "512x2"), (2, 8193, "512x2 twice"), (2, 32768, "512x2 twice"), (2, 32769, "1024x4 twice")]

@@ -160,7 +160,7 @@ def test_rms_norm(rows, width, dtype):
     R.check(E.rms_norm(gpu(x), eps=0.5).y, y, e, t, "no weight")
 
 
-@pytest.mark.parametrize("rows,width", [(3, 100), (5, 1001), (3, 3000), (2, 40000), (1100, 600)])
+@pytest.mark.parametrize("rows,width", [(3, 100), (5, 1001), (3, 3000), (4, 6000), (3, 9000), (2, 40000), (1100, 600)])
 def test_rms_norm_in_place_and_beside(rows, width):
     """The total as x and as the residual; column blocks of wider matrices, aligned or not, NaN around the inputs."""
     g, t = gen(rows), torch.bfloat16
