@@ -789,3 +789,37 @@ def test_more_than_32_bits_of_elements():
     at = slice(tokens - 500, tokens)
     want, e, _ = F.experts64((X.values[at].cpu(), X.scales[at].cpu()), we, R.dispatch64(index[at], experts), kk, combine=True, weight=weight[at])
     R.check(y[at], want, e, torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows,k,n", [(3, 1 << 20, 3), (2, 9, 1 << 20), (70, 17, (1 << 20) - 3), (700, 8200, 701), (700, 8201, 700)])
+def test_widest(rows, k, n):
+    """The largest widths, and long rows through the kernels that stage them."""
+    g = gen(rows + k)
+    x, w = operands(g, rows, k, n)
+    X, W, b = on_gpu(x), on_gpu(w), rnd(g, n)
+    for full in (False, True):
+        want = F.linear64(x, w, b, full=full)
+        for t in (torch.float32, FP8) if full else (torch.bfloat16,):
+            log("widest", rows, k, n, t, K.linear_kernel(rows, k, n, out_dtype=E._OUT[t]))
+            y = E.linear(X, W, gpu(b), out_dtype=t)
+            F.check_quantized(y, *want) if t == FP8 else R.check(y, *want, t)
+
+
+def test_widest_rows():
+    g, t, width = gen(90), torch.bfloat16, 1 << 20
+    x, r, w = rnd(g, 3, width, dtype=t), rnd(g, 3, width, dtype=t), rnd(g, width, dtype=t)
+    y, e, total = F.norm64(x, w, r)
+    got = E.rms_norm(gpu(x), gpu(w), residual=gpu(r), out="both")
+    R.check(got.y, y, e, t)
+    assert torch.equal(got.total.cpu(), total)
+    same(got.quantized, tuple(q.cpu() for q in E.rms_norm(gpu(x), gpu(w), residual=gpu(r), out="fp8").quantized))
+    for block_rows in (1, 128):
+        got = E.quantize(gpu(x), block_rows=block_rows)
+        one = E.quantize(gpu(x[:, 5 * 128:6 * 128].contiguous()), block_rows=block_rows)
+        assert torch.equal(bits(got.values[:, 640:768]), bits(one.values)) and torch.equal(got.scales[:, 5:6], one.scales)
+        last = E.quantize(gpu(x[:, -256:].contiguous()), block_rows=block_rows)
+        assert torch.equal(bits(got.values[:, -256:]), bits(last.values)) and torch.equal(got.scales[:, -2:], last.scales)
+    index = torch.tensor([[0, 1], [1, 1]], dtype=torch.int32)
+    plan, x, w = R.dispatch64(index, 2), F.quantize(rnd(g, 2, 40)), F.quantize_weights(rnd(g, 2, width, 40))
+    y = E.expert_linear(put(x), put(w), ops.Dispatch(*map(gpu, plan)), k=2, combine=True)
+    R.check(y, *F.experts64(x, w, plan, 2, combine=True)[:2], t)
