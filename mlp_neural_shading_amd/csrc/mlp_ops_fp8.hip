@@ -776,15 +776,16 @@ __global__ __launch_bounds__(256) void sum_terms(TermsArgs c)
 // ---- which kernel ---------------------------------------------------------------------------------
 
 // kBig 256 weight rows x 256 rows (FULL: 256 x 128), kMid 128 x 128 (of 8 waves; FULL: of 4), kSmall 128 x 64 (all three
-// straight into LDS), kTile 64 x 128 through registers, kFew 16 x 16, kFewWide 32 x 16.  kMid of 8 waves against 4:
+// straight into LDS), kTile 64 x 128 through registers, kFew 16 x 16, kFewWide 32 x 16, kThin 64 x 64 straight into LDS (gated,
+// by two waves that hold 32 gates and the 32 they gate: 13.5 against kSmall's 15.6 for 64 x 4,096 -> 2 x 2,048, not built).  kMid of 8 waves against 4:
 // 5,003 x 1,008 -> 777 15.7 against 16.9, 65,536 x 1,024 -> 1,024 107 against 109; widened 207 against 171.
-enum Form { kBig, kMid, kSmall, kTile, kFew, kFewWide };
+enum Form { kBig, kMid, kSmall, kTile, kFew, kFewWide, kThin };
 struct Shape {
     int bm, bn, threads;
 };
 Shape shape(Form f, bool full)
 {
-    static constexpr Shape shapes[] = {{256, 256, 512}, {128, 128, 512}, {128, 64, 256}, {64, 128, 256}, {16, 16, 1024}, {32, 16, 1024}};
+    static constexpr Shape shapes[] = {{256, 256, 512}, {128, 128, 512}, {128, 64, 256}, {64, 128, 256}, {16, 16, 1024}, {32, 16, 1024}, {64, 64, 256}};
     return !full ? shapes[f] : f == kBig ? Shape{256, 128, 512} : f == kMid ? Shape{128, 128, 256} : shapes[f];
 }
 
@@ -816,15 +817,18 @@ bool rounds_itself(Form f, bool gated) { return f <= kSmall && shape(f, true).bm
 bool big_fits(bool full, bool gated_eight) { return !full || gated_eight; }
 
 // The kernel, for 256 CUs (MI355X); times in us of every kernel forced on the size:
-//   - few tiles of 16 x 16 in all: kFew, whose waves share K, from 512 on 32 weight rows at a time.  1 x 4,096 -> 4,096 7.5
-//     (kSmall 15), 16 rows 7.5 (kFewWide 8.7), 33 rows kFewWide 13.7 (kFew 14.7, kSmall 15.5).  Behind the border: 64 rows kSmall
-//     15.6 (kFewWide 15.5), 128 rows 15.5 (29); widened, 64 rows kFewWide 16.5 (25.7), 128 rows kSmall 25.7 (31.5);
+//   - few tiles of 16 x 16 in all: kFew, whose waves share K, and with more of them than CUs 32 weight rows at a time.
+//     16 x 4,096 -> 4,096 kFew 8.4 (kFewWide 8.8, kThin 11.3), 32 rows kFewWide 8.9 (11.5), 96 x 4,096 -> 1,024 kFewWide 8.7
+//     (kFew 11.1, kThin 10.9).  Behind the border: 64 x 4,096 -> 4,096 kThin 11.7 (kFewWide 15.6); widened 17 (16.5).  Gated and
+//     experts' layers, which have no kThin: 64 x 4,096 -> 2 x 2,048 kSmall 15.6 (15.6), 128 rows 15.6 (29);
 //   - at most 64 weight rows, or rows that are not 4-byte aligned: kTile, which takes them;
-//   - else the one of kBig, kMid and kSmall that takes the least time by its rounds, each of so much per 1,024 columns and so
+//   - else the one of kBig, kMid, kSmall and kThin that takes the least time by its rounds, each of so much per 1,024 columns and so
 //     much for its start and epilogue, fitted to 65,536 x 1,024 -> 1,024 (86, 107 and 135; widened 183, 172 and 205) and
-//     8,192^3 (457, 555 and 714; 925, 917 and 1,124), and where 8-bit outputs need another kernel, that kernel's launch and the
-//     bytes of the FP32 rows.  It gives kSmall for 512 x 4,096 -> 4,096 (16.4; 23, 48), kMid for 1,024 rows (25; kSmall 27, kBig
-//     49) and for 5,003 x 1,001 -> 777 (16.5; 19.3, 27.5) and kBig for 4,096 rows (63; 76, 97).
+//     8,192^3 (457, 555 and 714; 925, 917 and 1,124), kThin to 256 and 512 tiles, and where 8-bit outputs need another kernel,
+//     that kernel's launch and the bytes of the FP32 rows.  It gives kThin for 64 to 256 x 4,096 -> 4,096 (11.7; kSmall 15.6;
+//     widened 17.5, 25.4) and 512 x 7,168 -> 2,048 (18; 24), kSmall for 512 x 4,096 -> 4,096 (16.4; kThin 18, kMid 23, kBig 48),
+//     kMid for 1,024 rows (25; kSmall 27, kBig 49) and for 5,003 x 1,001 -> 777 (16.5; 19.3, 27.5) and kBig for 4,096 rows (63;
+//     76, 97).
 //     The experts' last tiles count as half full, and from 64 (kMid) and 128 rows (kBig) per expert on.  32 experts, 2,048 ->
 //     2,048, by rows per expert: 32 kSmall 24 (kMid 27, kBig 38), 64 kMid 29 (39; 40), 128 kBig 42 (kMid 52, kSmall 49).
 Form choose_form(const Fp8ProductArgs &p, bool full, bool gated, bool grouped)
@@ -832,8 +836,9 @@ Form choose_form(const Fp8ProductArgs &p, bool full, bool gated, bool grouped)
     const bool even = p.ldx % 4 == 0 && p.ldw % 4 == 0 && p.w_stride % 4 == 0 && (((uintptr_t)p.x | (uintptr_t)p.w) & 3) == 0;
     const int64_t wide = (int64_t)p.out * (gated ? 2 : 1);
     const int64_t few = row_tiles(p, grouped, 16) * ((wide + 15) / 16);
-    if (few < (full ? 1536 : 1024))
-        return gated || few >= 512 ? kFewWide : kFew;
+    const bool plain = !gated && !grouped;
+    if (few <= (plain ? (full ? 1024 : 512) : full ? 1535 : 1023))
+        return gated || few > (plain ? 256 : 511) ? kFewWide : kFew;
     if (!even || wide <= 64)
         return kTile;
     const int64_t used = !grouped ? 0 : p.rows < p.experts ? p.rows : p.experts;
@@ -847,6 +852,11 @@ Form choose_form(const Fp8ProductArgs &p, bool full, bool gated, bool grouped)
     const float big = full ? time(kBig, 13.3f, 9.6f, 256) : time(kBig, 13.2f, 8.3f, 256);
     const float mid = full ? time(kMid, 13.3f, 8.2f, 512) : time(kMid, 8.1f, 5.5f, 512);
     const float small = full ? time(kSmall, 8.2f, 4.6f, 512) : time(kSmall, 5.2f, 3.3f, 512);
+    if (plain) {
+        const float thin = full ? time(kThin, 5.3f, 4.6f, 512) : time(kThin, 3.2f, 4.0f, 512);
+        if (thin < small && thin < mid && thin < big)
+            return kThin;
+    }
     const int64_t each = used ? p.rows / used : INT64_MAX;  // rows per expert
     if (big_fits(full, gated && p.eight) && each >= shape(kBig, full).bn / 2 && big <= mid && big <= small)
         return kBig;
@@ -876,6 +886,10 @@ hipError_t launch(const Fp8ProductArgs &p, hipStream_t stream)
         break;
     case kSmall:
         hipLaunchKernelGGL((fp8_big<T, GROUPED, GATED, 2, 2, 2, 1, 3, 2>), grid, block, 0, stream, p);
+        break;
+    case kThin:
+        if constexpr (!GROUPED && !GATED)
+            hipLaunchKernelGGL((fp8_big<T, false, false, 2, 2, 1, 1, 3, 2>), grid, block, 0, stream, p);
         break;
     case kTile:
         hipLaunchKernelGGL((fp8_tile<T, GROUPED, GATED, 1, 4, 2, 1, 2>), grid, block, 0, stream, p);
@@ -941,7 +955,7 @@ hipError_t launch_terms(const TermsArgs &c, int out_dtype, hipStream_t stream)
 
 const char *fp8_product_kernel(const Fp8ProductArgs &p, int type, bool gated, bool grouped)
 {
-    static const char *const names[] = {"big", "mid", "small", "tile", "few", "few wide"};
+    static const char *const names[] = {"big", "mid", "small", "tile", "few", "few wide", "thin"};
     return names[choose_form(p, type == kFp32, gated, grouped)];
 }
 

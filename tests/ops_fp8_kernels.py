@@ -47,7 +47,7 @@ def norm_kernel(rows, width, dtype=1):
 
 
 # The kernel that writes 16 bits, by size; FP32 and 8-bit outputs take others of them.
-LINEAR = {"few": (70, 100, 60, False), "few wide": (300, 72, 700, False), "small": (601, 136, 699, False),
+LINEAR = {"few": (70, 100, 60, False), "few wide": (100, 72, 700, False), "thin": (300, 3000, 1001, False), "small": (601, 136, 699, False),
           "mid": (2601, 200, 2501, False), "big": (5001, 200, 1801, False), "tile": (9001, 72, 63, False)}
 GATED = {"few wide": (100, 72, 40, True), "small": (600, 136, 351, True), "mid": (2601, 200, 1251, True),
          "big": (2601, 264, 1700, True), "tile": (8200, 72, 32, True)}

@@ -252,7 +252,7 @@ def test_linear(rows, k, n):
 LARGE = [(5000, 200, 1800, False), (5000, 40, 1801, False), (4864, 128, 2048, False), (2600, 264, 1700, True),
          (2500, 72, 1500, False), (2048, 640, 2048, False), (1300, 200, 1100, True), (600, 136, 700, False), (640, 384, 640, False),
          (300, 64, 650, True), (9000, 72, 64, False), (9001, 33, 50, False), (4000, 64, 32, True), (700, 101, 903, False),
-         (513, 77, 455, True), (150, 1040, 1000, False), (20000, 64, 128, False), (5000, 202, 1800, False),
+         (513, 77, 455, True), (150, 1040, 1000, False), (20000, 64, 128, False), (5000, 202, 1800, False), (300, 2049, 1001, False),
          (2500, 130, 1500, True), (700, 102, 640, False), (700, 512, 1000, False), (2600, 513, 1700, True)]
 
 
@@ -280,7 +280,7 @@ def whole_numbers(g, rows, k, lo, hi, ld):
     return v[:, :k]
 
 
-@pytest.mark.parametrize("rows,n", [(5000, 1800), (4000, 900), (2500, 640), (60, 900)])
+@pytest.mark.parametrize("rows,n", [(5000, 1800), (4000, 900), (2500, 640), (520, 640), (60, 900)])
 @pytest.mark.parametrize("k", [64, 66, 68, 96, 126, 128, 130, 132, 188, 192, 254, 256, 260, 380, 384, 388, 65, 127, 129, 383, 34, 3])
 def test_last_columns_count_once(rows, n, k):
     """Whole numbers with scales that are powers of two, whose sums are exact, for widths that end anywhere in a block; a
