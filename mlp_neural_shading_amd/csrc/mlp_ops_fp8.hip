@@ -69,14 +69,26 @@ __device__ __forceinline__ void store16(uint8_t *p, u4 v)
     ((Bytes16 *)p)->v = v;
 }
 
-// The 16 columns from `col` of a row of `width`, zero past its end; reads no byte past it.
+// The 16 columns from `col` of a row of `width`, zero past its end; reads no byte past it.  A chunk that the row's end
+// divides is the row's last 16 bytes, shifted into place; of a row with fewer, bytes.  (Bytes always: 27,420 x 111 -> 1,241
+// 98 us instead of 36 in fp8_tile, 40,000 x 24 -> 256 15 instead of 12 in fp8_big.)
 __device__ __forceinline__ u4 load16_tail(const uint8_t *row, int col, int width)
 {
     if (col + 16 <= width)
         return load16(row + col);
     u4 v = (u4)0u;
+    if (col >= width)
+        return v;
+    if (width >= 16) {
+        typedef uint64_t u2 __attribute__((ext_vector_type(2)));
+        const u2 last = __builtin_bit_cast(u2, load16(row + width - 16));
+        const int drop = 8 * (16 - (width - col));  // 8 .. 120
+        const uint64_t lo = last[0], hi = last[1];
+        const u2 w = drop < 64 ? u2{lo >> drop | hi << (64 - drop), hi >> drop} : u2{hi >> (drop - 64), 0};
+        return __builtin_bit_cast(u4, w);
+    }
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < 15; ++j)
         if (col + j < width)
             v[j / 4] |= (unsigned)row[col + j] << (8 * (j % 4));
     return v;
@@ -479,7 +491,8 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 }
 
 // The same through registers, for rows at any address: each thread loads its chunks of stage s + 1 while stage s is
-// multiplied.  Bound by latency: 65,536 x 1,001 -> 64 22 us (75 MB, 3.4 TB/s).
+// multiplied.  Bound by latency, with three workgroups a CU (168 registers): rows 1,001 bytes apart, 65,536 -> 64 22 us (75 MB,
+// 3.4 TB/s), 5,003 -> 777 22 (two a CU and every chunk tested for the row's end: 26, 32); 27,420 x 111 -> 1,241 36.
 template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int WPE>
 __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void fp8_tile(Fp8ProductArgs p)
 {
@@ -530,12 +543,21 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
     const int steps = (p.in + BK - 1) / BK;
     auto load = [&](int s) {
         const int col = s * BK + 16 * c;
+        if ((s + 1) * BK <= p.in) {
 #pragma unroll
-        for (int i = 0; i < CA; ++i)
-            ra[i] = load16_tail(wp[i], col, p.in);
+            for (int i = 0; i < CA; ++i)
+                ra[i] = load16(wp[i] + col);
 #pragma unroll
-        for (int i = 0; i < CB; ++i)
-            rb[i] = load16_tail(xp[i], col, p.in);
+            for (int i = 0; i < CB; ++i)
+                rb[i] = load16(xp[i] + col);
+        } else {
+#pragma unroll
+            for (int i = 0; i < CA; ++i)
+                ra[i] = load16_tail(wp[i], col, p.in);
+#pragma unroll
+            for (int i = 0; i < CB; ++i)
+                rb[i] = load16_tail(xp[i], col, p.in);
+        }
         rs = scale[s];
     };
     auto store = [&](int s) {
@@ -892,7 +914,7 @@ hipError_t launch(const Fp8ProductArgs &p, hipStream_t stream)
             hipLaunchKernelGGL((fp8_big<T, false, false, 2, 2, 1, 1, 3, 2>), grid, block, 0, stream, p);
         break;
     case kTile:
-        hipLaunchKernelGGL((fp8_tile<T, GROUPED, GATED, 1, 4, 2, 1, 2>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((fp8_tile<T, GROUPED, GATED, 1, 4, 2, 1, 3>), grid, block, 0, stream, p);
         break;
     default:
         // a block for each of up to 16 waves

@@ -192,30 +192,43 @@ PyObject *rms_norm(PyObject *, PyObject *const *o, Py_ssize_t n)
     });
 }
 
-// x, block_rows -> (values, scales); one matrix
+// x, block_rows -> (values, scales); one matrix, or several
 PyObject *quantize(PyObject *, PyObject *const *o, Py_ssize_t n)
 {
     return guarded(n, 2, [&]() {
         const at::Tensor &x = tensor(o[0]);
-        need(x.dim() == 2);
         const Call c(x);
-        const int64_t rows = x.size(0), width = x.size(1), block_rows = number(o[1]);
-        need((block_rows == 1 || block_rows == MLP_FP8_BLOCK) && width <= MLP_OPS_MAX_WIDTH);
+        const bool many = x.dim() == 3;
+        need(many || x.dim() == 2);
+        const int64_t count = many ? x.size(0) : 1, rows = x.size(many), width = x.size(many + 1), block_rows = number(o[1]);
+        need((block_rows == 1 || block_rows == MLP_FP8_BLOCK) && width <= MLP_OPS_MAX_WIDTH && count <= MLP_FP8_MAX_COUNT);
         const int64_t down = block_rows == 1 ? rows : blocks(rows);
-        const at::Tensor values = c.values(rows, width), scales = c.empty(down, blocks(width), Type::Float);
+        at::Tensor values = c.values(count * rows, width), scales = c.empty(count * down, blocks(width), Type::Float);
         mlp_quantize_args a{};
         a.rows = rows;
-        a.count = 1;
+        a.count = (int32_t)count;
         a.width = (int32_t)width;
         a.dtype = code(x.scalar_type());
         a.block_rows = (int32_t)block_rows;
         a.x = x.data_ptr();
-        a.ldx = c.matrix(x, rows, width);
+        if (many) {
+            need(x.stride(2) == 1 || width <= 1);
+            a.ldx = rows > 1 ? x.stride(1) : width;
+            a.x_stride = x.stride(0);
+        } else {
+            a.ldx = c.matrix(x, rows, width);
+        }
         a.values = (uint8_t *)values.data_ptr();
         a.ldv = values.stride(0);
+        a.v_stride = rows * a.ldv;
         a.scales = (float *)scales.data_ptr();
         a.lds = blocks(width);
+        a.s_stride = down * a.lds;
         need(mlp_quantize(&a, c.stream()) == MLP_OK);
+        if (many) {
+            values = values.unflatten(0, {count, rows});
+            scales = scales.unflatten(0, {count, down});
+        }
         return tuple({values, scales});
     });
 }

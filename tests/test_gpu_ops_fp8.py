@@ -281,7 +281,7 @@ def whole_numbers(g, rows, k, lo, hi, ld):
 
 
 @pytest.mark.parametrize("rows,n", [(5000, 1800), (4000, 900), (2500, 640), (520, 640), (60, 900)])
-@pytest.mark.parametrize("k", [64, 66, 68, 96, 126, 128, 130, 132, 188, 192, 254, 256, 260, 380, 384, 388, 65, 127, 129, 383, 34, 3])
+@pytest.mark.parametrize("k", [64, 66, 68, 96, 126, 128, 130, 132, 188, 192, 254, 256, 260, 380, 384, 388, 65, 127, 129, 383, 34, 3, 15, 16, 17, 23, 24, 25, 31, 111])
 def test_last_columns_count_once(rows, n, k):
     """Whole numbers with scales that are powers of two, whose sums are exact, for widths that end anywhere in a block; a
     row stride beyond the width holds NaN, and one row a NaN in the first column of its last 128."""
@@ -656,6 +656,7 @@ def test_both_ways_to_the_library_are_one(rows, k, n, monkeypatch):
     calls = [lambda: E.rms_norm(f), lambda: E.rms_norm(f.half(), weight.half(), residual=r.half(), out="both", eps=1e-3),
              lambda: E.rms_norm(f.bfloat16(), weight.bfloat16(), out="fp8"), lambda: E.rms_norm(f.half(), out_dtype=torch.float32),
              lambda: E.quantize(f), lambda: E.quantize(f.half(), block_rows=128), lambda: E.linear(X, W),
+             lambda: E.quantize(f.view(rows, 1, k).expand(rows, 3, k).contiguous(), block_rows=128), lambda: E.quantize(f.half()[None]),
              lambda: E.linear(X, W, b, residual=res.half(), act="gelu", out_dtype=torch.float16),
              lambda: E.linear(X, WG, act="silu", gated=True, out_dtype=FP8), lambda: E.linear(X, W, out_dtype=torch.float32),
              lambda: E.expert_linear(X, w3, plan, k=2, combine=True, weight=torch.ones(rows, 2, device=device()), residual=res.bfloat16()),
