@@ -799,8 +799,8 @@ __global__ __launch_bounds__(256) void sum_terms(TermsArgs c)
 
 // kBig 256 weight rows x 256 rows (FULL: 256 x 128), kMid 128 x 128 (of 8 waves; FULL: of 4), kSmall 128 x 64 (all three
 // straight into LDS), kTile 64 x 128 through registers, kFew 16 x 16, kFewWide 32 x 16, kThin 64 x 64 straight into LDS (gated,
-// by two waves that hold 32 gates and the 32 they gate: 13.5 against kSmall's 15.6 for 64 x 4,096 -> 2 x 2,048, not built).  kMid of 8 waves against 4:
-// 5,003 x 1,008 -> 777 15.7 against 16.9, 65,536 x 1,024 -> 1,024 107 against 109; widened 207 against 171.
+// by two waves that hold 32 gates and the 32 they gate: 13.5 against kSmall's 15.6 for 64 x 4,096 -> 2 x 2,048, not built).
+// kMid of 8 waves against 4: 5,003 x 1,008 -> 777 15.7 against 16.9, 65,536 x 1,024 -> 1,024 107 against 109; widened 207 against 171.
 enum Form { kBig, kMid, kSmall, kTile, kFew, kFewWide, kThin };
 struct Shape {
     int bm, bn, threads;
