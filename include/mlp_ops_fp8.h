@@ -114,9 +114,8 @@ int mlp_fp8_linear(const mlp_fp8_linear_args *args, void *stream);
 
 /* mlp_expert_linear with operands in the format above, each expert's layer as in mlp_fp8_linear.  offsets, slots and
  * places are mlp_dispatch's, with the same clamping; x_scale has a row for each row of x, y_scale for each of y (rows
- * behind offsets[experts] are left as they were).  MLP_DTYPE_FP8 goes without combine.  Combined into 16 bits, a term may be
- * off by 0.51 * 2^-15 of the largest of its 32 neighbouring outputs of the slot (or of 2^-111, if that is more); the sum is
- * FP32 and is rounded once. */
+ * behind offsets[experts] are left as they were).  MLP_DTYPE_FP8 goes without combine.  Combined, a token's terms and their sum
+ * are FP32, rounded once. */
 typedef struct mlp_fp8_expert_linear_args {
     int64_t tokens; /* tokens * k: 0 .. INT32_MAX */
     int32_t k;

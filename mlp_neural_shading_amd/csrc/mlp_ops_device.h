@@ -304,65 +304,6 @@ struct __attribute__((packed, aligned(2))) Float8 {
     float v[8];
 };
 
-// Terms of a sum on their way to it, where it is rounded to 16 bits: 32 neighbouring outputs of a row as whole numbers up to
-// 32,766 and their FP32 scale, of which four neighbouring lanes hold 8 each.  Off by at most 0.51 * 2^-15 of the largest of
-// the 32: a 16-bit float's own rounding of the term alone is up to 64 times that (FP16: 8), and FP32 rows are twice the
-// bytes.  Larger numbers stand for infinities and NaN.
-__device__ __forceinline__ u4 to_terms(f8 v, float &scale)
-{
-    float m = 0.0f, sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        m = fmaxf(m, fabsf(v[j]));
-        sum += v[j];
-    }
-    const bool odd = !(fabsf(sum) < __builtin_inff());  // wherever one of them is not finite, hardly ever else
-    if (odd) {
-        m = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            m = fmaxf(m, fabsf(v[j]) < __builtin_inff() ? fabsf(v[j]) : 0.0f);
-    }
-    auto other = [](float w, auto perm) {
-        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, w), decltype(perm)::value, 0xf, 0xf, true));
-    };
-    m = fmaxf(m, other(m, Number<0xb1>{}));  // quad_perm 1 0 3 2
-    m = fmaxf(m, other(m, Number<0x4e>{}));  // quad_perm 2 3 0 1
-    scale = fmaxf(m * (1.0f / 32766.0f), 0x1p-126f);
-    const float inv = 1.0f / scale * (1.0f / 32767.0f);
-    u4 q;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        q[j] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_pknorm_i16(v[2 * j] * inv, v[2 * j + 1] * inv));  // times 32,767, nearest
-    if (odd)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (!(fabsf(v[j]) < __builtin_inff())) {
-                const unsigned code = v[j] > 0.0f ? 0x7fffu : v[j] < 0.0f ? 0x8001u : 0x8000u, both = q[j / 2];
-                q[j / 2] = j % 2 ? (both & 0xffffu) | code << 16 : (both & 0xffff0000u) | code;
-            }
-    return q;
-}
-
-__device__ __forceinline__ f8 from_terms(u4 q, float scale)
-{
-    typedef short s8 __attribute__((ext_vector_type(8)));
-    const s8 t = __builtin_bit_cast(s8, q);
-    f8 v;
-    bool odd = false;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        v[j] = (float)t[j] * scale;
-        odd |= t[j] == 32767 || t[j] < -32766;
-    }
-    if (odd)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (t[j] == 32767 || t[j] < -32766)
-                v[j] = t[j] == -32768 ? __builtin_nanf("") : t[j] < 0 ? -__builtin_inff() : __builtin_inff();
-    return v;
-}
-
 // The epilogue of one wave: MT x NT MFMA tiles whose first weight row is tile row r0 and first row `row` (the same
 // in all lanes).  One 32 x 32 tile of outputs at a time: the activation and the gate on the sums as they lie, then
 // through 4 KB of LDS of the wave's own (no barrier: one wave writes and reads it) into rows, from which a lane takes
@@ -373,7 +314,7 @@ __device__ __forceinline__ f8 from_terms(u4 q, float scale)
 // SIXTEEN: a tile is four of 16 x 16, of which lane (g, n) holds outputs 4 g .. 4 g + 3 of row n: element 4 e + i is that
 // of outputs 16 (e / 2) .. and rows 16 (e % 2) ..  OUT: what is written, where the kernel is for one kind (the branches of
 // the others cost 10 us of 96 in 65,536 x 1,024 -> 1,024 with 8-bit operands).
-enum { kAnyRows = -1, kHalfRows, kWholeRows, kTermRows };  // 16 bits or FP32 by p.y_fp32, 16 bits, FP32, terms
+enum { kAnyRows = -1, kHalfRows, kWholeRows };  // 16 bits or FP32 by p.y_fp32, 16 bits, FP32
 template <class T, bool GATED, bool SIXTEEN = false, int OUT = kAnyRows, class ARGS, int MT, int NT>
 __device__ __forceinline__ void epilogue(const ARGS &p, f16x (&acc)[MT][NT], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
 {
@@ -428,28 +369,6 @@ __device__ __forceinline__ void epilogue(const ARGS &p, f16x (&acc)[MT][NT], uin
             z *= acc[mt + 1][nt];
         const int left = outs - 32 * (t % MO) - oc;  // outputs from this lane's first on
         const int64_t y_tile = (int64_t)(32 * nt) * ldy + 32 * (t % MO), r_tile = (int64_t)(32 * nt) * ldr + 32 * (t % MO);
-        if constexpr (OUT == kTermRows) {  // 16-bit whole numbers and a scale for the 32 of a row
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int r = 16 * (q % 2) + (lane & 15);
-                *(f4 *)(ob + r * 128 + 16 * ((4 * (q / 2) + (lane >> 4)) ^ ((r >> 1) & 7))) = f4{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int rt = 16 * i + rl, sw = (rt >> 1) & 7;
-                const f4 lo = *(const f4 *)(ob + rt * 128 + 16 * ((oc / 4) ^ sw)), hi = *(const f4 *)(ob + rt * 128 + 16 * ((oc / 4 + 1) ^ sw));
-                const f8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                float scale;
-                const u4 term = to_terms(v, scale);
-                if (32 * nt + rt >= rows)
-                    continue;
-                *(u4 *)((int16_t *)p.y + row * p.ldy + first + y_tile + y_at[i]) = term;
-                if (oc == 0)
-                    p.terms[(row + 32 * nt + rt) * (p.ldy / 32) + first / 32 + t % MO] = scale;
-            }
-            continue;
-        }
         if (!p.residual && !y_fp32) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {

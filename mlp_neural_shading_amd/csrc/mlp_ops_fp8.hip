@@ -122,6 +122,8 @@ __device__ __forceinline__ f4 bias_rows(const float *bias, int o0, int r, int ou
     return b;
 }
 
+struct Parts;  // what a kernel writes, for T below
+
 // The epilogue of a wave's MT x NT tiles of 32 x 32.
 template <class T, bool GATED, int MT, int NT>
 __device__ __forceinline__ void finish(const Fp8ProductArgs &p, float (&acc)[2 * MT][2 * NT][4], uint8_t *ob, int o0, int r0, int64_t row, int64_t row1)
@@ -134,10 +136,8 @@ __device__ __forceinline__ void finish(const Fp8ProductArgs &p, float (&acc)[2 *
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 t[mt][nt][j] = acc[2 * mt + j / 8][2 * nt + j / 4 % 2][j % 4];
-    if constexpr (std::is_same<T, float>::value)
+    if constexpr (std::is_same<T, float>::value || std::is_same<T, Parts>::value)
         epilogue<_Float16, GATED, true, kWholeRows>(p, t, ob, o0, r0, row, row1);
-    else if constexpr (std::is_same<T, int16_t>::value)
-        epilogue<_Float16, GATED, true, kTermRows>(p, t, ob, o0, r0, row, row1);
     else
         epilogue<T, GATED, true, kHalfRows>(p, t, ob, o0, r0, row, row1);
 }
@@ -225,8 +225,8 @@ __device__ __forceinline__ void finish8(const Fp8ProductArgs &p, float (&acc)[2 
     }
 }
 
-// T is what a kernel writes: _Float16 or __bf16 rows, float (FULL: FP32 or 8-bit rows) or int16_t (terms).  (One kernel for
-// all, by branches in the epilogue: 96 us for 65,536 x 1,024 -> 1,024 instead of 83.)
+// T is what a kernel writes: _Float16 or __bf16 rows, float (FULL: FP32 or 8-bit rows) or Parts (FP32 rows that are summed
+// into 16 bits).  (One kernel for all, by branches in the epilogue: 96 us for 65,536 x 1,024 -> 1,024 instead of 83.)
 //
 // WM x WN waves, each MT x NT tiles of 32 weight rows x 32 rows, as four of 16 x 16.  A stage is 128 columns, 128 bytes
 // of every row; NS stages go from memory straight into LDS, and so do the rows' scales, for four blocks at a time.  Chunk c
@@ -740,61 +740,6 @@ __global__ __launch_bounds__(1024) void fp8_few(Fp8ProductArgs p)
     }
 }
 
-// One token's row of a combined product from 16-bit terms, in the order of j and in FP32; 8 outputs per thread.  Bound by
-// bytes: 8,192 tokens x 4 x 2,048 with a residual 34 us (210 MB); from FP32 rows 66.
-template <class T, class INDEX>
-__global__ __launch_bounds__(256) void sum_terms(TermsArgs c)
-{
-    typedef typename Vec8<T>::type V8;
-    struct __attribute__((packed, aligned(2))) Half8 {
-        V8 v;
-    };
-    const INDEX chunks = (c.out + 7) / 8, all = (INDEX)c.tokens * chunks;
-    const int64_t n = c.tokens * c.k;
-    for (INDEX i = (INDEX)blockIdx.x * 256 + threadIdx.x; i < all; i += (INDEX)gridDim.x * 256) {
-        const INDEX t = i / chunks;
-        const int o = (int)(i - t * chunks) * 8;
-        const int32_t *places = c.places + (int64_t)t * c.k;
-        const float *weights = c.weight + (int64_t)t * c.k;
-        f8 v = (f8)0.0f;
-        for (int j0 = 0; j0 < c.k; j0 += 4) {
-            u4 term[4];
-            float scale[4], weight[4];
-            bool on[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int place = j0 + j < c.k ? places[j0 + j] : -1;
-                on[j] = place >= 0 && place < n;  // else dropped
-                weight[j] = on[j] && c.weight ? weights[j0 + j] : 1.0f;
-                if (on[j]) {
-                    term[j] = *(const u4 *)(c.terms + (int64_t)place * c.ld + o);
-                    scale[j] = c.scales[(int64_t)place * (c.ld / 32) + o / 32];
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (on[j]) {
-                    const f8 part = from_terms(term[j], scale[j]);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[e] = fmaf(weight[j], part[e], v[e]);
-                }
-        }
-        T *y = (T *)c.y + (int64_t)t * c.ldy + o;
-        const T *res = c.residual ? (const T *)c.residual + (int64_t)t * c.ldr + o : nullptr;
-        if (o + 8 <= c.out) {
-            if (res)
-                v += __builtin_convertvector(((const Half8 *)res)->v, f8);
-            ((Half8 *)y)->v = __builtin_convertvector(v, V8);  // nearest even
-        } else {
-#pragma unroll
-            for (int e = 0; e < 7; ++e)
-                if (o + e < c.out)
-                    y[e] = (T)(v[e] + (res ? (float)res[e] : 0.0f));
-        }
-    }
-}
-
 // ---- which kernel ---------------------------------------------------------------------------------
 
 // kBig 256 weight rows x 256 rows (FULL: 256 x 128), kMid 128 x 128 (of 8 waves; FULL: of 4), kSmall 128 x 64 (all three
@@ -933,7 +878,7 @@ hipError_t launch(const Fp8ProductArgs &p, bool gated, bool grouped, hipStream_t
 {
     if (grouped)
         return gated ? launch<T, true, true>(p, stream) : launch<T, true, false>(p, stream);
-    if constexpr (std::is_same<T, int16_t>::value)  // terms are of slots
+    if constexpr (std::is_same<T, Parts>::value)  // they are of slots
         return hipErrorInvalidValue;
     else
         return gated ? launch<T, false, true>(p, stream) : launch<T, false, false>(p, stream);
@@ -952,29 +897,6 @@ bool fp8_product_rounds(const Fp8ProductArgs &p, bool gated, bool grouped)
     return rounds_itself(choose_form(p, true, gated, grouped), gated);
 }
 
-bool fp8_product_terms(const Fp8ProductArgs &p, int type, bool gated, bool grouped)
-{
-    const Form form = choose_form(p, type == kFp32, gated, grouped);
-    return type != kFp32 && form != kFew && form != kFewWide;
-}
-
-template <class T>
-hipError_t launch_terms_typed(const TermsArgs &c, hipStream_t stream)
-{
-    const int64_t work = c.tokens * ((c.out + 7) / 8), most = 256 * 32, blocks = (work + 255) / 256;
-    const dim3 grid((unsigned)(blocks < most ? blocks : most));
-    if (work < (int64_t)1 << 31)  // and so is the last step past it
-        hipLaunchKernelGGL((sum_terms<T, unsigned>), grid, dim3(256), 0, stream, c);
-    else
-        hipLaunchKernelGGL((sum_terms<T, int64_t>), grid, dim3(256), 0, stream, c);
-    return hipGetLastError();
-}
-
-hipError_t launch_terms(const TermsArgs &c, int out_dtype, hipStream_t stream)
-{
-    return out_dtype == kFp16 ? launch_terms_typed<_Float16>(c, stream) : launch_terms_typed<__bf16>(c, stream);
-}
-
 const char *fp8_product_kernel(const Fp8ProductArgs &p, int type, bool gated, bool grouped)
 {
     static const char *const names[] = {"big", "mid", "small", "tile", "few", "few wide", "thin"};
@@ -983,8 +905,8 @@ const char *fp8_product_kernel(const Fp8ProductArgs &p, int type, bool gated, bo
 
 hipError_t launch_fp8_product(const Fp8ProductArgs &p, int type, bool gated, bool grouped, hipStream_t stream)
 {
-    if (p.terms)
-        return launch<int16_t>(p, gated, grouped, stream);
+    if (type != kFp32 && p.y_fp32)
+        return launch<Parts>(p, gated, grouped, stream);
     return type == kFp16 ? launch<_Float16>(p, gated, grouped, stream)
            : type == kBf16 ? launch<__bf16>(p, gated, grouped, stream)
                            : launch<float>(p, gated, grouped, stream);

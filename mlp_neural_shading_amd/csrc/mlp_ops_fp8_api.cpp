@@ -186,27 +186,17 @@ Fp8ProductArgs sizes(const mlp_fp8_expert_linear_args *a)
 // 8-bit outputs have FP32 scales.
 int result_type(int out_dtype) { return out_dtype == MLP_DTYPE_FP8 ? kFp32 : out_dtype; }
 
-// What the workspace holds: rows for another kernel to combine or to round to 8 bits, in FP32, or as 16-bit terms (32's
-// multiple of them a row) and behind them their scales.
-enum Rows { kNoRows, kFp32Rows, kTermRows };
-
-Rows rows_of(const Fp8ProductArgs &p, int out_dtype, bool combine, bool gated, bool grouped)
+// Whether the workspace holds FP32 rows, for another kernel to combine or to round to 8 bits.
+bool needs_rows(const Fp8ProductArgs &p, int out_dtype, bool combine, bool gated, bool grouped)
 {
-    if (combine)
-        return fp8_product_terms(p, result_type(out_dtype), gated, grouped) ? kTermRows : kFp32Rows;
-    return out_dtype == MLP_DTYPE_FP8 && !fp8_product_rounds(p, gated, grouped) ? kFp32Rows : kNoRows;
+    return combine || (out_dtype == MLP_DTYPE_FP8 && !fp8_product_rounds(p, gated, grouped));
 }
-
-int64_t term_stride(int out_width) { return round_up(out_width, 32); }
 
 template <class A>
 uint64_t rows_need(const A *a, bool combine, bool grouped)
 {
     const Fp8ProductArgs p = sizes(a);
-    if (p.rows == 0)
-        return 0;
-    const Rows r = rows_of(p, a->out_dtype, combine, a->gated, grouped);
-    return r == kNoRows ? 0 : (uint64_t)p.rows * (r == kTermRows ? term_stride(p.out) * 2 + term_stride(p.out) / 32 * 4 : part_stride(p.out) * 4);
+    return p.rows && needs_rows(p, a->out_dtype, combine, a->gated, grouped) ? (uint64_t)p.rows * part_stride(p.out) * 4 : 0;
 }
 
 uint64_t linear_need(const mlp_fp8_linear_args *a) { return rows_need(a, false, false); }
@@ -276,12 +266,7 @@ void outputs(const A *a, bool combine, bool grouped, Fp8ProductArgs &p)
     p.ldws = a->ldws;
     p.bias = a->bias;
     p.act = activation(a->act, a->out_dtype);
-    const Rows rows = rows_of(p, a->out_dtype, combine, a->gated, grouped);
-    if (rows == kTermRows) {
-        p.y = a->workspace;
-        p.ldy = term_stride(p.out);
-        p.terms = (float *)((int16_t *)a->workspace + p.rows * p.ldy);
-    } else if (rows == kFp32Rows) {
+    if (needs_rows(p, a->out_dtype, combine, a->gated, grouped)) {
         p.y = a->workspace;
         p.ldy = part_stride(p.out);
         p.y_fp32 = 1;
@@ -485,24 +470,7 @@ int mlp_fp8_expert_linear(const mlp_fp8_expert_linear_args *a, void *stream)
     hipError_t err = launch_fp8_product(p, result_type(a->out_dtype), a->gated, true, (hipStream_t)stream);
     if (err != hipSuccess)
         return hip_fail(err, "launching the experts' layer");
-    if (a->combine && p.terms) {
-        TermsArgs c{};
-        c.terms = (const int16_t *)p.y;
-        c.scales = p.terms;
-        c.ld = p.ldy;
-        c.places = a->places;
-        c.weight = a->weight;
-        c.residual = a->residual;
-        c.ldr = a->ldr;
-        c.y = a->y;
-        c.ldy = a->ldy;
-        c.tokens = a->tokens;
-        c.k = a->k;
-        c.out = a->out_width;
-        err = launch_terms(c, a->out_dtype, (hipStream_t)stream);
-        if (err != hipSuccess)
-            return hip_fail(err, "launching the combination");
-    } else if (a->combine) {
+    if (a->combine) {
         CombineArgs c{};
         c.part = (const float *)a->workspace;
         c.ldp = part_stride(a->out_width);

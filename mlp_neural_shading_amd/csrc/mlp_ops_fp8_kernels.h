@@ -54,31 +54,13 @@ struct Fp8ProductArgs : ProductArgs {
     int64_t ldv;
     float *ys;
     int64_t ldys;
-    float *terms;  // scales [rows][ldy / 32] of terms: y is int16_t then, rows of 32's multiples; or NULL
 };
-// type: what becomes of the results, kFp16 or kBf16 (at once, or from FP32 rows in a workspace), or kFp32 for FP32's accuracy.
+// type: what becomes of the results, kFp16 or kBf16 (at once, or with y_fp32 from FP32 rows in a workspace), or kFp32 for FP32's
+// accuracy.
 hipError_t launch_fp8_product(const Fp8ProductArgs &p, int type, bool gated, bool grouped, hipStream_t stream);
 bool fp8_product_fits(const Fp8ProductArgs &p, int type, bool gated, bool grouped);
 // Whether the product's kernel (type kFp32) rounds to 8 bits itself: `values` and `ys` may be set, y is not used then.
 bool fp8_product_rounds(const Fp8ProductArgs &p, bool gated, bool grouped);
-// Whether its kernel writes terms (to be summed and rounded to 16 bits).
-bool fp8_product_terms(const Fp8ProductArgs &p, int type, bool gated, bool grouped);
-
-// y[t] = round(sum_j weight[t][j] * terms[places[t][j]] + residual[t]).
-struct TermsArgs {
-    const int16_t *terms;  // [slots][ld]
-    const float *scales;   // [slots][ld / 32]
-    int64_t ld;
-    const int32_t *places;
-    const float *weight;  // NULL: 1
-    const void *residual;
-    int64_t ldr;
-    void *y;
-    int64_t ldy;
-    int64_t tokens;
-    int k, out;
-};
-hipError_t launch_terms(const TermsArgs &c, int out_dtype, hipStream_t stream);
 const char *fp8_product_kernel(const Fp8ProductArgs &p, int type, bool gated, bool grouped);
 
 }  // namespace mlpk
