@@ -30,9 +30,12 @@ __device__ __forceinline__ h8 widen(int lo, int hi)
 // The sums of a block: 16 weight rows x 16 rows over 128 columns, of which lane (g, n) holds 32 of row n for both operands
 // (which 32 does not matter, as long as it is the same ones) and weight rows 4 g .. 4 g + 3 of row n of the result.
 // The matrix unit adds the products of E4M3 operands 8 at a time (8 neighbouring bytes of a lane), each cut to a multiple
-// of 2^-13 of the largest one's power of two, and then in FP32: off by about 2^-16 of a result.  That is far below the
-// rounding of a 16-bit output.  For outputs that keep more (FULL: FP32 rows, and 8-bit rows, whose scales are FP32) the
-// operands are widened to FP16, which holds them exactly and whose products are added in FP32, at half the rate.
+// of 2^-13 of the largest one's power of two, and then in FP32: off by up to 7 * 2^-13 of the groups' largest products, of a
+// sum that cancels too.  In the root mean square that is 2^-16 of the results' own (2^-14 where one column of 8 outweighs the
+// others), below a 16-bit rounding's 2^-12 (BF16 2^-9), while 2 % (10 %) of the results are off by more than FP16's half a step,
+// 0.3 % (1.4 %) by more than BF16's.  It is what 8-bit operands are taken for: their own rounding is 2^-5 of a result, and twice
+// the rate.  For outputs that keep more (FULL: FP32 rows, and 8-bit rows, whose scales are FP32) the operands are widened to
+// FP16, which holds them exactly and whose products are added in FP32, at half the rate.
 template <bool FULL>
 __device__ __forceinline__ f4 block_sums(i8 a, i8 b)
 {

@@ -249,7 +249,11 @@ def _done(out, given):
 
 def linear(x: Quantized, w: Quantized, bias=None, *, residual=None, act="none", gated=False, out=None,
            out_dtype=torch.bfloat16):
-    """``act(x w^T + bias) + residual``, summed in FP32 and rounded once: one affine layer with 8-bit operands.
+    """``act(x w^T + bias) + residual``: one affine layer with 8-bit operands, rounded once from an FP32 sum.
+
+    The products of 16-bit outputs are the matrix unit's own, cut 8 at a time to 2^-13 of the largest: in the root mean
+    square off by 2^-16 to 2^-14 of the outputs' own, which an output whose products cancel may exceed by far.  Of float32
+    and float8_e4m3fn outputs no product is cut, at half the rate; ``include/mlp_ops_fp8.h`` states the bound.
 
     ``x`` has a scale for each row and 128 columns, ``w`` [out, in] one for each 128 x 128; ``bias`` float32 [out];
     ``act`` one of ``ops.ACTIVATIONS``.  ``gated``: w and bias have 2 * out rows, the gates first, with blocks of their
@@ -273,7 +277,8 @@ def linear(x: Quantized, w: Quantized, bias=None, *, residual=None, act="none", 
 
 def expert_linear(x: Quantized, w: Quantized, plan: Dispatch, bias=None, *, k, act="none", gated=False, rows="tokens",
                   combine=False, weight=None, residual=None, out=None, out_dtype=torch.bfloat16):
-    """Each routed row through its own expert's layer with 8-bit operands, as ``ops.expert_linear``.
+    """Each routed row through its own expert's layer with 8-bit operands, as ``ops.expert_linear``, with the products of
+    ``linear`` here; ``combine`` sums FP32 rows, whose products are cut where ``out_dtype`` has 16 bits.
 
     ``w`` [experts, out or 2 * out, in] with scales [experts, blocks of 128 rows (of each half), blocks], ``bias``
     float32 [experts, out or 2 * out], ``plan`` from ``ops.dispatch``.  Rows by slot may be float8_e4m3fn: ``Quantized``
