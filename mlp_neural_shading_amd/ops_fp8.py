@@ -6,7 +6,7 @@ the experts' layers on routed rows (``expert_linear``).
 rows (weights).  As in ``ops``: tensors are checked, outputs and scratch memory come from torch's allocator on the
 current stream, nothing here computes or waits, and inputs that require gradients are refused.  The usual call of each
 (new outputs, the current device) goes through an extension in C++, ``_torch_fp8``, which leaves any other to the
-functions here.  A layer of experts with its weights rounded once::
+functions here; where it is not built, they take every call.  A layer of experts with its weights rounded once::
 
     w1, w2 = ops_fp8.quantize(w1, block_rows=128, gated=True), ops_fp8.quantize(w2, block_rows=128)
 
@@ -19,21 +19,28 @@ functions here.  A layer of experts with its weights rounded once::
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
 from torch.autograd import forward_ad
 
+from .ops import (ACTIVATIONS, DTYPES, Dispatch, _call, _choice, _count, _f32, _FLOATS, _i32, _i64, _matrix, _out_dtype,
+                  _p, _packer, _tensor, _u64, _vector, _workspace, _written)
+
 try:
     from . import _torch_fp8 as _usual
 except ImportError as e:
-    raise RuntimeError("the extension _torch_fp8 is not built; run `python -m mlp_neural_shading_amd.build`: %s" % e) from e
-from .ops import (ACTIVATIONS, DTYPES, Dispatch, _call, _choice, _count, _f32, _FLOATS, _i32, _i64, _matrix, _out_dtype,
-                  _p, _packer, _tensor, _u64, _vector, _workspace, _written)
+    class _usual:
+        """In its place: leaves every call to the functions here."""
+        rms_norm = quantize = linear = expert_linear = staticmethod(lambda *a: None)
+    if not isinstance(e, ModuleNotFoundError):
+        warnings.warn("the extension _torch_fp8 does not load, build it again: %s" % e)
 
 MLP_DTYPE_FP8 = 3
 BLOCK = 128
 FP8 = torch.float8_e4m3fn
+
 
 class RmsNormArgs(ctypes.Structure):
     _fields_ = [("rows", _i64), ("width", _i32), ("dtype", _i32), ("out_dtype", _i32), ("eps", _f32), ("x", _p),
