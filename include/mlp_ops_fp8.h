@@ -7,7 +7,8 @@
  * column 0, the last of a row or column is as short as it has to be.  The element is value * scale.
  *   scale = max(amax / 448, 2^-126),  value = round(v * (1 / scale)),  to nearest, ties to even,
  * amax over the block's finite elements; a NaN or an infinity becomes NaN by itself and leaves the others as they are.
- * Scales made elsewhere are taken as they are, of any sign and size.
+ * Scales made elsewhere are taken as they are, of any sign; a layer multiplies those of its two operands' blocks in FP32, so a
+ * block whose product is infinite gives infinities or NaN, whatever its values, and one below 2^-126 has fewer bits.
  *
  * Conventions as in mlp_ops.h: status codes and mlp_last_error, arguments checked on the host before any HIP call,
  * work enqueued on `stream` without allocating or waiting, scratch memory the caller's, no state, the same bits for

@@ -80,3 +80,35 @@ def test_sums_of_cut_products(rows, k, n, gated, kind):
         assert float(off / (half.square().mean() / 3).sqrt()) < 1.1, (t, kind)
     exact, bound = F.linear64(x, w, full=True)
     R.check(E.linear(put(x), put(w), out_dtype=torch.float32), exact, bound, torch.float32, kind)
+
+
+@pytest.mark.parametrize("scale,other", [(float("inf"), 1.0), (2.0 ** 100, 2.0 ** 100)])
+@pytest.mark.parametrize("rows,k,n,gated", K.LINEAR.values())
+def test_scales_past_the_range(rows, k, n, gated, scale, other):
+    """An infinite scale, or two whose product is infinite, leave their own rows and outputs without finite numbers, and the
+    others as they are."""
+    g = gen(rows + n)
+    x, w = F.quantize(torch.randn(rows, k, generator=g)), F.quantize_weights(torch.randn(n, k, generator=g))
+    row, sure = rows // 2, n
+    xs, ws = x[1].clone(), w[1].clone()
+    if other != 1.0:
+        ws[:, -1] *= other  # with the other rows' scales, of some 2^-8, in range
+    elif n > 128:
+        sure = (F.blocks(n) - 1) * 128
+    want, bound = F.linear64(x, (w[0], ws))
+    exact, close = F.linear64(x, (w[0], ws), full=True)
+    xs[row, -1] = scale
+    if sure < n:
+        ws[-1, 0] = scale
+    X, W = put((x[0], xs)), put((w[0], ws))
+    keep = [r for r in range(rows) if r != row]
+    log("scales", rows, k, n, scale, other)
+    for t, v, e in ((torch.bfloat16, want, bound), (torch.float32, exact, close)):
+        y = E.linear(X, W, out_dtype=t).cpu()
+        assert not torch.isfinite(y[row]).any()
+        assert not torch.isfinite(y[:, sure:]).any()
+        R.check(y[keep][:, :sure], v[keep][:, :sure], e[keep][:, :sure], t)
+    q = E.linear(X, W, out_dtype=FP8)
+    values, scales = q.values.cpu().view(torch.uint8), q.scales.cpu()
+    assert bool((values[row] & 0x7F == 0x7F).all()) and bool((values[:, sure:] & 0x7F == 0x7F).all())
+    F.check_quantized((values[keep][:, :sure].view(FP8), scales[keep][:, :F.blocks(sure)]), exact[keep][:, :sure], close[keep][:, :sure])
