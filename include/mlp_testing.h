@@ -49,8 +49,9 @@ int mlp_testing_linear_kernel(const struct mlp_linear_args *args, char *name, si
 int mlp_testing_expert_linear_kernel(const struct mlp_expert_linear_args *args, char *name, size_t cap);
 int mlp_testing_route_kernel(const struct mlp_route_args *args, char *name, size_t cap);
 
-/* The same for the calls of mlp_ops_fp8.h: of the norm "LxC" (L lanes or threads a row, C chunks of 8 each), of the products
- * "big", "mid", "small", "tile", "few" or "few wide".  The whole call is checked. */
+/* The same for the calls of mlp_ops_fp8.h: of the norm "LxC" (L lanes or threads a row, C chunks of 8 each) or "LxC twice" (its
+ * rows are read twice), of the products "big", "mid", "small", "thin", "tile", "few" or "few wide"; "none" for no rows.  The
+ * whole call is checked. */
 struct mlp_rms_norm_args;
 struct mlp_fp8_linear_args;
 struct mlp_fp8_expert_linear_args;

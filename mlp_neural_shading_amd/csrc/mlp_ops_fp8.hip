@@ -236,10 +236,11 @@ __device__ __forceinline__ void finish8(const Fp8ProductArgs &p, float (&acc)[2 
 // (16 bytes) of row r sits at slot c ^ ((r / 2) % 8), as in the 16-bit products.  A tile's multiply-adds follow the matrix
 // instructions of the next tiles, and the stage's last row of tiles is multiplied after the barrier that frees it, while the
 // next stage's first operands are read.
-// Measured: 8,192^3 440 to 457 us (2,400 to 2,500 TFLOP/s), the matrix unit busy 60 % of the cycles at a clock of 1.9 GHz:
-// its power, and the feed (370 us with no loads at all).  FULL 875 to 917 (1,200 to 1,260; a library's 16-bit product 1,589):
+// Measured: 8,192^3 440 to 467 us (2,350 to 2,500 TFLOP/s), the matrix unit busy 60 % of the cycles at a clock of 1.9 GHz:
+// its power, and the feed (370 us with no loads at all).  FULL 875 to 934 (1,180 to 1,260; a library's 16-bit product 1,589):
 // matrix and vector instructions 58 and 51 % of the cycles, the widening itself for nothing.  65,536 x 1,024 -> 1,024 into
-// 16 bits 80 to 86 us: the product, and the outputs' bytes, in all CUs at once between two tiles.
+// 16 bits 80 to 86 us (91 with other inputs each time): the product, and the outputs' bytes, in all CUs at once between two
+// tiles.
 template <class T, bool GROUPED, bool GATED, int WM, int WN, int MT, int NT, int NS, int WPE>
 __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void fp8_big(Fp8ProductArgs p)
 {
@@ -616,7 +617,7 @@ __global__ __launch_bounds__(64 * WM *WN) __attribute__((amdgpu_waves_per_eu(WPE
 // Few rows: a workgroup of up to 16 waves takes 16 * MA weight rows and up to 16 rows of x, and its waves share the
 // blocks of K: each multiplies a run of them straight from memory (16 x 16 x 128 MFMA: one block), kDepth requested at
 // once, and the waves' sums meet in LDS.  Bound by the weights' bytes and two memory latencies: 1 x 1,024 -> 1,024 3.6 us,
-// 16 x 4,096 -> 4,096 7.2 (2.3 TB/s), 7 x 2,048 -> 2 x 4,096 6.0 (2.8 TB/s).
+// 16 x 4,096 -> 4,096 7.3 (2.3 TB/s), 7 x 2,048 -> 2 x 4,096 6.0 (2.8 TB/s).
 template <class T, bool FULL, bool GROUPED, bool GATED, int MA>
 __global__ __launch_bounds__(1024) void fp8_few(Fp8ProductArgs p)
 {
@@ -749,6 +750,8 @@ __global__ __launch_bounds__(1024) void fp8_few(Fp8ProductArgs p)
 // straight into LDS), kTile 64 x 128 through registers, kFew 16 x 16, kFewWide 32 x 16, kThin 64 x 64 straight into LDS (gated,
 // by two waves that hold 32 gates and the 32 they gate: 13.5 against kSmall's 15.6 for 64 x 4,096 -> 2 x 2,048, not built).
 // kMid of 8 waves against 4: 5,003 x 1,008 -> 777 15.7 against 16.9, 65,536 x 1,024 -> 1,024 107 against 109; widened 207 against 171.
+// Gated both are as fast, 19 sizes within 4 %: 1,024 x 4,096 -> 2 x 2,048 24.8 against 24.7, 4,096 x 1,024 -> 2 x 1,024 17.8 against
+// 17.2, 900 x 4 rows over 32 experts, 2,048 -> 2 x 1,024, 51.4 against 53.3.
 enum Form { kBig, kMid, kSmall, kTile, kFew, kFewWide, kThin };
 struct Shape {
     int bm, bn, threads;
@@ -788,19 +791,20 @@ bool big_fits(bool full, bool gated_eight) { return !full || gated_eight; }
 
 // The kernel, for 256 CUs (MI355X); times in us of every kernel forced on the size:
 //   - few tiles of 16 x 16 in all: kFew, whose waves share K, and with more of them than CUs 32 weight rows at a time.
-//     16 x 4,096 -> 4,096 kFew 8.4 (kFewWide 8.8, kThin 11.3), 32 rows kFewWide 8.9 (11.5), 96 x 4,096 -> 1,024 kFewWide 8.7
-//     (kFew 11.1, kThin 10.9).  Behind the border: 64 x 4,096 -> 4,096 kThin 11.7 (kFewWide 15.6); widened 17 (16.5).  Gated and
-//     experts' layers, which have no kThin: 64 x 4,096 -> 2 x 2,048 kSmall 15.6 (15.6), 128 rows 15.6 (29);
+//     16 x 4,096 -> 4,096 kFew 7.3 (kFewWide 8.6, kThin 11.3), 32 rows kFewWide 8.6 (kFew 12.1, kThin 11.4), 96 x 4,096 -> 1,024
+//     kFewWide 8.4 (kFew 11.1, kThin 10.9).  Behind the border: 64 x 4,096 -> 4,096 kThin 11.7 (kFewWide 15.4); widened 17 (16.5).
+//     Gated and experts' layers, which have no kThin: 64 x 4,096 -> 2 x 2,048 kSmall 15.7 (kFewWide 15.4), 128 rows 15.5 (29);
 //   - at most 64 weight rows, or rows that are not 4-byte aligned: kTile, which takes them;
 //   - else the one of kBig, kMid, kSmall and kThin that takes the least time by its rounds, each of so much per 1,024 columns and so
 //     much for its start and epilogue, fitted to 65,536 x 1,024 -> 1,024 (86, 107 and 135; widened 183, 172 and 205) and
 //     8,192^3 (457, 555 and 714; 925, 917 and 1,124), kThin to 256 and 512 tiles, and where 8-bit outputs need another kernel,
 //     that kernel's launch and the bytes of the FP32 rows.  It gives kThin for 64 to 256 x 4,096 -> 4,096 (11.7; kSmall 15.6;
-//     widened 17.5, 25.4) and 512 x 7,168 -> 2,048 (18; 24), kSmall for 512 x 4,096 -> 4,096 (16.4; kThin 18, kMid 23, kBig 48),
-//     kMid for 1,024 rows (25; kSmall 27, kBig 49) and for 5,003 x 1,001 -> 777 (16.5; 19.3, 27.5) and kBig for 4,096 rows (63;
-//     76, 97).
+//     widened 17.5, 25.4) and 512 x 7,168 -> 2,048 (18; 24), kSmall for 512 x 4,096 -> 4,096 (16.3; kThin 17, kMid 23, kBig 48),
+//     kMid for 1,024 rows (25; kSmall 26, kBig 49) and for 5,003 x 1,001 -> 777 (16.4; 19.2, 27.8) and kBig for 4,096 rows (62;
+//     75, 95).
 //     The experts' last tiles count as half full, and from 64 (kMid) and 128 rows (kBig) per expert on.  32 experts, 2,048 ->
-//     2,048, by rows per expert: 32 kSmall 24 (kMid 27, kBig 38), 64 kMid 29 (39; 40), 128 kBig 42 (kMid 52, kSmall 49).
+//     2,048, by rows per expert: 32 kSmall 29 (kMid 31, kBig 41), 64 kMid 34 (kSmall 37, kBig 41), 128 kBig 43 (kSmall 50, kMid 53);
+//     summed, 1,024 -> 2,048: 32 kSmall 20 (kMid 20, kBig 27), 128 kBig 38 (40; 41), 1,024 kBig 206 (kMid 225, kSmall 247).
 Form choose_form(const Fp8ProductArgs &p, bool full, bool gated, bool grouped)
 {
     const bool even = p.ldx % 4 == 0 && p.ldw % 4 == 0 && p.w_stride % 4 == 0 && (((uintptr_t)p.x | (uintptr_t)p.w) & 3) == 0;

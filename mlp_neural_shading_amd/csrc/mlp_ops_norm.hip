@@ -3,7 +3,8 @@
 // so 16 neighbouring lanes hold a block of 128, whose largest value they find among themselves.  Measured: the norm of
 // 65,536 x 1,024 BF16 with a residual into 8 bits 90 us (472 MB, 5.2 TB/s, what a large copy reaches), without a residual 49
 // (201 MB: 72 % of the vector cycles, most of them the rounding's); 65,536 x 1,024 by rows 37 us; 32 matrices of
-// 2,048 x 2,048 by blocks 87 us (403 MB, 4.6 TB/s).
+// 2,048 x 2,048 by blocks 87 us (403 MB, 4.6 TB/s).  Small rows are bound by latencies: each chunk's load is waited for before
+// the next one's, a last chunk's elements one by one (5,003 x 1,001 of FP16 6.6 us, x 1,007 8.0).
 #include <hip/hip_runtime.h>
 
 #include "mlp_ops_device.h"
@@ -278,7 +279,7 @@ __global__ __launch_bounds__(256) void quantize_blocks(QuantizeArgs p)
 //   8,192 x 8,192    512x2 57 (110)     256x4 76 (125), 1024x1 76 (110)
 //   4,096 x 16,384   512x2 twice 59 (127)   1024x2 78 (124), 512x4 97 (144): the second reading comes from the caches
 //   4,096 x 32,768   512x2 twice 118 (260)  1024x2 twice 144 (254), 1024x4 211 (288, registers spilled)
-//   1,024 x 65,536   1024x4 twice 66 (145)  512x4 twice 68 (173)
+//   1,024 x 65,536   1024x4 twice 66 to 69 (145)  512x4 twice 68 (173)
 struct NormForm {
     int lanes, chunks;
     bool loop;
