@@ -6,7 +6,9 @@
  * MLP_FP8_BLOCK columns, of one row (activations) or of MLP_FP8_BLOCK rows (weights); blocks begin at row and
  * column 0, the last of a row or column is as short as it has to be.  The element is value * scale.
  *   scale = max(amax / 448, 2^-126),  value = round(v * (1 / scale)),  to nearest, ties to even,
- * amax over the block's finite elements; a NaN or an infinity becomes NaN by itself and leaves the others as they are.
+ * amax over the block's finite elements; a NaN or an infinity becomes NaN by itself and leaves the others as they are.  The
+ * reciprocal and the product are rounded to FP32 first: v / scale within 2^-22 of itself of the middle between two E4M3
+ * numbers may go to either.
  * Scales made elsewhere are taken as they are, of any sign; a layer multiplies those of its two operands' blocks in FP32, so a
  * block whose product is infinite gives infinities or NaN, whatever its values, and one below 2^-126 has fewer bits.
  *

@@ -159,6 +159,7 @@ def quantize(x, *, block_rows=1, gated=False) -> Quantized:
     with contiguous rows.
 
     ``block_rows`` 1: a scale for each row and 128 columns (activations); 128: for 128 rows and 128 columns (weights).
+    A value is ``v * (1 / scale)``, both rounded in FP32, to E4M3: next to the middle between two numbers it may go to either.
     ``gated``: the weights of a gated layer, whose two halves of the rows are matrices of their own."""
     if not gated and forward_ad._current_level < 0:
         r = _usual.quantize(x, block_rows)
